@@ -187,6 +187,55 @@ pa_status paged_qkv_append_qknorm(pa_shape shape, int32_t hidden, float rope_the
                                   size_t workspace_bytes, void *stream);
 
 /*
+ * paged_rope_append: the new tokens' q, k and v between any projection and the attention, in
+ * one pass: q and k heads normalised (optional) and rotated at their positions, q to q_out,
+ * k and v to their cache slots by the kv_append rule.  (paged_qkv_append does this for its own
+ * projection; here the rows come from the caller, e.g. from a projection with adapters or a
+ * quantised weight.)  In fp32, with one rounding to bf16 at the end:
+ *   q_norm_weight, k_norm_weight (both or neither): the norm of paged_qkv_append_qknorm;
+ *   rope_theta > 1: the rotation of paged_qkv_append, rope_theta = 0: none.  Pair d (dims d and
+ *   d + 64) turns by p * rope_theta^(-d/64), where
+ *     positions NULL:  p = the token's position in the cache, seq_len - q_len + i;
+ *     positions [axes][total_tokens] int32 device array: p = positions[pair_axis[d]][t], so
+ *     that the pairs of a head can turn with several axes (time, height, width of an image or
+ *     video patch).  1 <= axes <= 3; pair_axis: 64 host bytes, each < axes (NULL with one
+ *     axis).  Where a token is stored does not depend on its given positions.  A position
+ *     outside (-2^24, 2^24) gives a NaN q row, no K/V row and PA_ERR_DEVICE.
+ *   v is copied as it is.
+ *   q, k_new, v_new: bf16, token t's [32][128] / [8][128] / [8][128] at t * stride elements; a
+ *   stride is a multiple of 8, at least the row's own length, so that all three may be slices
+ *   of one projection's rows.  q_out [total_tokens][32][128] may be q itself when q's stride
+ *   is 4096; otherwise it overlaps no input.
+ * Pools, block_table, cu_q_lens, seq_lens and workspace as for kv_append, except that tokens
+ * behind the last sequence (t >= cu_q_lens[num_seqs], a padded batch) are left alone: their
+ * q_out rows keep what they held.  A token whose block id is outside the pool gets no K/V row
+ * and records PA_ERR_DEVICE; one whose sequence data are inconsistent gets no K/V row either
+ * and, where the cache position is its rotation's, a NaN q row.
+ * paged_rope_append_fp8 writes the 8-bit cache (below): a k row is quantised from its rotated
+ * fp32 values, a v row as kv_append_fp8 does.
+ */
+pa_status paged_rope_append(pa_shape shape, float rope_theta, const int32_t *positions, int32_t axes,
+                            const uint8_t *pair_axis, const void *q_norm_weight,
+                            const void *k_norm_weight, float norm_eps, void *q_out, const void *q,
+                            int64_t q_stride, const void *k_new, int64_t k_stride,
+                            const void *v_new, int64_t v_stride, void *k_pool, void *v_pool,
+                            const int32_t *block_table, int32_t max_blocks_per_seq,
+                            int32_t num_blocks, const int32_t *cu_q_lens, const int32_t *seq_lens,
+                            int32_t num_seqs, int32_t total_tokens, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+pa_status paged_rope_append_fp8(pa_shape shape, float rope_theta, const int32_t *positions, int32_t axes,
+                                const uint8_t *pair_axis, const void *q_norm_weight,
+                                const void *k_norm_weight, float norm_eps, void *q_out,
+                                const void *q, int64_t q_stride, const void *k_new,
+                                int64_t k_stride, const void *v_new, int64_t v_stride,
+                                void *k_codes, void *v_codes, float *k_scale, float *v_scale,
+                                const int32_t *block_table, int32_t max_blocks_per_seq,
+                                int32_t num_blocks, const int32_t *cu_q_lens,
+                                const int32_t *seq_lens, int32_t num_seqs, int32_t total_tokens,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * paged_attn_decode: one query token per sequence [P1 §4.4.2].
  * out[b][h] = sum_{j < seq_lens[b]} softmax_j(scale * q[b][h] . K_b[j][h/4]) V_b[j][h/4]
  * where K_b[j] is slot j % 256 of block block_table[b][j / 256].  seq_lens[b] >= 1

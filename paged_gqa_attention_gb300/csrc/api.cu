@@ -352,6 +352,89 @@ pa_status qkv_impl(pa_shape shape, int32_t hidden, float rope_theta, const void 
     return launch_qk_norm(a, sms, st) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+// Frequencies of the 64 rotated pairs, theta^(-i/64), each as a float-float pair hi + lo.  One
+// power and 63 double products (relative error below 64 * 2^-53, so under 2e-7 rad at the
+// farthest position, 2^24): 64 calls of pow cost more than the launch of a small append.
+void rope_frequencies(double theta, float *hi, float *lo) {
+    const double step = std::pow(theta, -1.0 / kRopePairs);
+    double f = 1.0;
+    for (int i = 0; i < kRopePairs; ++i, f *= step) {
+        hi[i] = (float)f;
+        lo[i] = (float)(f - (double)hi[i]);
+    }
+}
+
+// paged_rope_append over the bf16 cache, or over the 8-bit cache when eight_bit.
+pa_status rope_append_impl(pa_shape shape, float rope_theta, const int32_t *positions, int32_t axes,
+                           const uint8_t *pair_axis, const void *q_norm, const void *k_norm, float norm_eps,
+                           void *q_out, const void *q, int64_t q_stride, const void *k_new, int64_t k_stride,
+                           const void *v_new, int64_t v_stride, bool eight_bit, void *k_pool, void *v_pool,
+                           float *k_scale, float *v_scale, const int32_t *block_table, int32_t max_blocks_per_seq,
+                           int32_t num_blocks, const int32_t *cu_q_lens, const int32_t *seq_lens, int32_t num_seqs,
+                           int32_t total_tokens, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || total_tokens < 0 || max_blocks_per_seq < 1 || num_blocks < 1 ||
+        (num_seqs == 0 && total_tokens != 0) || (long long)max_blocks_per_seq * kBlock > (1ll << 30))
+        return PA_ERR_INVALID_ARG;
+    if (rope_theta != 0.f) {
+        if (!(std::isfinite(rope_theta) && rope_theta > 1.f)) return PA_ERR_INVALID_ARG;
+        // cache positions must stay exact in fp32 (given positions are checked on the device)
+        if (!positions && (long long)max_blocks_per_seq * kBlock > (1ll << 24)) return PA_ERR_INVALID_ARG;
+        if (axes < 1 || axes > kMaxRopeAxes || (axes > 1 && (!positions || !pair_axis))) return PA_ERR_INVALID_ARG;
+        for (int i = 0; pair_axis && i < kRopePairs; ++i)
+            if (pair_axis[i] >= axes) return PA_ERR_INVALID_ARG;
+    } else if (positions || pair_axis) {
+        return PA_ERR_INVALID_ARG;   // positions without a rotation
+    }
+    if ((q_norm == nullptr) != (k_norm == nullptr)) return PA_ERR_INVALID_ARG;
+    if (q_norm && (!aligned16(q_norm) || !aligned16(k_norm) || !(std::isfinite(norm_eps) && norm_eps >= 0.f)))
+        return PA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kHeaderBytes || !aligned16(workspace)) return PA_ERR_INVALID_ARG;
+    // rows at least their own length apart, on 16-byte boundaries
+    if (q_stride < kHq * kD || k_stride < kHkv * kD || v_stride < kHkv * kD || q_stride % 8 || k_stride % 8 ||
+        v_stride % 8)
+        return PA_ERR_INVALID_ARG;
+    if (total_tokens == 0) return PA_OK;
+    if (!q_out || !q || !k_new || !v_new || !k_pool || !v_pool || !block_table || !cu_q_lens || !seq_lens ||
+        (eight_bit && (!k_scale || !v_scale)))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(q_out) || !aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) ||
+        !aligned16(v_pool) || !aligned16(k_scale) || !aligned16(v_scale) || !aligned4(block_table) ||
+        !aligned4(cu_q_lens) || !aligned4(seq_lens) || !aligned4(positions))
+        return PA_ERR_INVALID_ARG;
+    if (q_out == q && q_stride != kHq * kD) return PA_ERR_INVALID_ARG;   // in place: the same rows
+    const int sms = sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
+    RopeAppendArgs a = {};
+    a.q_out = q_out;
+    a.q = q;
+    a.k_new = k_new;
+    a.v_new = v_new;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.block_table = block_table;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.cu_q_lens = cu_q_lens;
+    a.seq_lens = seq_lens;
+    a.num_seqs = num_seqs;
+    a.total_tokens = total_tokens;
+    a.err = static_cast<uint32_t *>(workspace);
+    a.rope = rope_theta != 0.f ? 1 : 0;
+    a.positions = positions;
+    a.axes = axes;
+    for (int i = 0; pair_axis && i < kRopePairs; ++i) a.pair_axis[i] = pair_axis[i];
+    if (a.rope) rope_frequencies(rope_theta, a.freq_hi, a.freq_lo);
+    a.q_norm = q_norm;
+    a.k_norm = k_norm;
+    a.norm_eps = norm_eps;
+    return launch_rope_append(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
 
 }  // namespace
 
@@ -488,6 +571,33 @@ pa_status kv_append_fp8(pa_shape shape, void *k_codes, void *v_codes, float *k_s
     a.total_tokens = total_tokens;
     a.err = static_cast<uint32_t *>(workspace);
     return launch_kv_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status paged_rope_append(pa_shape shape, float rope_theta, const int32_t *positions, int32_t axes,
+                            const uint8_t *pair_axis, const void *q_norm_weight, const void *k_norm_weight,
+                            float norm_eps, void *q_out, const void *q, int64_t q_stride, const void *k_new,
+                            int64_t k_stride, const void *v_new, int64_t v_stride, void *k_pool, void *v_pool,
+                            const int32_t *block_table, int32_t max_blocks_per_seq, int32_t num_blocks,
+                            const int32_t *cu_q_lens, const int32_t *seq_lens, int32_t num_seqs,
+                            int32_t total_tokens, void *workspace, size_t workspace_bytes, void *stream) {
+    return rope_append_impl(shape, rope_theta, positions, axes, pair_axis, q_norm_weight, k_norm_weight, norm_eps,
+                            q_out, q, q_stride, k_new, k_stride, v_new, v_stride, false, k_pool, v_pool, nullptr,
+                            nullptr, block_table, max_blocks_per_seq, num_blocks, cu_q_lens, seq_lens, num_seqs,
+                            total_tokens, workspace, workspace_bytes, stream);
+}
+
+pa_status paged_rope_append_fp8(pa_shape shape, float rope_theta, const int32_t *positions, int32_t axes,
+                                const uint8_t *pair_axis, const void *q_norm_weight, const void *k_norm_weight,
+                                float norm_eps, void *q_out, const void *q, int64_t q_stride, const void *k_new,
+                                int64_t k_stride, const void *v_new, int64_t v_stride, void *k_codes, void *v_codes,
+                                float *k_scale, float *v_scale, const int32_t *block_table,
+                                int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *cu_q_lens,
+                                const int32_t *seq_lens, int32_t num_seqs, int32_t total_tokens, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    return rope_append_impl(shape, rope_theta, positions, axes, pair_axis, q_norm_weight, k_norm_weight, norm_eps,
+                            q_out, q, q_stride, k_new, k_stride, v_new, v_stride, true, k_codes, v_codes, k_scale,
+                            v_scale, block_table, max_blocks_per_seq, num_blocks, cu_q_lens, seq_lens, num_seqs,
+                            total_tokens, workspace, workspace_bytes, stream);
 }
 
 static pa_status decode_fp8_impl(pa_shape shape, void *out, float *lse, const void *q, const void *k_new, const void *v_new,

@@ -27,6 +27,7 @@ constexpr uint32_t kErrBadBlock = 1u << 8;
 constexpr uint32_t kErrBadSeqLen = 1u << 9;
 constexpr uint32_t kErrBadCuQ = 1u << 10;
 constexpr uint32_t kErrQLen = 1u << 11;
+constexpr uint32_t kErrBadPosition = 1u << 12;
 
 // ------------------------------------------------------------------ workspace layout
 // [0, 256)                      error word and details

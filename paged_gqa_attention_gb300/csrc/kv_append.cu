@@ -24,27 +24,12 @@
 // waits for this one to finish before it reads the pools.
 #include "common.cuh"
 #include "launch.h"
+#include "tokens.cuh"
 
 namespace pa {
 namespace {
 
 constexpr int kWarps = 8;  // 4 tokens x {K, V} per CTA
-
-// Largest s in [0, n) with cu[s] <= t (cu non-decreasing, cu[0] <= t): each round the
-// 32 lanes probe 32 evenly spaced entries, narrowing the range 32-fold.
-__device__ __forceinline__ int warp_find_sequence(const int32_t *cu, int n, int t, int lane) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int idx = lo + lane * step;
-        const bool le = idx < hi && __ldg(cu + idx) <= t;
-        const unsigned m = __ballot_sync(0xffffffffu, le);
-        const int last = m ? 31 - __clz(m) : 0;
-        lo = lo + last * step;
-        hi = min(hi, lo + step);
-    }
-    return lo;
-}
 
 template <bool kFp8>
 __global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(AppendArgs a) {

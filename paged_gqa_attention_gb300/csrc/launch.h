@@ -124,7 +124,39 @@ struct QkvArgs {
     float norm_eps;
 };
 
+// Norm and rotation of the new tokens' q and k with the append of k and v (rope_append.cu).
+constexpr int kMaxRopeAxes = 3;
+struct RopeAppendArgs {
+    void *q_out;            // [total_tokens][32][128] bf16
+    const void *q;          // rows of 32 / 8 / 8 heads x 128 bf16, `stride` elements apart
+    const void *k_new;
+    const void *v_new;
+    int64_t q_stride, k_stride, v_stride;
+    void *k_pool;           // bf16 pools, or the 8-bit code pools when k_scale is set
+    void *v_pool;
+    float *k_scale;
+    float *v_scale;
+    const int32_t *block_table;
+    int32_t max_blocks_per_seq;
+    int32_t num_blocks;
+    const int32_t *cu_q_lens;
+    const int32_t *seq_lens;
+    int32_t num_seqs;
+    int32_t total_tokens;
+    uint32_t *err;
+    int32_t rope;           // 0: no rotation
+    const int32_t *positions;   // [axes][total_tokens], or null: the position in the cache
+    int32_t axes;
+    uint8_t pair_axis[kRopePairs];
+    float freq_hi[kRopePairs];  // frequency of pair i: hi + lo = theta^(-i/64)
+    float freq_lo[kRopePairs];
+    const void *q_norm;     // bf16 gains [128] of the q and the k heads, or null: no norm
+    const void *k_norm;
+    float norm_eps;
+};
+
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream);
+cudaError_t launch_rope_append(const RopeAppendArgs &a, int num_sms, cudaStream_t stream);
 
 // x_map: x [total_tokens][hidden] bf16, box {64, qkv_tile_rows_loaded(total_tokens)}; w_map:
 // w [6144][hidden] bf16, box {64, qkv_weight_box_rows()}; both 128-byte swizzle.

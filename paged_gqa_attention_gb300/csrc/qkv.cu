@@ -44,6 +44,7 @@
 // Every wait is bounded; on expiry the CTA records PA_ERR_TIMEOUT and unwinds.
 #include "common.cuh"
 #include "launch.h"
+#include "tokens.cuh"
 
 namespace pa {
 namespace {
@@ -66,13 +67,6 @@ constexpr int kRunCols = 32;                   // weight rows per TMA box: one r
 __host__ __device__ __forceinline__ int run_row(int r) {
     return (r >> 2) * kD + (r & 1) * (kD / 2) + ((r >> 1) & 1) * kRunCols;
 }
-
-// 2 pi in three fp32 parts (hi + mid + lo, each the rounding of what remains) and 1 / (2 pi)
-constexpr double kTwoPiD = 6.28318530717958647692528676655900577;
-constexpr float kTwoPiHi = (float)kTwoPiD;
-constexpr float kTwoPiMid = (float)(kTwoPiD - (double)kTwoPiHi);
-constexpr float kTwoPiLo = (float)(kTwoPiD - (double)kTwoPiHi - (double)kTwoPiMid);
-constexpr float kInvTwoPi = (float)(1.0 / kTwoPiD);
 
 // BN output columns per tile, BMA rows of x loaded per stage (128, or 32 for <= 32 tokens).
 // A stage covers kSub adjacent sub-tiles of 64 hidden elements: with few tokens the weights
@@ -197,20 +191,6 @@ __device__ __forceinline__ long long token_slot(const QkvArgs &a, int t, int *po
         return -1;
     }
     return ((long long)blk * kBlock + p % kBlock) * kHkv * kD;
-}
-
-// cos and sin of the rotation angle at position pf (an integer below 2^24, exact in fp32) for
-// the frequency fh + fl (pair i's: rope_cos_sin).  p * freq is formed as hi + lo (the product's rounding error recovered with an fma),
-// the multiple of 2 pi nearest hi is taken off in three parts (Cody and Waite), lo is added
-// back, and the reduced angle (|r| < 4) goes to the fast sine/cosine.
-__device__ __forceinline__ void angle_cos_sin(float pf, float fh, float fl, float &c, float &s) {
-    const float ah = __fmul_rn(pf, fh);
-    const float al = fmaf(pf, fl, fmaf(pf, fh, -ah));
-    const float k = rintf(__fmul_rn(ah, kInvTwoPi));
-    float r = fmaf(-k, kTwoPiHi, ah);
-    r = fmaf(-k, kTwoPiMid, r);
-    r = fmaf(-k, kTwoPiLo, r);
-    __sincosf(__fadd_rn(r, al), &s, &c);
 }
 
 __device__ __forceinline__ void rope_cos_sin(const QkvArgs &a, int i, float pf, float &c, float &s) {

@@ -7,6 +7,7 @@ if the library is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -78,6 +79,12 @@ def load() -> ctypes.CDLL:
     lib.paged_qkv_append_qknorm.argtypes = [pa_shape, i32, ctypes.c_float, vp, vp, ctypes.c_float, vp, vp, vp, vp, vp,
                                             vp, i32, i32, vp, vp, i32, i32, vp, sz, vp]
     lib.paged_qkv_append_qknorm.restype = ctypes.c_int
+    i64 = ctypes.c_int64
+    rope = [pa_shape, f32, vp, i32, vp, vp, vp, f32, vp, vp, i64, vp, i64, vp, i64]
+    lib.paged_rope_append.argtypes = rope + [vp, vp, vp, i32, i32, vp, vp, i32, i32, vp, sz, vp]
+    lib.paged_rope_append.restype = ctypes.c_int
+    lib.paged_rope_append_fp8.argtypes = rope + [vp, vp, vp, vp, vp, i32, i32, vp, vp, i32, i32, vp, sz, vp]
+    lib.paged_rope_append_fp8.restype = ctypes.c_int
     lib.paged_attn_decode.argtypes = [pa_shape, vp, vp, vp, vp, vp, vp, i32, i32, vp, i32, f32, vp,
                                       sz, vp]
     lib.paged_attn_decode.restype = ctypes.c_int
@@ -137,6 +144,11 @@ def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
+
+
+def _on(dev):
+    """Make dev current for a call (a launch goes to the current device), if it is not already."""
+    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
 def _ptr(t) -> int | None:
@@ -259,6 +271,124 @@ def paged_qkv_append(x, w_qkv, k_pool, v_pool, block_table, cu_q_lens, seq_lens,
                                         workspace.data_ptr(), workspace.numel(), _stream(stream))
     _check("paged_qkv_append_qknorm", st)
     return q_out
+
+
+ROPE_PAIRS = HEAD_DIM // 2
+
+
+def rope_pair_axes(sections, interleaved: bool = False) -> bytes:
+    """Axis of each of the 64 rotated pairs, for paged_rope_append: `sections` gives how many
+    pairs turn with each axis (time, height, width; one to three that sum to 64).  In order, axis
+    by axis, or, `interleaved`, alternating: pair i turns with axis i % 3 as long as that axis of
+    the last two has pairs left (i < 3 * its section), with the first otherwise."""
+    sections = [int(n) for n in sections]
+    if not 1 <= len(sections) <= 3 or min(sections) < 0 or sum(sections) != ROPE_PAIRS:
+        raise ValueError(f"sections must be one to three counts that sum to {ROPE_PAIRS}, got {sections}")
+    if not interleaved:
+        return bytes(a for a, n in enumerate(sections) for _ in range(n))
+    if len(sections) != 3:
+        raise ValueError("interleaved sections are three")
+    axes = bytes(i % 3 if i % 3 and i < 3 * sections[i % 3] else 0 for i in range(ROPE_PAIRS))
+    if [axes.count(a) for a in range(3)] != sections:
+        raise ValueError(f"sections {sections} cannot be interleaved over {ROPE_PAIRS} pairs")
+    return axes
+
+
+def _need_rows(t, name: str, heads: int, tokens, dev) -> int:
+    """The token stride (elements) of a [tokens, heads, 128] bf16 tensor whose rows are whole."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != HEAD_DIM or (tokens is not None and t.shape[0] != tokens):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({tokens if tokens is not None else 'T'}, "
+                         f"{heads}, {HEAD_DIM})")
+    row = heads * HEAD_DIM
+    if t.shape[0] == 0:
+        return row
+    stride, head, dim = t.stride()
+    if t.shape[0] == 1:
+        stride = row
+    if dim != 1 or head != HEAD_DIM or stride < row or stride % 8:
+        raise ValueError(f"{name}: each token's [{heads}, {HEAD_DIM}] must be contiguous and tokens a multiple of "
+                         f"8 elements apart, got strides {t.stride()}")
+    return stride
+
+
+def _rope_append(fp8, q, k_new, v_new, cache, block_table, cu_q_lens, seq_lens, workspace, rope_theta, positions,
+                 pair_axis, q_norm_weight, k_norm_weight, norm_eps, q_out, stream):
+    dev = q.device
+    q_stride = _need_rows(q, "q", NUM_Q_HEADS, None, dev)
+    tokens = q.shape[0]
+    k_stride = _need_rows(k_new, "k_new", NUM_KV_HEADS, tokens, dev)
+    v_stride = _need_rows(v_new, "v_new", NUM_KV_HEADS, tokens, dev)
+    if fp8:
+        _need_fp8_cache(*cache, dev)
+    else:
+        _need(cache[0], "k_pool", torch.bfloat16, (None, BLOCK_SIZE, NUM_KV_HEADS, HEAD_DIM), dev)
+        _need(cache[1], "v_pool", torch.bfloat16, tuple(cache[0].shape), dev)
+    _need(block_table, "block_table", torch.int32, (None, None), dev)
+    num_seqs = block_table.shape[0]
+    _need(cu_q_lens, "cu_q_lens", torch.int32, (num_seqs + 1,), dev)
+    _need(seq_lens, "seq_lens", torch.int32, (num_seqs,), dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    axes = 1
+    if positions is not None:
+        if positions.dim() == 1:
+            _need(positions, "positions", torch.int32, (tokens,), dev)
+        else:
+            axes = positions.shape[0]
+            _need(positions, "positions", torch.int32, (axes, tokens), dev)
+    if pair_axis is not None:
+        pair_axis = bytes(pair_axis)
+        if len(pair_axis) != ROPE_PAIRS:
+            raise ValueError(f"pair_axis must name {ROPE_PAIRS} axes")
+    if (q_norm_weight is None) != (k_norm_weight is None):
+        raise ValueError("QK-norm takes both q_norm_weight and k_norm_weight")
+    if q_norm_weight is not None:
+        _need(q_norm_weight, "q_norm_weight", torch.bfloat16, (HEAD_DIM,), dev)
+        _need(k_norm_weight, "k_norm_weight", torch.bfloat16, (HEAD_DIM,), dev)
+    if q_out is None:
+        q_out = torch.empty((tokens, NUM_Q_HEADS, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+    else:
+        _need(q_out, "q_out", torch.bfloat16, (tokens, NUM_Q_HEADS, HEAD_DIM), dev)
+    lib = load()
+    fn = lib.paged_rope_append_fp8 if fp8 else lib.paged_rope_append
+    with _on(dev):
+        st = fn(SHAPE, rope_theta, _ptr(positions), axes, pair_axis, _ptr(q_norm_weight), _ptr(k_norm_weight),
+                norm_eps, q_out.data_ptr(), q.data_ptr(), q_stride, k_new.data_ptr(), k_stride, v_new.data_ptr(),
+                v_stride, *[t.data_ptr() for t in cache], block_table.data_ptr(), block_table.shape[1],
+                cache[0].shape[0], cu_q_lens.data_ptr(), seq_lens.data_ptr(), num_seqs, tokens,
+                workspace.data_ptr(), workspace.numel(), _stream(stream))
+    _check("paged_rope_append_fp8" if fp8 else "paged_rope_append", st)
+    return q_out
+
+
+def paged_rope_append(q, k_new, v_new, k_pool, v_pool, block_table, cu_q_lens, seq_lens, workspace, *,
+                      rope_theta: float, positions=None, pair_axis=None, q_norm_weight=None, k_norm_weight=None,
+                      norm_eps: float = QWEN3_NORM_EPS, q_out=None, stream=None) -> torch.Tensor:
+    """The new tokens' q [T, 32, 128], k and v [T, 8, 128] from any projection: q and k heads
+    normalised (q_norm_weight / k_norm_weight, bf16 [128], both or neither) and rotated
+    (rope_theta > 1; 0: no rotation), k and v written into the pools at each sequence's tail
+    positions, in one pass; returns q.  The operands may be slices of one [T, 6144] projection.
+    positions (int32 [T] or [axes, T]) replace the cache positions in the rotation; with several
+    axes, pair_axis (rope_pair_axes) names the axis of each of the 64 pairs.  q_out may be q
+    itself.  Tokens behind the last sequence are left alone."""
+    return _rope_append(False, q, k_new, v_new, (k_pool, v_pool), block_table, cu_q_lens, seq_lens, workspace,
+                        rope_theta, positions, pair_axis, q_norm_weight, k_norm_weight, norm_eps, q_out, stream)
+
+
+def paged_rope_append_fp8(q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, block_table, cu_q_lens, seq_lens,
+                          workspace, *, rope_theta: float, positions=None, pair_axis=None, q_norm_weight=None,
+                          k_norm_weight=None, norm_eps: float = QWEN3_NORM_EPS, q_out=None,
+                          stream=None) -> torch.Tensor:
+    """paged_rope_append into the 8-bit cache (fp8_cache): k rows quantised from their rotated
+    fp32 values, v rows as kv_append_fp8 does."""
+    return _rope_append(True, q, k_new, v_new, (k_codes, v_codes, k_scale, v_scale), block_table, cu_q_lens,
+                        seq_lens, workspace, rope_theta, positions, pair_axis, q_norm_weight, k_norm_weight,
+                        norm_eps, q_out, stream)
 
 
 def paged_attn_decode(q, k_pool, v_pool, block_table, seq_lens, workspace, *,

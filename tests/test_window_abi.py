@@ -1,0 +1,123 @@
+"""What the rotated append refuses on the host, before any CUDA work (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+import definitions
+from paged_gqa_attention_gb300 import build as pa_build
+from paged_gqa_attention_gb300 import ops
+
+
+@pytest.fixture(scope="module")
+def lib():
+    pa_build.build()
+    return ops.load()
+
+
+class Addresses:
+    """16-byte aligned host addresses: no call below may get past validation."""
+
+    def __init__(self):
+        self.buf = (ctypes.c_uint8 * 16384)()
+        self.base = (ctypes.addressof(self.buf) + 255) // 256 * 256
+
+    def __call__(self, i, off=0):
+        return ctypes.c_void_p(self.base + 256 * i + off)
+
+
+def rope_args(p, **kw):
+    a = dict(shape=ops.SHAPE, theta=1e6, positions=None, axes=1, pair_axis=None, gq=None, gk=None, eps=1e-6, q_out=p(0),
+             q=p(1), qs=4096, k=p(2), ks=1024, v=p(3), vs=1024, kp=p(4), vp=p(5), bt=p(6), w=1, nb=1, cu=p(7), sl=p(8),
+             seqs=1, tokens=1, ws=p(9), ws_bytes=1024, stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    return list(a.values())
+
+
+REFUSED = [
+    (dict(shape=ops.pa_shape(32, 8, 64, 256)), 2),
+    (dict(theta=1.0), 1), (dict(theta=-2.0), 1), (dict(theta=float("inf")), 1), (dict(theta=float("nan")), 1),
+    (dict(axes=0), 1), (dict(axes=4), 1), (dict(axes=2), 1), (dict(axes=3, pair_axis=bytes(64)), 1),
+    (dict(pair_axis=bytes([1] + [0] * 63)), 1), (dict(theta=0.0, pair_axis=bytes(64)), 1),
+    (dict(w=(1 << 16) + 1), 1),                               # positions past 2^24
+    (dict(w=1 << 23, theta=0.0), 1),
+    (dict(eps=-1.0, gq=1, gk=1), 1), (dict(eps=float("nan"), gq=1, gk=1), 1),
+    (dict(gq=1), 1), (dict(gk=1), 1),
+    (dict(qs=4095), 1), (dict(qs=4088), 1), (dict(ks=1020), 1), (dict(vs=1028), 1), (dict(ks=0), 1), (dict(vs=-1024), 1),
+    (dict(seqs=-1), 1), (dict(tokens=-1), 1), (dict(seqs=0), 1), (dict(w=0), 1), (dict(nb=0), 1),
+    (dict(ws=None), 1), (dict(ws_bytes=255), 1),
+    *[({n: None}, 1) for n in ("q_out", "q", "k", "v", "kp", "vp", "bt", "cu", "sl")],
+    *[({n: 8}, 1) for n in ("q_out", "q", "k", "v", "kp", "vp", "ws")],
+    *[({n: 2}, 1) for n in ("bt", "cu", "sl")],
+]
+
+
+@pytest.mark.parametrize("change,status", REFUSED, ids=[str(c[0])[:40] for c in REFUSED])
+def test_rope_append_refuses(lib, change, status):
+    p = Addresses()
+    names = ("q_out", "q", "k", "v", "kp", "vp", "ws", "bt", "cu", "sl")
+    kw = {}
+    for n, x in change.items():
+        if n in names and x is not None:
+            x = p(20, x)                                      # misaligned by that many bytes
+        if n in ("gq", "gk") and x is not None:
+            x = p(21)
+        kw[n] = x
+    assert lib.paged_rope_append(*rope_args(p, **kw)) == status
+    args = rope_args(p, **kw)
+    assert lib.paged_rope_append_fp8(*args[:17], p(22), p(23), *args[17:]) == status
+
+
+def test_rope_append_refuses_in_place_over_strided_rows(lib):
+    p = Addresses()
+    assert lib.paged_rope_append(*rope_args(p, q=p(0), qs=6144)) == 1
+    args = rope_args(p)
+    assert lib.paged_rope_append_fp8(*args[:17], None, p(23), *args[17:]) == 1
+    assert lib.paged_rope_append_fp8(*args[:17], p(22), p(23, 8), *args[17:]) == 1
+
+
+def test_rope_append_of_no_tokens_is_done(lib):
+    p = Addresses()
+    assert lib.paged_rope_append(*rope_args(p, tokens=0, seqs=0, q=None, k=None)) == 0
+
+
+def test_rope_pair_axes():
+    assert ops.rope_pair_axes((16, 24, 24)) == bytes([0] * 16 + [1] * 24 + [2] * 24)
+    assert ops.rope_pair_axes((64,)) == bytes(64)
+    x = ops.rope_pair_axes((24, 20, 20), interleaved=True)
+    assert x[:60] == bytes([0, 1, 2] * 20) and x[60:] == bytes(4)
+    for bad in ((64, 1), (), (10, 10, 10), (16, 16, 16, 16), (-1, 65)):
+        with pytest.raises(ValueError):
+            ops.rope_pair_axes(bad)
+    for bad in ((32, 32), (4, 30, 30), (64,)):
+        with pytest.raises(ValueError):
+            ops.rope_pair_axes(bad, interleaved=True)
+
+
+def test_the_binding_refuses_wrong_rows():
+    t = torch.zeros(2, 32, 128, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        ops._need_rows(t.float(), "q", 32, None, t.device)
+    with pytest.raises(ValueError):
+        ops._need_rows(t, "q", 32, None, t.device)            # not a CUDA tensor
+
+
+def test_the_rotation_written_out_keeps_lengths_and_relative_positions():
+    """The definition the GPU tests compare with: a rotation keeps each pair's length, and a
+    product of two rotated heads depends on the distance of their positions alone."""
+    g = torch.Generator().manual_seed(1)
+    x, y = torch.randn(2, 5, 2, 128, generator=g, dtype=torch.float64)
+    p = torch.tensor([0, 3, 17, 400, 100000])
+    a, size = definitions.rotated(x, p, 1e6)
+    assert torch.allclose(a.square().sum(-1), x.square().sum(-1)) and torch.equal(a[0], x[0])
+    b, _ = definitions.rotated(y, p + 9, 1e6)
+    a2, _ = definitions.rotated(x, p + 1000, 1e6)
+    b2, _ = definitions.rotated(y, p + 1009, 1e6)
+    assert torch.allclose((a * b).sum(-1), (a2 * b2).sum(-1))
+    n, _ = definitions.rotated(x, p, 0.0, gain=torch.ones(128), eps=0.0)
+    assert torch.allclose(n.square().mean(-1), torch.ones(5, 2, dtype=torch.float64))
+    three = torch.stack([p, p + 5, p + 7])
+    c, _ = definitions.rotated(x, three, 1e6, [0] * 16 + [1] * 24 + [2] * 24)
+    d, _ = definitions.rotated(x, p + 5, 1e6)
+    assert torch.equal(c[..., 16:40], d[..., 16:40]) and not torch.allclose(c[..., 40:64], d[..., 40:64])

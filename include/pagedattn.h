@@ -319,6 +319,39 @@ pa_status paged_attn_decode_fp8_split(pa_shape shape, void *out, float *lse, con
                                       size_t workspace_bytes, void *stream);
 
 /*
+ * Attention over a sliding window with visible first tokens (sinks).  The query at position p
+ * sees the keys j <= p with j < sinks or j > p - window: the first `sinks` tokens of its
+ * sequence and the last `window` ones, its own included (window >= 1, sinks >= 0, else
+ * PA_ERR_INVALID_ARG; a window as long as the context is full attention).
+ * A server may give back the blocks that no query sees any more: table entries of blocks without a
+ * visible token are not used (-1 will do), and slots of the other blocks that no query of the
+ * call sees may hold anything, NaN included.
+ *
+ * paged_attn_decode_window, paged_attn_decode_window_fp8: paged_attn_decode and
+ * paged_attn_decode_fp8 with a window, p = seq_lens[b] - 1.  Append first
+ * (paged_rope_append, kv_append).  seq_lens[b] = 0 is a padded row of the batch: its output
+ * is zeros, its lse -infinity.  split_tokens: visible tokens one CTA handles (a positive
+ * multiple of 64, of 128 over the 8-bit cache), 0 = the library's choice; results depend on it
+ * only by rounding.  The workspace of pa_workspace_bytes() suits the library's choice.
+ */
+pa_status paged_attn_decode_window(pa_shape shape, void *out, float *lse, const void *q,
+                                   const void *k_pool, const void *v_pool,
+                                   const int32_t *block_table, int32_t max_blocks_per_seq,
+                                   int32_t num_blocks, const int32_t *seq_lens, int32_t batch,
+                                   int32_t window, int32_t sinks, float scale,
+                                   int32_t split_tokens, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+pa_status paged_attn_decode_window_fp8(pa_shape shape, void *out, float *lse, const void *q,
+                                       const void *k_codes, const void *v_codes,
+                                       const float *k_scale, const float *v_scale,
+                                       const int32_t *block_table, int32_t max_blocks_per_seq,
+                                       int32_t num_blocks, const int32_t *seq_lens, int32_t batch,
+                                       int32_t window, int32_t sinks, float scale,
+                                       int32_t split_tokens, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+
+/*
  * paged_attn_decode_append: kv_append of one new token per sequence followed by
  * paged_attn_decode, in one kernel [P1 §4.3.1 append, §4.4.2 decode; P3 §4.2 "append,
  * then attend"].  Row b of k_new / v_new ([batch][8][128] bf16) is written to position
@@ -469,6 +502,22 @@ pa_status paged_attn_prefill(pa_shape shape, void *out, float *lse, const void *
                              const int32_t *seq_lens, int32_t num_seqs, int32_t total_tokens,
                              int32_t max_q_len, float scale, void *workspace,
                              size_t workspace_bytes, void *stream);
+
+/*
+ * paged_attn_prefill_window: paged_attn_prefill with a sliding window and sinks (the rule above,
+ * p each new token's position).  Arguments, workspace and errors as for paged_attn_prefill; the
+ * table entries of blocks that none of a sequence's new tokens sees are not used.  A NaN or
+ * infinity in a V row that some of the 64 positions of a work unit see and others do not may
+ * reach the outputs of all 64.
+ */
+pa_status paged_attn_prefill_window(pa_shape shape, void *out, float *lse, const void *q,
+                                    const void *k_pool, const void *v_pool,
+                                    const int32_t *block_table, int32_t max_blocks_per_seq,
+                                    int32_t num_blocks, const int32_t *cu_q_lens,
+                                    const int32_t *seq_lens, int32_t num_seqs,
+                                    int32_t total_tokens, int32_t max_q_len, int32_t window,
+                                    int32_t sinks, float scale, void *workspace,
+                                    size_t workspace_bytes, void *stream);
 
 /*
  * paged_attn_prefill_append: kv_append of each sequence's new tokens followed by

@@ -149,6 +149,22 @@ int auto_split_tokens(int batch, int max_blocks_per_seq, int num_sms) {
     return (int)split;
 }
 
+// Tiles of `tile` tokens that can hold a visible one under a sliding window: those of the
+// sinks and of a window that starts at any token, at most the whole table's.
+long long window_tiles_bound(int window, int sinks, int max_blocks_per_seq, int tile) {
+    const long long all = (long long)max_blocks_per_seq * (kBlock / tile);
+    const long long n = ((long long)sinks + tile - 1) / tile + ((long long)window + tile - 2) / tile + 1;
+    return n < all ? n : all;
+}
+
+// Tiles per split of a windowed decode, whose sequences hold up to `tiles` each.
+int auto_window_split(int batch, long long tiles, int num_sms) {
+    const long long pairs = (long long)batch * kHkv;
+    long long n = (2LL * num_sms + pairs - 1) / pairs;   // splits of a pair: one wave of CTAs
+    if (n > tiles) n = tiles;
+    return (int)((tiles + n - 1) / n);
+}
+
 size_t partial_entries_bound(int max_batch, int max_blocks_per_seq) {
     // auto split: pairs * ceil(target / pairs) <= target + pairs; never more than one
     // entry per 64-token tile of the widest context either.
@@ -196,11 +212,19 @@ struct CascadeExtras {
     int32_t shared_blocks;
 };
 
+// A sliding window with visible first tokens.
+struct Window {
+    int32_t window;
+    int32_t sinks;
+};
+
+bool window_ok(int32_t window, int32_t sinks) { return window >= 1 && sinks >= 0; }
+
 pa_status decode_impl(pa_shape shape, void *out, float *lse, const void *q, const void *k_new,
                       const void *v_new, const void *k_pool, const void *v_pool, const int32_t *block_table,
                       int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *seq_lens, int32_t batch,
                       float scale, int32_t split_tokens, void *workspace, size_t workspace_bytes, void *stream,
-                      const CascadeExtras *cx = nullptr) {
+                      const CascadeExtras *cx = nullptr, const Window *win = nullptr) {
     if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
     if (batch < 0 || batch > kMaxBatch || max_blocks_per_seq < 1 || num_blocks < 1 || !std::isfinite(scale) ||
         split_tokens < 0 || split_tokens % kDecodeTileTokens != 0)
@@ -218,8 +242,12 @@ pa_status decode_impl(pa_shape shape, void *out, float *lse, const void *q, cons
     if (sms <= 0) return PA_ERR_CUDA;
     if (!get_encoder()) return PA_ERR_CUDA;
     const int skip_blocks = cx ? cx->kv_begin / kBlock : 0;   // a cascade splits only the suffix
-    const int split = split_tokens ? split_tokens : auto_split_tokens(batch, max_blocks_per_seq - skip_blocks, sms);
-    const long long max_tokens = (long long)(max_blocks_per_seq - skip_blocks) * kBlock;
+    const long long max_tokens =
+        win ? kDecodeTileTokens * window_tiles_bound(win->window, win->sinks, max_blocks_per_seq, kDecodeTileTokens)
+            : (long long)(max_blocks_per_seq - skip_blocks) * kBlock;
+    const int split = split_tokens ? split_tokens
+                      : win ? kDecodeTileTokens * auto_window_split(batch, max_tokens / kDecodeTileTokens, sms)
+                            : auto_split_tokens(batch, max_blocks_per_seq - skip_blocks, sms);
     const long long nsplit = (max_tokens + split - 1) / split;
     if (nsplit > 65535) return PA_ERR_INVALID_ARG;
     const size_t entries = (size_t)batch * kHkv * (size_t)nsplit;
@@ -261,6 +289,16 @@ pa_status decode_impl(pa_shape shape, void *out, float *lse, const void *q, cons
     // A grid that fits in one wave (two CTAs per SM) with at most 8 splits a pair: the splits
     // of a pair merge as a cluster, through its shared memory.
     a.cluster_merge = nsplit > 1 && nsplit <= 8 && (long long)batch * kHkv * nsplit <= 2LL * sms ? 1 : 0;
+    if (win) {
+        a.window = win->window;
+        a.sinks = win->sinks;
+        CUtensorMap k16_map, v16_map;
+        if (!encode_pool_map(&k16_map, k_pool, num_blocks, 16) || !encode_pool_map(&v16_map, v_pool, num_blocks, 16))
+            return PA_ERR_INVALID_ARG;
+        return launch_decode_window(a, k_map, v_map, k16_map, v16_map, static_cast<cudaStream_t>(stream)) == cudaSuccess
+                   ? PA_OK
+                   : PA_ERR_CUDA;
+    }
     return launch_decode(a, k_map, v_map, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
                                                                                                  : PA_ERR_CUDA;
 }
@@ -604,7 +642,7 @@ static pa_status decode_fp8_impl(pa_shape shape, void *out, float *lse, const vo
                           const void *k_codes, const void *v_codes, const float *k_scale, const float *v_scale,
                           const int32_t *block_table, int32_t max_blocks_per_seq, int32_t num_blocks,
                           const int32_t *seq_lens, int32_t batch, float scale, int32_t split_tokens,
-                          void *workspace, size_t workspace_bytes, void *stream) {
+                          void *workspace, size_t workspace_bytes, void *stream, const Window *win = nullptr) {
     if ((k_new == nullptr) != (v_new == nullptr) || (k_new && (!aligned16(k_new) || !aligned16(v_new))))
         return PA_ERR_INVALID_ARG;
     if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
@@ -622,11 +660,15 @@ static pa_status decode_fp8_impl(pa_shape shape, void *out, float *lse, const vo
     const int sms = sm_count();
     if (sms <= 0) return PA_ERR_CUDA;
     if (!get_encoder()) return PA_ERR_CUDA;
+    const long long max_tokens =
+        win ? kDecodeFp8TileTokens *
+                  window_tiles_bound(win->window, win->sinks, max_blocks_per_seq, kDecodeFp8TileTokens)
+            : (long long)max_blocks_per_seq * kBlock;
     // the library's split rounded up to whole 128-token stages
     const int split = split_tokens ? split_tokens
-                                   : (auto_split_tokens(batch, max_blocks_per_seq, sms) + kDecodeFp8TileTokens - 1) /
-                                         kDecodeFp8TileTokens * kDecodeFp8TileTokens;
-    const long long max_tokens = (long long)max_blocks_per_seq * kBlock;
+                      : win ? kDecodeFp8TileTokens * auto_window_split(batch, max_tokens / kDecodeFp8TileTokens, sms)
+                            : (auto_split_tokens(batch, max_blocks_per_seq, sms) + kDecodeFp8TileTokens - 1) /
+                                  kDecodeFp8TileTokens * kDecodeFp8TileTokens;
     const long long nsplit = (max_tokens + split - 1) / split;
     if (nsplit > 65535) return PA_ERR_INVALID_ARG;
     const size_t entries = (size_t)batch * kHkv * (size_t)nsplit;
@@ -663,6 +705,17 @@ static pa_status decode_fp8_impl(pa_shape shape, void *out, float *lse, const vo
     a.part_o = reinterpret_cast<float *>(ws + kPartialOffset);
     a.part_ml = reinterpret_cast<float *>(ws + kPartialOffset + entries * kPartialOBytes);
     a.err = reinterpret_cast<uint32_t *>(ws);
+    if (win) {
+        a.window = win->window;
+        a.sinks = win->sinks;
+        CUtensorMap k16_map, v16_map;
+        if (!encode_code_map(&k16_map, k_codes, num_blocks, 16) || !encode_code_map(&v16_map, v_codes, num_blocks, 16))
+            return PA_ERR_INVALID_ARG;
+        return launch_decode_window_fp8(a, k_map, v_map, k16_map, v16_map, static_cast<cudaStream_t>(stream)) ==
+                       cudaSuccess
+                   ? PA_OK
+                   : PA_ERR_CUDA;
+    }
     return launch_decode_fp8(a, k_map, v_map, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
                                                                                              : PA_ERR_CUDA;
 }
@@ -712,6 +765,33 @@ pa_status paged_attn_decode_split(pa_shape shape, void *out, float *lse, const v
                                   int32_t split_tokens, void *workspace, size_t workspace_bytes, void *stream) {
     return decode_impl(shape, out, lse, q, nullptr, nullptr, k_pool, v_pool, block_table, max_blocks_per_seq,
                        num_blocks, seq_lens, batch, scale, split_tokens, workspace, workspace_bytes, stream);
+}
+
+pa_status paged_attn_decode_window(pa_shape shape, void *out, float *lse, const void *q, const void *k_pool,
+                                   const void *v_pool, const int32_t *block_table, int32_t max_blocks_per_seq,
+                                   int32_t num_blocks, const int32_t *seq_lens, int32_t batch, int32_t window,
+                                   int32_t sinks, float scale, int32_t split_tokens, void *workspace,
+                                   size_t workspace_bytes, void *stream) {
+    if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
+    if (!window_ok(window, sinks)) return PA_ERR_INVALID_ARG;
+    const Window win = {window, sinks};
+    return decode_impl(shape, out, lse, q, nullptr, nullptr, k_pool, v_pool, block_table, max_blocks_per_seq,
+                       num_blocks, seq_lens, batch, scale, split_tokens, workspace, workspace_bytes, stream, nullptr,
+                       &win);
+}
+
+pa_status paged_attn_decode_window_fp8(pa_shape shape, void *out, float *lse, const void *q, const void *k_codes,
+                                       const void *v_codes, const float *k_scale, const float *v_scale,
+                                       const int32_t *block_table, int32_t max_blocks_per_seq, int32_t num_blocks,
+                                       const int32_t *seq_lens, int32_t batch, int32_t window, int32_t sinks,
+                                       float scale, int32_t split_tokens, void *workspace, size_t workspace_bytes,
+                                       void *stream) {
+    if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
+    if (!window_ok(window, sinks)) return PA_ERR_INVALID_ARG;
+    const Window win = {window, sinks};
+    return decode_fp8_impl(shape, out, lse, q, nullptr, nullptr, k_codes, v_codes, k_scale, v_scale, block_table,
+                           max_blocks_per_seq, num_blocks, seq_lens, batch, scale, split_tokens, workspace,
+                           workspace_bytes, stream, &win);
 }
 
 pa_status paged_attn_decode_append(pa_shape shape, void *out, float *lse, const void *q, const void *k_new,
@@ -862,7 +942,8 @@ static pa_status prefill_impl(pa_shape shape, void *out, float *lse, const void 
                               const void *v_new, const void *k_pool, const void *v_pool, const int32_t *block_table,
                               int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *cu_q_lens,
                               const int32_t *seq_lens, int32_t num_seqs, int32_t total_tokens, int32_t max_q_len,
-                              float scale, void *workspace, size_t workspace_bytes, void *stream) {
+                              float scale, void *workspace, size_t workspace_bytes, void *stream,
+                              const Window *win = nullptr) {
     if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
     if (num_seqs < 0 || total_tokens < 0 || max_q_len < 0 || max_blocks_per_seq < 1 || num_blocks < 1 ||
         !std::isfinite(scale) || (num_seqs == 0 && total_tokens != 0) || max_q_len > total_tokens ||
@@ -911,12 +992,15 @@ static pa_status prefill_impl(pa_shape shape, void *out, float *lse, const void 
     // Several sequences: the units are sorted by work first, into the workspace's partial
     // area (decode scratch, unused by the prefill) when it is large enough.
     a.order = nullptr;
+    a.window = win ? win->window : 0;
+    a.sinks = win ? win->sinks : 0;
     const long long plan_units = prefill_plan_units(a);
     if (plan_units > 0 && workspace_bytes >= kPartialOffset + (size_t)plan_units * sizeof(int32_t))
         a.order = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + kPartialOffset);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = k_new ? launch_prefill_append(a, q_map, k_map, v_map, kn_map, vn_map, sms, st)
-                                : launch_prefill(a, q_map, k_map, v_map, sms, st);
+    const cudaError_t e = win     ? launch_prefill_window(a, q_map, k_map, v_map, sms, st)
+                          : k_new ? launch_prefill_append(a, q_map, k_map, v_map, kn_map, vn_map, sms, st)
+                                  : launch_prefill(a, q_map, k_map, v_map, sms, st);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
@@ -928,6 +1012,20 @@ pa_status paged_attn_prefill(pa_shape shape, void *out, float *lse, const void *
     return prefill_impl(shape, out, lse, q, nullptr, nullptr, k_pool, v_pool, block_table, max_blocks_per_seq,
                         num_blocks, cu_q_lens, seq_lens, num_seqs, total_tokens, max_q_len, scale, workspace,
                         workspace_bytes, stream);
+}
+
+pa_status paged_attn_prefill_window(pa_shape shape, void *out, float *lse, const void *q, const void *k_pool,
+                                    const void *v_pool, const int32_t *block_table, int32_t max_blocks_per_seq,
+                                    int32_t num_blocks, const int32_t *cu_q_lens, const int32_t *seq_lens,
+                                    int32_t num_seqs, int32_t total_tokens, int32_t max_q_len, int32_t window,
+                                    int32_t sinks, float scale, void *workspace, size_t workspace_bytes,
+                                    void *stream) {
+    if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
+    if (!window_ok(window, sinks)) return PA_ERR_INVALID_ARG;
+    const Window win = {window, sinks};
+    return prefill_impl(shape, out, lse, q, nullptr, nullptr, k_pool, v_pool, block_table, max_blocks_per_seq,
+                        num_blocks, cu_q_lens, seq_lens, num_seqs, total_tokens, max_q_len, scale, workspace,
+                        workspace_bytes, stream, &win);
 }
 
 pa_status paged_attn_prefill_append(pa_shape shape, void *out, float *lse, const void *q, const void *k_new,

@@ -28,6 +28,13 @@
 // recorded in the error word and makes the (sequence, KV head)'s output NaN.
 // The kernel is launched as a programmatic dependent of the previous kernel on the
 // stream, so its launch and prologue overlap e.g. the kv_append that precedes it.
+//
+// The sliding-window form (kWindow) attends to a sequence's first `sinks` and last `window`
+// tokens: the same kernel over the list of tiles that hold one of them.  Blocks without a
+// visible token are not touched, their table entries not used.  A tile that is visible only in
+// part is loaded in 16-row groups (a consumer warp's share), so that at most 15 rows are read
+// in vain at each end of the window and of the sinks; the rest of its rows are masked in the
+// scores and zeroed in V like those past the context end.
 #include <atomic>
 #include <mutex>
 
@@ -35,6 +42,7 @@
 
 #include "common.cuh"
 #include "launch.h"
+#include "window.cuh"
 
 namespace pa {
 namespace {
@@ -138,10 +146,12 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 // an atomic counter; splits past the context do no work but still meet the others at both
 // cluster barriers (so no barrier waits on a CTA that has left).  Same merge order and
 // arithmetic as the workspace path, so the results are bit-identical.
-template <bool kCluster>
-__global__ void __launch_bounds__(kThreads, 2)
-decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-              const DecodeArgs a) {
+//
+// kWindow: the splits cut the list of visible tiles; k16_map / v16_map have boxes of 16 rows.
+template <bool kCluster, bool kWindow>
+__device__ __forceinline__ void decode_body(const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                            const CUtensorMap &k16_map, const CUtensorMap &v16_map,
+                                            const DecodeArgs &a) {
     extern __shared__ uint8_t smem_raw[];
     DecodeSmem &sm = *reinterpret_cast<DecodeSmem *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -171,10 +181,31 @@ decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         if (lane == 0) {
             tma_prefetch_map(&k_map);
             tma_prefetch_map(&v_map);
+            if constexpr (kWindow) {
+                tma_prefetch_map(&k16_map);
+                tma_prefetch_map(&v16_map);
+            }
         }
-        if (wlo + lane < a.max_blocks_per_seq) bwin = __ldg(bt + wlo + lane);
+        if (!kWindow && wlo + lane < a.max_blocks_per_seq) bwin = __ldg(bt + wlo + lane);
     }
     const int seq_len = __ldg(a.seq_lens + b);
+    if constexpr (kWindow) {
+        // an empty sequence (a padded row of the batch) has nothing to see: zeros, lse -inf
+        if (seq_len == 0) {
+            if (split == 0 && warp < kConsumerWarps) {
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                const int qh = g * kGroup + warp;
+                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                store_out4(static_cast<__nv_bfloat16 *>(a.out) + ((size_t)b * kHq + qh) * kD + lane * 4, zero, 0.f);
+                if (a.lse && lane == 0) a.lse[(size_t)b * kHq + qh] = -INFINITY;
+            }
+            if constexpr (kCluster) {
+                cluster_sync_all();
+                cluster_sync_all();
+            }
+            return;
+        }
+    }
     // (a cascade attends only past the shared prefix: the context must extend beyond it)
     if (seq_len < 1 || seq_len > a.max_blocks_per_seq * kBlock || seq_len <= a.kv_begin) {
         if (split == 0 && g == 0 && threadIdx.x == 0) record_error(a.err, kErrDevice | kErrBadSeqLen);
@@ -185,7 +216,9 @@ decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         return;  // every CTA of this sequence takes the same exit: counters untouched
     }
     const int n_ctx = seq_len - a.kv_begin;
-    const int nsplit_b = (n_ctx + a.split_tokens - 1) / a.split_tokens;
+    const WindowTiles<kTile> wt(kWindow ? a.window : seq_len, kWindow ? a.sinks : 0, seq_len - 1, seq_len - 1);
+    const int nsplit_b = kWindow ? (wt.n + a.split_tokens / kTile - 1) / (a.split_tokens / kTile)
+                                 : (n_ctx + a.split_tokens - 1) / a.split_tokens;
     if (split >= nsplit_b) {              // this split lies past the context
         if constexpr (kCluster) {
             cluster_sync_all();
@@ -196,7 +229,10 @@ decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     const int len_b = ((n_ctx + nsplit_b - 1) / nsplit_b + kTile - 1) / kTile * kTile;
     const int t_begin = a.kv_begin + split * len_b;
     const int t_end = min(t_begin + len_b, seq_len);
-    const int n_tiles = (t_end - t_begin + kTile - 1) / kTile;
+    // (window: tiles v_begin .. v_begin + n_tiles - 1 of the list of visible ones)
+    const int v_len = (wt.n + nsplit_b - 1) / nsplit_b;
+    const int v_begin = split * v_len;
+    const int n_tiles = kWindow ? min(v_len, wt.n - v_begin) : (t_end - t_begin + kTile - 1) / kTile;
 
     if (threadIdx.x == 0) {
 #pragma unroll
@@ -213,7 +249,8 @@ decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
         // ------------------------------------------------------------ TMA producer
         const int wi = t_begin / kBlock - wlo;   // >= 0; beyond the window: fetch it now
         int blk0 = __shfl_sync(0xffffffffu, bwin, wi & 31);
-        if (wi < 0 || wi >= 32) blk0 = __ldg(bt + t_begin / kBlock);
+        if constexpr (kWindow) blk0 = __ldg(bt + wt.tile(v_begin) / (kBlock / kTile));
+        else if (wi < 0 || wi >= 32) blk0 = __ldg(bt + t_begin / kBlock);
         if (lane == 0) {
             // The pools may be written by the kernel just before this one on the stream
             // (kv_append lets us launch early): wait for it before the first pool read.
@@ -226,7 +263,7 @@ decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                     record_error(a.err, kErrTimeout);
                     break;
                 }
-                const int tok = t_begin + i * kTile;
+                const int tok = kWindow ? wt.tile(v_begin + i) * kTile : t_begin + i * kTile;
                 int blk = i == 0 ? blk0 : __ldg(bt + tok / kBlock);
                 if (blk < 0 || blk >= a.num_blocks) {
                     // a block id outside the pool: read block 0 instead and poison the result
@@ -236,6 +273,25 @@ decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
                 }
                 const int off = tok % kBlock;
                 const uint32_t bar = smem_u32(&sm.full[st]);
+                if constexpr (kWindow) {
+                    // the tile's 16-row groups that hold a visible token
+                    uint32_t need = 0;
+#pragma unroll
+                    for (int r = 0; r < kTile / 16; ++r)
+                        if (tok + 16 * r < seq_len && wt.sees_any(tok + 16 * r, 16)) need |= 1u << r;
+                    if (need != (1u << (kTile / 16)) - 1) {
+                        mbar_arrive_expect_tx(bar, __popc(need) * 16 * 2 * kRowBytes);
+                        for (int r = 0; r < kTile / 16; ++r) {
+                            if (!(need >> r & 1u)) continue;
+                            tma_load_4d(smem_u32(sm.tiles[st][0] + r * 2048), &k16_map, bar, 0, g, off + 16 * r, blk);
+                            tma_load_4d(smem_u32(sm.tiles[st][1] + r * 2048), &k16_map, bar, 64, g, off + 16 * r, blk);
+                            tma_load_4d(smem_u32(sm.tiles[st][2] + r * 2048), &v16_map, bar, 0, g, off + 16 * r, blk);
+                            tma_load_4d(smem_u32(sm.tiles[st][3] + r * 2048), &v16_map, bar, 64, g, off + 16 * r, blk);
+                        }
+                        issued = i + 1;
+                        continue;
+                    }
+                }
                 mbar_arrive_expect_tx(bar, kStageBytes);
                 tma_load_4d(smem_u32(sm.tiles[st][0]), &k_map, bar, 0, g, off, blk);
                 tma_load_4d(smem_u32(sm.tiles[st][1]), &k_map, bar, 64, g, off, blk);
@@ -295,7 +351,7 @@ decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     // V row of this KV head now (lanes 0-15: K, 16-31: V, 16 bytes each), stores them into the
     // pool and patches them over the (stale) row of the landed tile before using it.
     const int p_new = seq_len - 1;
-    const int i_new = (a.k_new && t_end == seq_len) ? (p_new - t_begin) / kTile : -1;
+    const int i_new = (!kWindow && a.k_new && t_end == seq_len) ? (p_new - t_begin) / kTile : -1;
     const int r_new = (p_new - t_begin) % kTile;        // row within that tile
     const bool new_here = i_new >= 0 && (r_new >> 4) == w;
     uint4 new_chunk = make_uint4(0u, 0u, 0u, 0u);
@@ -328,8 +384,12 @@ decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             fence_proxy_async_smem();   // generic writes before the stage is refilled by TMA
             __syncwarp();
         }
-        const int my_valid = min(max(t_end - (t_begin + i * kTile) - w * 16, 0), 16);
-        if (my_valid > 0) {
+        // this warp's 16 rows hold positions p_w .. p_w + 15, of which the first my_valid are in
+        // the context; valid(r): row r is attended to
+        const int p_w = kWindow ? wt.tile(v_begin + i) * kTile + w * 16 : t_begin + i * kTile + w * 16;
+        const int my_valid = min(max((kWindow ? seq_len : t_end) - p_w, 0), 16);
+        const auto valid = [&](int r) { return r < my_valid && (!kWindow || wt.sees(p_w + r)); };
+        if (my_valid > 0 && (!kWindow || wt.sees_any(p_w, 16))) {
             const uint32_t k_lo = smem_u32(sm.tiles[st][0]);
             const uint32_t k_hi = smem_u32(sm.tiles[st][1]);
             const uint32_t v_lo = smem_u32(sm.tiles[st][2]);
@@ -348,8 +408,8 @@ decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             // s[2]: (token gq+8, head 2tq) s[3]: (token gq+8, head 2tq+1)
             float x0, x1, x2, x3;
             if (tq < 2) {
-                const bool v_lo_ok = gq < my_valid;
-                const bool v_hi_ok = gq + 8 < my_valid;
+                const bool v_lo_ok = valid(gq);
+                const bool v_hi_ok = valid(gq + 8);
                 x0 = v_lo_ok ? s[0] * a.scale_log2 : -INFINITY;
                 x1 = v_lo_ok ? s[1] * a.scale_log2 : -INFINITY;
                 x2 = v_hi_ok ? s[2] * a.scale_log2 : -INFINITY;
@@ -384,11 +444,10 @@ decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
             // P^T as the B operand of O^T += V^T P^T: transpose the 8x8 bf16 blocks.
             const uint32_t pb0 = movmatrix_trans(pp_lo);
             const uint32_t pb1 = movmatrix_trans(pp_hi);
-            // V rows past the context end are zeroed in the fragment (0 * NaN = NaN).
-            const uint32_t keep_lo = (2 * tq < my_valid ? 0x0000ffffu : 0u) |
-                                     (2 * tq + 1 < my_valid ? 0xffff0000u : 0u);
-            const uint32_t keep_hi = (2 * tq + 8 < my_valid ? 0x0000ffffu : 0u) |
-                                     (2 * tq + 9 < my_valid ? 0xffff0000u : 0u);
+            // V rows not attended to are zeroed in the fragment (0 * NaN = NaN).
+            const uint32_t keep_lo = (valid(2 * tq) ? 0x0000ffffu : 0u) | (valid(2 * tq + 1) ? 0xffff0000u : 0u);
+            const uint32_t keep_hi = (valid(2 * tq + 8) ? 0x0000ffffu : 0u) |
+                                     (valid(2 * tq + 9) ? 0xffff0000u : 0u);
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
                 uint32_t af[4];
@@ -566,29 +625,25 @@ decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__
     if (a.lse && (c & 31) == 0) a.lse[(size_t)b * kHq + qh] = (GM + __log2f(GL)) * kLn2;
 }
 
-}  // namespace
-
-cudaError_t configure_decode() {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    static std::atomic<bool> configured[64] = {};
-    if (dev < 0 || dev >= 64 || !configured[dev].load()) {
-        e = cudaFuncSetAttribute(decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-        if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) configured[dev].store(true);
-    }
-    return cudaSuccess;
+template <bool kCluster>
+__global__ void __launch_bounds__(kThreads, 2)
+decode_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+              const DecodeArgs a) {
+    decode_body<kCluster, false>(k_map, v_map, k_map, v_map, a);
 }
 
-cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
-                          int num_sms, cudaStream_t stream) {
-    (void)num_sms;
-    if (a.batch == 0) return cudaSuccess;
-    cudaError_t e = configure_decode();
-    if (e != cudaSuccess) return e;
+template <bool kCluster>
+__global__ void __launch_bounds__(kThreads, 2)
+decode_window_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                     const __grid_constant__ CUtensorMap k16_map, const __grid_constant__ CUtensorMap v16_map,
+                     const DecodeArgs a) {
+    decode_body<kCluster, true>(k_map, v_map, k16_map, v16_map, a);
+}
+
+// Launch `plain`, or `clustered` with a pair's splits as a cluster when the call asks for it.
+template <typename Kernel, typename... Maps>
+cudaError_t launch_either(Kernel plain, Kernel clustered, const DecodeArgs &a, cudaStream_t stream,
+                          const Maps &...maps) {
     // Programmatic dependent launch: the prologue may overlap the previous kernel on the
     // stream; the producer waits for it (griddepcontrol.wait) before reading the pools.
     cudaLaunchConfig_t cfg = {};
@@ -608,7 +663,7 @@ cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map, const C
         attr[1].val.clusterDim.y = (unsigned)a.nsplit;
         attr[1].val.clusterDim.z = 1;
         cfg.numAttrs = 2;
-        e = cudaLaunchKernelEx(&cfg, decode_kernel<true>, k_map, v_map, a);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, clustered, maps..., a);
         if (e != cudaErrorLaunchOutOfResources && e != cudaErrorInvalidClusterSize && e != cudaErrorNotSupported &&
             e != cudaErrorCooperativeLaunchTooLarge)
             return e;
@@ -618,7 +673,48 @@ cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map, const C
         cudaGetLastError();
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, decode_kernel<false>, k_map, v_map, a);
+    return cudaLaunchKernelEx(&cfg, plain, maps..., a);
+}
+
+}  // namespace
+
+cudaError_t configure_decode() {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<bool> configured[64] = {};
+    if (dev < 0 || dev >= 64 || !configured[dev].load()) {
+        e = cudaFuncSetAttribute(decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(decode_window_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kSmemBytes);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(decode_window_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kSmemBytes);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev].store(true);
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                          int num_sms, cudaStream_t stream) {
+    (void)num_sms;
+    if (a.batch == 0) return cudaSuccess;
+    cudaError_t e = configure_decode();
+    if (e != cudaSuccess) return e;
+    return launch_either(decode_kernel<false>, decode_kernel<true>, a, stream, k_map, v_map);
+}
+
+cudaError_t launch_decode_window(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                 const CUtensorMap &k16_map, const CUtensorMap &v16_map, cudaStream_t stream) {
+    if (a.batch == 0) return cudaSuccess;
+    const cudaError_t e = configure_decode();
+    if (e != cudaSuccess) return e;
+    return launch_either(decode_window_kernel<false>, decode_window_kernel<true>, a, stream, k_map, v_map, k16_map,
+                         v16_map);
 }
 
 // ------------------------------------------------------------------ fixed scratch

@@ -27,10 +27,13 @@
 //     largest V scale it has seen), accumulates P * (s_v / sigma) in f16 and rescales
 //     its accumulator when sigma grows, as the online softmax does for its maximum; the
 //     warp merge multiplies by sigma back.
+// The sliding-window form (kWindow) walks the list of stages that hold a visible token, as in
+// decode.cu: a stage that is visible only in part gets its 16-row groups one by one.
 #include <atomic>
 
 #include "common.cuh"
 #include "launch.h"
+#include "window.cuh"
 
 namespace pa {
 namespace {
@@ -79,9 +82,11 @@ __device__ __forceinline__ void v_pairs(uint32_t r, uint32_t &lo, uint32_t &hi) 
     e4m3x4_to_f16x2x2(__byte_perm(r, 0u, 0x3120), lo, hi);
 }
 
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
-decode_fp8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
-                  const DecodeArgs a) {
+// kWindow: k16_map / v16_map have boxes of 16 rows.
+template <bool kWindow>
+__device__ __forceinline__ void decode_fp8_body(const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                                const CUtensorMap &k16_map, const CUtensorMap &v16_map,
+                                                const DecodeArgs &a) {
     extern __shared__ uint8_t smem_raw[];
     DecodeFp8Smem &sm = *reinterpret_cast<DecodeFp8Smem *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -99,18 +104,42 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
     if (warp == kConsumerWarps && lane == 0) {
         tma_prefetch_map(&k_map);
         tma_prefetch_map(&v_map);
-        blk0 = __ldg(bt + (split * a.split_tokens) / kBlock);   // < max_blocks_per_seq
+        if constexpr (kWindow) {
+            tma_prefetch_map(&k16_map);
+            tma_prefetch_map(&v16_map);
+        } else {
+            blk0 = __ldg(bt + (split * a.split_tokens) / kBlock);   // < max_blocks_per_seq
+        }
     }
     const int seq_len = __ldg(a.seq_lens + b);
+    if constexpr (kWindow) {
+        // an empty sequence (a padded row of the batch) has nothing to see: zeros, lse -inf
+        if (seq_len == 0) {
+            if (split == 0 && warp < kGroup) {
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                const int qh = g * kGroup + warp;
+                const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+                store_out4(static_cast<__nv_bfloat16 *>(a.out) + ((size_t)b * kHq + qh) * kD + lane * 4, zero, 0.f);
+                if (a.lse && lane == 0) a.lse[(size_t)b * kHq + qh] = -INFINITY;
+            }
+            return;
+        }
+    }
     if (seq_len < 1 || seq_len > a.max_blocks_per_seq * kBlock) {
         if (split == 0 && g == 0 && threadIdx.x == 0) record_error(a.err, kErrDevice | kErrBadSeqLen);
         return;
     }
+    const WindowTiles<kTile> wt(kWindow ? a.window : seq_len, kWindow ? a.sinks : 0, seq_len - 1, seq_len - 1);
+    const int per_split = a.split_tokens / kTile;
+    const int nsplit_b = kWindow ? (wt.n + per_split - 1) / per_split
+                                 : (seq_len + a.split_tokens - 1) / a.split_tokens;
+    if (split >= nsplit_b) return;        // past the context
     const int t_begin = split * a.split_tokens;
-    if (t_begin >= seq_len) return;
     const int t_end = min(t_begin + a.split_tokens, seq_len);
-    const int nsplit_b = (seq_len + a.split_tokens - 1) / a.split_tokens;
-    const int n_tiles = (t_end - t_begin + kTile - 1) / kTile;
+    // (window: tiles v_begin .. v_begin + n_tiles - 1 of the list of visible ones)
+    const int v_len = (wt.n + nsplit_b - 1) / nsplit_b;
+    const int v_begin = split * v_len;
+    const int n_tiles = kWindow ? min(v_len, wt.n - v_begin) : (t_end - t_begin + kTile - 1) / kTile;
 
     if (threadIdx.x == 0) {
 #pragma unroll
@@ -129,13 +158,14 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
             // the cache may be written by the kernel just before this one on the stream
             asm volatile("griddepcontrol.wait;" ::: "memory");
             int issued = 0;
+            if constexpr (kWindow) blk0 = __ldg(bt + wt.tile(v_begin) / (kBlock / kTile));
             for (int i = 0; i < n_tiles; ++i) {
                 const int st = i % kStages;
                 if (i >= kStages && !mbar_wait(smem_u32(&sm.empty[st]), ((i / kStages) - 1) & 1)) {
                     record_error(a.err, kErrTimeout);
                     break;
                 }
-                const int tok = t_begin + i * kTile;
+                const int tok = kWindow ? wt.tile(v_begin + i) * kTile : t_begin + i * kTile;
                 int blk = i == 0 ? blk0 : __ldg(bt + tok / kBlock);
                 if (blk < 0 || blk >= a.num_blocks) {
                     record_error(a.err, kErrDevice | kErrBadBlock);
@@ -145,9 +175,25 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
                 const int off = tok % kBlock;
                 const uint32_t bar = smem_u32(&sm.full[st]);
                 const size_t srow = ((size_t)blk * kHkv + g) * kBlock + off;   // 64 scales, 256 B aligned
-                mbar_arrive_expect_tx(bar, kStageTx);
-                tma_load_4d(smem_u32(sm.codes[st][0]), &k_map, bar, 0, g, off, blk);
-                tma_load_4d(smem_u32(sm.codes[st][1]), &v_map, bar, 0, g, off, blk);
+                // the stage's 16-row groups that hold a visible token
+                uint32_t need = kWindow ? 0 : (1u << (kTile / 16)) - 1;
+                if constexpr (kWindow) {
+#pragma unroll
+                    for (int r = 0; r < kTile / 16; ++r)
+                        if (tok + 16 * r < seq_len && wt.sees_any(tok + 16 * r, 16)) need |= 1u << r;
+                }
+                if (!kWindow || need == (1u << (kTile / 16)) - 1) {
+                    mbar_arrive_expect_tx(bar, kStageTx);
+                    tma_load_4d(smem_u32(sm.codes[st][0]), &k_map, bar, 0, g, off, blk);
+                    tma_load_4d(smem_u32(sm.codes[st][1]), &v_map, bar, 0, g, off, blk);
+                } else {
+                    mbar_arrive_expect_tx(bar, __popc(need) * 16 * 2 * kD + 2 * kScaleBytes);
+                    for (int r = 0; r < kTile / 16; ++r) {
+                        if (!(need >> r & 1u)) continue;
+                        tma_load_4d(smem_u32(sm.codes[st][0] + r * 2048), &k16_map, bar, 0, g, off + 16 * r, blk);
+                        tma_load_4d(smem_u32(sm.codes[st][1] + r * 2048), &v16_map, bar, 0, g, off + 16 * r, blk);
+                    }
+                }
                 bulk_load(smem_u32(sm.scales[st][0]), a.k_scale + srow, kScaleBytes, bar);
                 bulk_load(smem_u32(sm.scales[st][1]), a.v_scale + srow, kScaleBytes, bar);
                 issued = i + 1;
@@ -199,7 +245,7 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
     // (lanes 16-31) row of this KV head, 8 values a lane, stores codes and scale into the
     // cache and patches them over the stale row of the landed stage before using it.
     const int p_new = seq_len - 1;
-    const int i_new = (a.k_new && t_end == seq_len) ? (p_new - t_begin) / kTile : -1;
+    const int i_new = (!kWindow && a.k_new && t_end == seq_len) ? (p_new - t_begin) / kTile : -1;
     const int r_new = (p_new - t_begin) % kTile;        // row within that stage
     const bool new_here = i_new >= 0 && (r_new >> 4) == w;
     uint2 new_codes = make_uint2(0u, 0u);
@@ -251,8 +297,12 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
             fence_proxy_async_smem();   // generic writes before the stage is refilled by TMA
             __syncwarp();
         }
-        const int my_valid = min(max(t_end - (t_begin + i * kTile) - w * 16, 0), 16);
-        if (my_valid > 0) {
+        // this warp's 16 rows hold positions p_w .. p_w + 15, of which the first my_valid are in
+        // the context; valid(r): row r is attended to
+        const int p_w = (kWindow ? wt.tile(v_begin + i) * kTile : t_begin + i * kTile) + w * 16;
+        const int my_valid = min(max((kWindow ? seq_len : t_end) - p_w, 0), 16);
+        const auto valid = [&](int r) { return r < my_valid && (!kWindow || wt.sees(p_w + r)); };
+        if (my_valid > 0 && (!kWindow || wt.sees_any(p_w, 16))) {
             const uint32_t kc = smem_u32(sm.codes[st][0]);
             const uint32_t vc = smem_u32(sm.codes[st][1]);
             const float *ksc = sm.scales[st][0] + w * 16;
@@ -276,8 +326,8 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
             for (int e = 0; e < 4; ++e) s[e] += s2[e];
             // s[0]: (token gq, head 2tq)   s[1]: (token gq, head 2tq+1)
             // s[2]: (token gq+8, head 2tq) s[3]: (token gq+8, head 2tq+1)
-            const bool v_lo_ok = gq < my_valid;
-            const bool v_hi_ok = gq + 8 < my_valid;
+            const bool v_lo_ok = valid(gq);
+            const bool v_hi_ok = valid(gq + 8);
             float x0, x1, x2, x3;
             if (tq < 2) {
                 const float k_lo = v_lo_ok ? ksc[gq] * a.scale_log2 : 0.f;
@@ -351,11 +401,10 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
             // P^T as the B operand of O^T += V^T P^T: transpose the 8x8 16-bit blocks.
             const uint32_t pb0 = movmatrix_trans(pp_lo);
             const uint32_t pb1 = movmatrix_trans(pp_hi);
-            // V codes of tokens past the context end are zeroed in the fragment.
-            const uint32_t keep_lo = (2 * tq < my_valid ? 0x0000ffffu : 0u) |
-                                     (2 * tq + 1 < my_valid ? 0xffff0000u : 0u);
-            const uint32_t keep_hi = (2 * tq + 8 < my_valid ? 0x0000ffffu : 0u) |
-                                     (2 * tq + 9 < my_valid ? 0xffff0000u : 0u);
+            // V codes of tokens not attended to are zeroed in the fragment.
+            const uint32_t keep_lo = (valid(2 * tq) ? 0x0000ffffu : 0u) | (valid(2 * tq + 1) ? 0xffff0000u : 0u);
+            const uint32_t keep_hi = (valid(2 * tq + 8) ? 0x0000ffffu : 0u) |
+                                     (valid(2 * tq + 9) ? 0xffff0000u : 0u);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 // matrices: tokens 0-7 / 8-15 of the warp x dims 32j..32j+15 / 32j+16..32j+31
@@ -486,10 +535,21 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
     if (a.lse && (c & 31) == 0) a.lse[(size_t)b * kHq + qh] = (GM + __log2f(GL)) * kLn2;
 }
 
-}  // namespace
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+decode_fp8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                  const DecodeArgs a) {
+    decode_fp8_body<false>(k_map, v_map, k_map, v_map, a);
+}
 
-cudaError_t launch_decode_fp8(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
-                              cudaStream_t stream) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+decode_window_fp8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                         const __grid_constant__ CUtensorMap k16_map, const __grid_constant__ CUtensorMap v16_map,
+                         const DecodeArgs a) {
+    decode_fp8_body<true>(k_map, v_map, k16_map, v16_map, a);
+}
+
+cudaError_t launch_fp8(bool window, const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                       const CUtensorMap &k16_map, const CUtensorMap &v16_map, cudaStream_t stream) {
     if (a.batch == 0) return cudaSuccess;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -497,6 +557,9 @@ cudaError_t launch_decode_fp8(const DecodeArgs &a, const CUtensorMap &k_map, con
     static std::atomic<bool> configured[64] = {};
     if (dev < 0 || dev >= 64 || !configured[dev].load()) {
         e = cudaFuncSetAttribute(decode_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(decode_window_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kSmemBytes);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(true);
     }
@@ -510,7 +573,20 @@ cudaError_t launch_decode_fp8(const DecodeArgs &a, const CUtensorMap &k_map, con
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, decode_fp8_kernel, k_map, v_map, a);
+    return window ? cudaLaunchKernelEx(&cfg, decode_window_fp8_kernel, k_map, v_map, k16_map, v16_map, a)
+                  : cudaLaunchKernelEx(&cfg, decode_fp8_kernel, k_map, v_map, a);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_fp8(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                              cudaStream_t stream) {
+    return launch_fp8(false, a, k_map, v_map, k_map, v_map, stream);
+}
+
+cudaError_t launch_decode_window_fp8(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                     const CUtensorMap &k16_map, const CUtensorMap &v16_map, cudaStream_t stream) {
+    return launch_fp8(true, a, k_map, v_map, k16_map, v16_map, stream);
 }
 
 }  // namespace pa

@@ -59,6 +59,11 @@ struct DecodeArgs {
     float *part_o;         // [batch * 8 * nsplit][4][128]
     float *part_ml;        // [batch * 8 * nsplit][4][2]
     uint32_t *err;
+    // Sliding window (window > 0): a sequence of n tokens attends to its first `sinks` and its
+    // last `window` ones.  Splits then cut the list of 64-token tiles (128 in the 8-bit cache)
+    // that hold a visible token, split_tokens / tile of them a CTA.
+    int32_t window;
+    int32_t sinks;
     // Decode kernel only: 1 = the splits of a (sequence, KV head) form a cluster (nsplit <= 8)
     // and merge through its shared memory; the counters and partials are not used.
     int32_t cluster_merge;
@@ -95,6 +100,10 @@ struct PrefillArgs {
     const void *v_new;
     void *k_pool_w;
     void *v_pool_w;
+    // Sliding window (launch_prefill_window): the query at position p sees keys j <= p with
+    // j < sinks or j > p - window.
+    int32_t window;
+    int32_t sinks;
 };
 
 constexpr int kRopePairs = 64;   // rotated pairs of a 128-dim head
@@ -176,6 +185,12 @@ cudaError_t configure_decode();
 
 cudaError_t launch_decode(const DecodeArgs &a, const CUtensorMap &k_map,
                           const CUtensorMap &v_map, int num_sms, cudaStream_t stream);
+// a.window set; k16 / v16: the same maps with boxes of 16 rows, for tiles of which only some
+// 16-row groups are visible.
+cudaError_t launch_decode_window(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                 const CUtensorMap &k16_map, const CUtensorMap &v16_map, cudaStream_t stream);
+cudaError_t launch_decode_window_fp8(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                                     const CUtensorMap &k16_map, const CUtensorMap &v16_map, cudaStream_t stream);
 
 // q_map: 3-D map over q; k_map / v_map: 4-D maps over the pools.
 // Decode over the 8-bit cache (code pools as k_map / v_map, scales in the args); its
@@ -195,6 +210,10 @@ long long prefill_plan_units(const PrefillArgs &a);
 cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map,
                            const CUtensorMap &k_map, const CUtensorMap &v_map, int num_sms,
                            cudaStream_t stream);
+
+// a.window set.
+cudaError_t launch_prefill_window(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
+                                  const CUtensorMap &v_map, int num_sms, cudaStream_t stream);
 
 // The prefill with the append of the new tokens fused in (a.k_new set): kn_map / vn_map are
 // 3-D maps (dim, head, token) over k_new / v_new with box {64, 1, 128}.

@@ -38,10 +38,14 @@
 // overwrite P_X(j) before O_X += P_X(j) V_j has read it.  The softmax keeps a running
 // max and, only when it grows by more than 2^8, rescales O (lazy rescaling); the row
 // sum accumulates the same bf16-rounded weights the PV product uses.
+// The sliding-window form (kWindow: each query sees the first `sinks` tokens and the `window`
+// ones up to itself) visits the key tiles that any of the unit's 64 positions sees -- those of
+// the sinks, then those of the window -- and masks at most the first and last of each.
 // Every wait is bounded; on expiry the CTA records PA_ERR_TIMEOUT, unwinds, waits
 // (bounded) for its own copies and MMAs, frees tensor memory and exits.
 #include "common.cuh"
 #include "launch.h"
+#include "window.cuh"
 
 namespace pa {
 namespace {
@@ -105,7 +109,17 @@ struct Unit {
     int c0;
     int n_old;
     int tok_base;
+    // Sliding window: the tiles visited are n_sink tiles from 0, then those from w0 on; keys in
+    // [s_end, lo) are seen by none of the unit's queries.
+    int s_end, lo, n_sink, w0;
 };
+
+// Key tile visited at step j of a unit.
+template <bool kWindow>
+__device__ __forceinline__ int key_tile(const Unit &t, int j) {
+    if constexpr (kWindow) return j < t.n_sink ? j : t.w0 + (j - t.n_sink);
+    else return t.kt0 + j;
+}
 
 // Position of row 0 of key tile jg and the bound past which its rows are not keys.
 __device__ __forceinline__ void key_tile_span(const Unit &t, int jg, int &base, int &limit) {
@@ -114,7 +128,7 @@ __device__ __forceinline__ void key_tile_span(const Unit &t, int jg, int &base, 
     limit = old_tile ? t.c0 : t.seq_len;
 }
 
-template <bool kAppend>
+template <bool kAppend, bool kWindow>
 __device__ __forceinline__ Unit unit_at(const PrefillArgs &a, int idx, int qblocks) {
     Unit t;
     const int per_qb = a.num_seqs * kHkv;
@@ -151,6 +165,14 @@ __device__ __forceinline__ Unit unit_at(const PrefillArgs &a, int idx, int qbloc
         t.n_kt = (t.pos0 + t.positions - 1) / kKT + 1;
         t.n_old = t.n_kt;
     }
+    if constexpr (kWindow) {
+        const WindowTiles<kKT> wt(a.window, a.sinks, t.pos0, t.pos0 + t.positions - 1);
+        t.s_end = wt.s;
+        t.lo = wt.lo;
+        t.n_sink = wt.n_sink;
+        t.w0 = wt.w0;
+        t.n_kt = wt.n;
+    }
     return t;
 }
 
@@ -179,17 +201,17 @@ __device__ __forceinline__ Unit unit_at_prefix(const PrefillArgs &a, int idx, in
     return t;
 }
 
-template <bool kPrefix, bool kPlanned, bool kAppend>
+template <bool kPrefix, bool kPlanned, bool kAppend, bool kWindow>
 __device__ __forceinline__ Unit unit_for(const PrefillArgs &a, int idx, int qblocks) {
     if constexpr (kPrefix) return unit_at_prefix(a, idx, qblocks);
-    else if constexpr (kPlanned) return unit_at<kAppend>(a, __ldg(a.order + idx), qblocks);
-    else return unit_at<kAppend>(a, idx, qblocks);
+    else if constexpr (kPlanned) return unit_at<kAppend, kWindow>(a, __ldg(a.order + idx), qblocks);
+    else return unit_at<kAppend, kWindow>(a, idx, qblocks);
 }
 
 // Key tiles of unit idx (the unit_at rule; 0 for a unit without work, which sorts last).
-template <bool kAppend>
+template <bool kAppend, bool kWindow>
 __device__ __forceinline__ int plan_key(const PrefillArgs &a, int idx, int qblocks) {
-    const Unit t = unit_at<kAppend>(a, idx, qblocks);
+    const Unit t = unit_at<kAppend, kWindow>(a, idx, qblocks);
     return t.run ? t.n_kt : 0;
 }
 
@@ -202,7 +224,7 @@ inline int plan_keys(const PrefillArgs &a) { return 2 * a.max_blocks_per_seq + 2
 // first (longest processing time first), written as order[rank] = unit.  Units with equal
 // keys take their ranks in whatever order the atomics resolve; every unit is computed by
 // one CTA on its own, so the outputs do not depend on that order.  nk = key buckets.
-template <bool kAppend>
+template <bool kAppend, bool kWindow>
 __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const PrefillArgs a, int qblocks, int total,
                                                                        int nk) {
     __shared__ int hist[kPlanMaxKeys];
@@ -211,7 +233,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const Pre
     for (int k = tid; k < nk; k += kPlanThreads) hist[k] = 0;
     __syncthreads();
     for (int idx = tid; idx < total; idx += kPlanThreads)
-        atomicAdd(&hist[min(plan_key<kAppend>(a, idx, qblocks), nk - 1)], 1);
+        atomicAdd(&hist[min(plan_key<kAppend, kWindow>(a, idx, qblocks), nk - 1)], 1);
     __syncthreads();
     // hist[k] <- first rank of key k = number of units with more key tiles.  Thread t owns
     // the keys hi, hi - 1, ..., hi - per + 1 counted from the top.
@@ -249,7 +271,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const Pre
     }
     __syncthreads();
     for (int idx = tid; idx < total; idx += kPlanThreads) {
-        const int rank = atomicAdd(&hist[min(plan_key<kAppend>(a, idx, qblocks), nk - 1)], 1);
+        const int rank = atomicAdd(&hist[min(plan_key<kAppend, kWindow>(a, idx, qblocks), nk - 1)], 1);
         a.order[rank] = idx;
     }
     // Complete only after the kernel before this one on the stream (kv_append lets its
@@ -349,7 +371,7 @@ __device__ __forceinline__ void append_share(const PrefillArgs &a, int lane) {
     }
 }
 
-template <bool kPrefix, bool kPlanned, bool kAppend>
+template <bool kPrefix, bool kPlanned, bool kAppend, bool kWindow>
 __global__ void __launch_bounds__(kAppend ? kThreadsAppend : kThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap kn_map,
@@ -424,7 +446,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         for (int r = 0; ok; ++r) {
             const int idx = snake(r, total);
             if (idx < 0) break;
-            const Unit t = unit_for<kPrefix, kPlanned, kAppend>(a, idx, qblocks);
+            const Unit t = unit_for<kPrefix, kPlanned, kAppend, kWindow>(a, idx, qblocks);
             if (qk && leader && t.error) record_error(a.err, kErrDevice | kErrQLen);
             if (!t.run) continue;
             if (qk) {
@@ -446,7 +468,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
             const int32_t *bt = a.block_table + (size_t)t.s * a.max_blocks_per_seq;
             for (int j = 0; j < t.n_kt; ++j, ++it) {
                 const int st = it % ns;
-                const int jg = t.kt0 + j;              // key tile within the context
+                const int jg = key_tile<kWindow>(t, j);   // key tile within the context
                 const bool cache_tile = !kAppend || jg < t.n_old;
                 int blk = cache_tile ? __ldg(bt + (jg >> 1)) : 0;
                 if (blk < 0 || blk >= a.num_blocks) {
@@ -559,7 +581,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         for (int r = 0; ok; ++r) {
             const int idx = snake(r, total);
             if (idx < 0) break;
-            const Unit t = unit_for<kPrefix, kPlanned, kAppend>(a, idx, qblocks);
+            const Unit t = unit_for<kPrefix, kPlanned, kAppend, kWindow>(a, idx, qblocks);
             if (!t.run) continue;
             if (!(ok = wait_all(&sm.q_full, tcount & 1))) break;
             for (int j = 0; j < t.n_kt; ++j, ++it) {
@@ -598,7 +620,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         for (int r = 0; !has_unit; ++r) {
             const int idx = snake(r, total);
             if (idx < 0) break;
-            has_unit = unit_for<kPrefix, kPlanned, kAppend>(a, idx, qblocks).run;
+            has_unit = unit_for<kPrefix, kPlanned, kAppend, kWindow>(a, idx, qblocks).run;
         }
         if (has_unit) mbar_wait(smem_u32(&sm.o_done[0]), 0, 200000ull);
         append_share(a, lane);
@@ -618,7 +640,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         for (int r = 0; ok; ++r) {
             const int idx = snake(r, total);
             if (idx < 0) break;
-            const Unit t = unit_for<kPrefix, kPlanned, kAppend>(a, idx, qblocks);
+            const Unit t = unit_for<kPrefix, kPlanned, kAppend, kWindow>(a, idx, qblocks);
             if (!t.run) continue;
             // the last key each row may see: its own position (causal), or the whole prefix
             const int pos_first = kPrefix ? t.seq_len - 1 : t.pos0 + x * kTilePos;
@@ -638,7 +660,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 // mask of the keys past each row's last visible key and of the tile's rows that
                 // are no keys (past its span; only on tiles reaching past either) and the row
                 // maximum of the raw scores
-                const int jg = t.kt0 + j;                  // key tile within the context
+                const int jg = key_tile<kWindow>(t, j);    // key tile within the context
                 int base = jg * kKT, kv_valid = t.seq_len - jg * kKT;   // rows 0 .. kv_valid-1 are keys
                 if constexpr (kAppend) {
                     int limit;
@@ -647,8 +669,28 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 }
                 // (without the fused append a tile's rows past kv_valid lie past every query's
                 // position, so the causal mask covers them)
-                if (base + kKT - 1 > pos_first || (kAppend && kv_valid < kKT)) {
-                    if constexpr (kAppend) {
+                // window: the tile's rows that some query of this MMA tile may not see lie past its
+                // first position, or before its last one's window and behind the sinks
+                const bool edge = base + kKT - 1 > pos_first || (kAppend && kv_valid < kKT) ||
+                                  (kWindow && base <= pos_first + kTilePos - 1 - a.window && base + kKT > a.sinks);
+                if (edge) {
+                    if constexpr (kWindow) {
+                        // a bit per column, 32 columns at a time: up to the row's position, and in
+                        // its window or among the sinks
+                        const int hi = pos - base + 1;               // columns below hi
+                        const int lo = hi - min(a.window, hi + kKT);   // columns from lo on
+                        const int sk = a.sinks - base;               // or below sk
+                        const auto below = [](int n) {               // bits 0 .. n-1
+                            return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+                        };
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const uint32_t see = below(hi - c * 32) & (~below(lo - c * 32) | below(sk - c * 32));
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see >> e & 1u)) s[c][e] = __float_as_uint(-INFINITY);
+                        }
+                    } else if constexpr (kAppend) {
                         // one bound per row, tile rows 0 .. lim-1 being keys this row may see
                         // (one compare per score instead of two: 2.8 % of the fused step)
                         const int lim = min(kv_valid, pos - base + 1);
@@ -710,11 +752,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 // positions, or rows of another sequence in k_new) may hold anything, NaN
                 // included; P is 0 there but 0 * NaN is not, so tile A (the V tile's first
                 // reader) zeroes them.
-                if (x == 0 && kv_valid < kKT) {
+                // (window: also the rows before every query's window and behind the sinks, which
+                // may have been dropped)
+                const bool hidden = kWindow && base < t.lo && base + kKT > t.s_end;
+                if (x == 0 && (kv_valid < kKT || hidden)) {
                     const int vs = it % kVStages;
                     ok = wait_or_abort(smem_u32(&sm.v_full[vs]), (it / kVStages) & 1, abort_flag, a.err);
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    if (row >= kv_valid) {
+                    if (row >= kv_valid || (hidden && base + row < t.lo && base + row >= t.s_end)) {
                         uint4 *r0 = reinterpret_cast<uint4 *>(sm.v[vs][0] + row * 128);
                         uint4 *r1 = reinterpret_cast<uint4 *>(sm.v[vs][1] + row * 128);
 #pragma unroll
@@ -820,7 +865,7 @@ __global__ void wait_selftest_kernel(uint32_t *err, uint64_t limit_ns) {
     if (threadIdx.x == 0 && !mbar_wait(smem_u32(&bar), 0, limit_ns)) record_error(err, kErrTimeout);
 }
 
-template <bool kPrefix, bool kPlanned, bool kAppend>
+template <bool kPrefix, bool kPlanned, bool kAppend, bool kWindow = false>
 cudaError_t launch_prefill_mode(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
                                 const CUtensorMap &v_map, const CUtensorMap &kn_map, const CUtensorMap &vn_map,
                                 int num_sms, cudaStream_t stream) {
@@ -829,7 +874,7 @@ cudaError_t launch_prefill_mode(const PrefillArgs &a, const CUtensorMap &q_map, 
     if (e != cudaSuccess) return e;
     static bool configured[64] = {};
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(prefill_kernel<kPrefix, kPlanned, kAppend>,
+        e = cudaFuncSetAttribute(prefill_kernel<kPrefix, kPlanned, kAppend, kWindow>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
@@ -850,14 +895,14 @@ cudaError_t launch_prefill_mode(const PrefillArgs &a, const CUtensorMap &q_map, 
         cfg.gridDim = dim3(1);
         cfg.blockDim = dim3(kPlanThreads);
         cfg.dynamicSmemBytes = 0;
-        e = cudaLaunchKernelEx(&cfg, prefill_plan_kernel<kAppend>, a, (int)qblocks, (int)units, plan_keys(a));
+        e = cudaLaunchKernelEx(&cfg, prefill_plan_kernel<kAppend, kWindow>, a, (int)qblocks, (int)units, plan_keys(a));
         if (e != cudaSuccess) return e;
     }
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kAppend ? kThreadsAppend : kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
-    return cudaLaunchKernelEx(&cfg, prefill_kernel<kPrefix, kPlanned, kAppend>, q_map, k_map, v_map, kn_map, vn_map,
-                              a);
+    return cudaLaunchKernelEx(&cfg, prefill_kernel<kPrefix, kPlanned, kAppend, kWindow>, q_map, k_map, v_map, kn_map,
+                              vn_map, a);
 }
 
 }  // namespace
@@ -873,6 +918,14 @@ cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map, const
     // (the maps of the new rows are unused without the fused append)
     if (a.order) return launch_prefill_mode<false, true, false>(a, q_map, k_map, v_map, k_map, v_map, num_sms, stream);
     return launch_prefill_mode<false, false, false>(a, q_map, k_map, v_map, k_map, v_map, num_sms, stream);
+}
+
+cudaError_t launch_prefill_window(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
+                                  const CUtensorMap &v_map, int num_sms, cudaStream_t stream) {
+    if (a.num_seqs == 0 || a.max_q_len == 0 || a.total_tokens == 0) return cudaSuccess;
+    if (a.order)
+        return launch_prefill_mode<false, true, false, true>(a, q_map, k_map, v_map, k_map, v_map, num_sms, stream);
+    return launch_prefill_mode<false, false, false, true>(a, q_map, k_map, v_map, k_map, v_map, num_sms, stream);
 }
 
 cudaError_t launch_prefill_append(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,

@@ -91,6 +91,15 @@ def load() -> ctypes.CDLL:
     lib.paged_attn_decode_split.argtypes = [pa_shape, vp, vp, vp, vp, vp, vp, i32, i32, vp, i32,
                                             f32, i32, vp, sz, vp]
     lib.paged_attn_decode_split.restype = ctypes.c_int
+    lib.paged_attn_decode_window.argtypes = [pa_shape, vp, vp, vp, vp, vp, vp, i32, i32, vp, i32, i32, i32, f32, i32,
+                                             vp, sz, vp]
+    lib.paged_attn_decode_window.restype = ctypes.c_int
+    lib.paged_attn_decode_window_fp8.argtypes = [pa_shape, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp, i32, i32, i32,
+                                                 f32, i32, vp, sz, vp]
+    lib.paged_attn_decode_window_fp8.restype = ctypes.c_int
+    lib.paged_attn_prefill_window.argtypes = [pa_shape, vp, vp, vp, vp, vp, vp, i32, i32, vp, vp, i32, i32, i32, i32,
+                                              i32, f32, vp, sz, vp]
+    lib.paged_attn_prefill_window.restype = ctypes.c_int
     lib.paged_attn_decode_append.argtypes = [pa_shape, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp,
                                              i32, f32, vp, sz, vp]
     lib.paged_attn_decode_append.restype = ctypes.c_int
@@ -701,6 +710,90 @@ def paged_attn_prefill_append(q, k_new, v_new, k_pool, v_pool, block_table, cu_q
                                           int(max_q_len), float(scale), workspace.data_ptr(), workspace.numel(),
                                           _stream(stream))
     _check("paged_attn_prefill_append", st)
+    return out
+
+
+def paged_attn_decode_window(q, k_pool, v_pool, block_table, seq_lens, workspace, *, window: int, sinks: int = 0,
+                             scale: float = DEFAULT_SCALE, out=None, lse=None, split_tokens: int = 0,
+                             stream=None) -> torch.Tensor:
+    """paged_attn_decode over the first `sinks` and the last `window` tokens of each context.
+    Blocks without a visible token are not touched: their table entries may be -1.
+    seq_lens[b] = 0 marks a padded row (zeros out, lse -inf).  split_tokens: visible tokens per
+    CTA (multiple of 64), 0 = the library's choice."""
+    dev = q.device
+    _need(q, "q", torch.bfloat16, (None, NUM_Q_HEADS, HEAD_DIM), dev)
+    batch = q.shape[0]
+    _need(k_pool, "k_pool", torch.bfloat16, (None, BLOCK_SIZE, NUM_KV_HEADS, HEAD_DIM), dev)
+    _need(v_pool, "v_pool", torch.bfloat16, tuple(k_pool.shape), dev)
+    out = _need_decode(q, block_table, seq_lens, workspace, out, lse, dev)
+    with _on(dev):
+        st = load().paged_attn_decode_window(SHAPE, out.data_ptr(), _ptr(lse), q.data_ptr(), k_pool.data_ptr(),
+                                             v_pool.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+                                             k_pool.shape[0], seq_lens.data_ptr(), batch, window, sinks, scale,
+                                             split_tokens, workspace.data_ptr(), workspace.numel(), _stream(stream))
+    _check("paged_attn_decode_window", st)
+    return out
+
+
+def paged_attn_decode_window_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens, workspace, *,
+                                 window: int, sinks: int = 0, scale: float = DEFAULT_SCALE, out=None, lse=None,
+                                 split_tokens: int = 0, stream=None) -> torch.Tensor:
+    """paged_attn_decode_window over the 8-bit cache (split_tokens a multiple of 128)."""
+    dev = q.device
+    _need(q, "q", torch.bfloat16, (None, NUM_Q_HEADS, HEAD_DIM), dev)
+    batch = q.shape[0]
+    _need_fp8_cache(k_codes, v_codes, k_scale, v_scale, dev)
+    out = _need_decode(q, block_table, seq_lens, workspace, out, lse, dev)
+    with _on(dev):
+        st = load().paged_attn_decode_window_fp8(SHAPE, out.data_ptr(), _ptr(lse), q.data_ptr(), k_codes.data_ptr(),
+                                                 v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                                 block_table.data_ptr(), block_table.shape[1], k_codes.shape[0],
+                                                 seq_lens.data_ptr(), batch, window, sinks, scale, split_tokens,
+                                                 workspace.data_ptr(), workspace.numel(), _stream(stream))
+    _check("paged_attn_decode_window_fp8", st)
+    return out
+
+
+def _need_decode(q, block_table, seq_lens, workspace, out, lse, dev):
+    batch = q.shape[0]
+    _need(block_table, "block_table", torch.int32, (batch, None), dev)
+    _need(seq_lens, "seq_lens", torch.int32, (batch,), dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (batch, NUM_Q_HEADS), dev)
+    if out is None:
+        return torch.empty_like(q)
+    _need(out, "out", torch.bfloat16, tuple(q.shape), dev)
+    return out
+
+
+def paged_attn_prefill_window(q, k_pool, v_pool, block_table, cu_q_lens, seq_lens, max_q_len: int, workspace, *,
+                              window: int, sinks: int = 0, scale: float = DEFAULT_SCALE, out=None, lse=None,
+                              stream=None) -> torch.Tensor:
+    """paged_attn_prefill where every new token sees the first `sinks` tokens of its sequence and
+    the `window` ones up to itself.  Table entries of blocks that no new token sees may be -1."""
+    dev = q.device
+    _need(q, "q", torch.bfloat16, (None, NUM_Q_HEADS, HEAD_DIM), dev)
+    _need(k_pool, "k_pool", torch.bfloat16, (None, BLOCK_SIZE, NUM_KV_HEADS, HEAD_DIM), dev)
+    _need(v_pool, "v_pool", torch.bfloat16, tuple(k_pool.shape), dev)
+    _need(block_table, "block_table", torch.int32, (None, None), dev)
+    num_seqs = block_table.shape[0]
+    _need(cu_q_lens, "cu_q_lens", torch.int32, (num_seqs + 1,), dev)
+    _need(seq_lens, "seq_lens", torch.int32, (num_seqs,), dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (q.shape[0], NUM_Q_HEADS), dev)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _need(out, "out", torch.bfloat16, tuple(q.shape), dev)
+    with _on(dev):
+        st = load().paged_attn_prefill_window(SHAPE, out.data_ptr(), _ptr(lse), q.data_ptr(), k_pool.data_ptr(),
+                                              v_pool.data_ptr(), block_table.data_ptr(), block_table.shape[1],
+                                              k_pool.shape[0], cu_q_lens.data_ptr(), seq_lens.data_ptr(), num_seqs,
+                                              q.shape[0], max_q_len, window, sinks, scale, workspace.data_ptr(),
+                                              workspace.numel(), _stream(stream))
+    _check("paged_attn_prefill_window", st)
     return out
 
 

@@ -121,3 +121,69 @@ def test_the_rotation_written_out_keeps_lengths_and_relative_positions():
     c, _ = definitions.rotated(x, three, 1e6, [0] * 16 + [1] * 24 + [2] * 24)
     d, _ = definitions.rotated(x, p + 5, 1e6)
     assert torch.equal(c[..., 16:40], d[..., 16:40]) and not torch.allclose(c[..., 40:64], d[..., 40:64])
+
+
+def decode_args(p, fp8, **kw):
+    a = dict(shape=ops.SHAPE, out=p(0), lse=None, q=p(1), kp=p(2), vp=p(3), ks=p(4), vs=p(5), bt=p(6), w=1, nb=1, sl=p(7),
+             batch=1, window=4, sinks=1, scale=0.1, split=0, ws=p(8), ws_bytes=1 << 20, stream=None)
+    assert set(kw) <= set(a)
+    a.update(kw)
+    if not fp8:
+        del a["ks"], a["vs"]
+    return list(a.values())
+
+
+BAD_WINDOWS = [dict(window=0), dict(window=-1), dict(window=-(2 ** 31)), dict(sinks=-1), dict(scale=float("nan"))]
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("change", BAD_WINDOWS + [dict(split=100), dict(split=-64), dict(batch=-1), dict(batch=8193),
+                                                  dict(out=None), dict(ws=None), dict(ws_bytes=100), dict(w=0),
+                                                  dict(nb=0), dict(w=1 << 23), dict(sl=None)], ids=str)
+def test_decode_window_refuses(lib, change, fp8):
+    p = Addresses()
+    fn = lib.paged_attn_decode_window_fp8 if fp8 else lib.paged_attn_decode_window
+    assert fn(*decode_args(p, fp8, **change)) == 1
+    assert fn(*decode_args(p, fp8, shape=ops.pa_shape(32, 4, 128, 256))) == 2
+    assert fn(*decode_args(p, fp8, batch=0)) == 0
+    if fp8:
+        assert fn(*decode_args(p, fp8, split=64)) == 1
+        assert fn(*decode_args(p, fp8, ks=None)) == 1
+
+
+@pytest.mark.parametrize("change", BAD_WINDOWS + [dict(max_q=0), dict(max_q=5), dict(out=16), dict(q=None), dict(seqs=0),
+                                                  dict(ws_bytes=255)], ids=str)
+def test_prefill_window_refuses(lib, change):
+    p = Addresses()
+
+    def args(**kw):
+        a = dict(shape=ops.SHAPE, out=p(0), lse=None, q=p(1), kp=p(2), vp=p(3), bt=p(4), w=1, nb=1, cu=p(5), sl=p(6),
+                 seqs=1, tokens=4, max_q=4, window=4, sinks=1, scale=0.1, ws=p(7), ws_bytes=1024, stream=None)
+        a.update(kw)
+        return list(a.values())
+
+    if change.get("out"):
+        change = dict(out=p(0, change["out"]))
+    assert lib.paged_attn_prefill_window(*args(**change)) == 1
+    assert lib.paged_attn_prefill_window(*args(shape=ops.pa_shape(32, 4, 128, 256))) == 2
+    assert lib.paged_attn_prefill_window(*args(tokens=0, max_q=0)) == 0
+
+
+def test_the_window_written_out_is_full_attention_when_long():
+    g = torch.Generator().manual_seed(2)
+    q, k, v = torch.randn(3, 32, 128, generator=g), torch.randn(9, 8, 128, generator=g), torch.randn(9, 8, 128, generator=g)
+    full = torch.nn.functional.scaled_dot_product_attention(
+        q.double().transpose(0, 1), k.double().repeat_interleave(4, 1).transpose(0, 1),
+        v.double().repeat_interleave(4, 1).transpose(0, 1),
+        attn_mask=torch.ones(3, 9, dtype=torch.bool).tril(6)).transpose(0, 1)
+    scale = 128 ** -0.5
+    out, _ = definitions.window_attention(q, [k], [v], [3], [9], 100, 0, scale)
+    assert torch.allclose(out, full)
+    out, _ = definitions.window_attention(q, [k], [v], [3], [9], 1, 100, scale)
+    assert torch.allclose(out, full)
+    # a window of one token without sinks returns its value; with one sink, a mix of the two
+    out, _ = definitions.window_attention(q, [k], [v], [3], [9], 1, 0, scale)
+    assert torch.allclose(out, v[6:].double().repeat_interleave(4, 1))
+    out, _ = definitions.window_attention(q, [k], [v], [3], [9], 2, 1, scale)
+    few, _ = definitions.window_attention(q[1:2], [k[[0, 6, 7]]], [v[[0, 6, 7]]], [1], [3], 9, 0, scale)
+    assert torch.allclose(out[1:2], few)

@@ -7,7 +7,6 @@ if the library is missing or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -155,9 +154,16 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
-def _on(dev):
-    """Make dev current for a call (a launch goes to the current device), if it is not already."""
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+def _launch(fn, dev, stream, *args) -> int:
+    """fn(*args, stream) with dev current (a launch goes to the current device); the stream is
+    dev's current one unless given.  torch.cuda's own functions for this cost more host time
+    than a small kernel takes (3 us for the stream alone)."""
+    index = dev.index
+    stream = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        return fn(*args, stream)
+    with torch.cuda.device(index):
+        return fn(*args, stream)
 
 
 def _ptr(t) -> int | None:
@@ -165,6 +171,14 @@ def _ptr(t) -> int | None:
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape=None, device=None):
+    # the usual case first, in as few reads of the tensor as it takes
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and (device is None or t.device == device) and t.is_cuda
+            and t.is_contiguous()):
+        if shape is None:
+            return
+        got = t.shape
+        if got == shape or (shape[0] is None and got[1:] == shape[1:] and len(got) == len(shape)):
+            return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -283,6 +297,12 @@ def paged_qkv_append(x, w_qkv, k_pool, v_pool, block_table, cu_q_lens, seq_lens,
 
 
 ROPE_PAIRS = HEAD_DIM // 2
+_POOL = (None, BLOCK_SIZE, NUM_KV_HEADS, HEAD_DIM)
+
+
+def _need_pools(k_pool, v_pool):
+    _need(k_pool, "k_pool", torch.bfloat16, _POOL)
+    _need(v_pool, "v_pool", torch.bfloat16, k_pool.shape, k_pool.device)
 
 
 def rope_pair_axes(sections, interleaved: bool = False) -> bytes:
@@ -303,75 +323,73 @@ def rope_pair_axes(sections, interleaved: bool = False) -> bytes:
     return axes
 
 
-def _need_rows(t, name: str, heads: int, tokens, dev) -> int:
-    """The token stride (elements) of a [tokens, heads, 128] bf16 tensor whose rows are whole."""
+def _need_table(block_table, dev):
+    """(sequences, width) of a block table."""
+    _need(block_table, "block_table", torch.int32, None, dev)
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table must have 2 dims, got {tuple(block_table.shape)}")
+    return block_table.shape
+
+
+def _need_rows(t, name: str, shape, dev) -> int:
+    """The token stride (elements) of a bf16 tensor of that shape, [tokens, heads, 128], whose
+    tokens' rows are whole."""
+    row = shape[1] * HEAD_DIM
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} is on {t.device}, expected {dev}")
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != HEAD_DIM or (tokens is not None and t.shape[0] != tokens):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({tokens if tokens is not None else 'T'}, "
-                         f"{heads}, {HEAD_DIM})")
-    row = heads * HEAD_DIM
-    if t.shape[0] == 0:
-        return row
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     stride, head, dim = t.stride()
-    if t.shape[0] == 1:
+    if shape[0] <= 1:
         stride = row
-    if dim != 1 or head != HEAD_DIM or stride < row or stride % 8:
-        raise ValueError(f"{name}: each token's [{heads}, {HEAD_DIM}] must be contiguous and tokens a multiple of "
+    if shape[0] and (dim != 1 or head != HEAD_DIM or stride < row or stride % 8):
+        raise ValueError(f"{name}: each token's [{shape[1]}, {HEAD_DIM}] must be contiguous and tokens a multiple of "
                          f"8 elements apart, got strides {t.stride()}")
     return stride
 
 
-def _rope_append(fp8, q, k_new, v_new, cache, block_table, cu_q_lens, seq_lens, workspace, rope_theta, positions,
+def _rope_append(name, fn, q, k_new, v_new, cache, block_table, cu_q_lens, seq_lens, workspace, rope_theta, positions,
                  pair_axis, q_norm_weight, k_norm_weight, norm_eps, q_out, stream):
-    dev = q.device
-    q_stride = _need_rows(q, "q", NUM_Q_HEADS, None, dev)
+    """paged_rope_append over a cache whose tensors have been checked."""
+    dev = cache[0].device
     tokens = q.shape[0]
-    k_stride = _need_rows(k_new, "k_new", NUM_KV_HEADS, tokens, dev)
-    v_stride = _need_rows(v_new, "v_new", NUM_KV_HEADS, tokens, dev)
-    if fp8:
-        _need_fp8_cache(*cache, dev)
-    else:
-        _need(cache[0], "k_pool", torch.bfloat16, (None, BLOCK_SIZE, NUM_KV_HEADS, HEAD_DIM), dev)
-        _need(cache[1], "v_pool", torch.bfloat16, tuple(cache[0].shape), dev)
-    _need(block_table, "block_table", torch.int32, (None, None), dev)
-    num_seqs = block_table.shape[0]
+    q_shape = (tokens, NUM_Q_HEADS, HEAD_DIM)
+    kv_shape = (tokens, NUM_KV_HEADS, HEAD_DIM)
+    q_stride = _need_rows(q, "q", q_shape, dev)
+    k_stride = _need_rows(k_new, "k_new", kv_shape, dev)
+    v_stride = _need_rows(v_new, "v_new", kv_shape, dev)
+    num_seqs, width = _need_table(block_table, dev)
     _need(cu_q_lens, "cu_q_lens", torch.int32, (num_seqs + 1,), dev)
     _need(seq_lens, "seq_lens", torch.int32, (num_seqs,), dev)
     _need(workspace, "workspace", torch.uint8, None, dev)
     axes = 1
     if positions is not None:
-        if positions.dim() == 1:
-            _need(positions, "positions", torch.int32, (tokens,), dev)
-        else:
-            axes = positions.shape[0]
-            _need(positions, "positions", torch.int32, (axes, tokens), dev)
+        axes = positions.shape[0] if positions.dim() > 1 else 1
+        _need(positions, "positions", torch.int32, (axes, tokens) if positions.dim() > 1 else (tokens,), dev)
+        positions = positions.data_ptr()
     if pair_axis is not None:
         pair_axis = bytes(pair_axis)
         if len(pair_axis) != ROPE_PAIRS:
             raise ValueError(f"pair_axis must name {ROPE_PAIRS} axes")
-    if (q_norm_weight is None) != (k_norm_weight is None):
-        raise ValueError("QK-norm takes both q_norm_weight and k_norm_weight")
-    if q_norm_weight is not None:
+    if q_norm_weight is not None and k_norm_weight is not None:
         _need(q_norm_weight, "q_norm_weight", torch.bfloat16, (HEAD_DIM,), dev)
         _need(k_norm_weight, "k_norm_weight", torch.bfloat16, (HEAD_DIM,), dev)
+        q_norm_weight, k_norm_weight = q_norm_weight.data_ptr(), k_norm_weight.data_ptr()
+    elif q_norm_weight is not None or k_norm_weight is not None:
+        raise ValueError("QK-norm takes both q_norm_weight and k_norm_weight")
     if q_out is None:
-        q_out = torch.empty((tokens, NUM_Q_HEADS, HEAD_DIM), dtype=torch.bfloat16, device=dev)
+        q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
     else:
-        _need(q_out, "q_out", torch.bfloat16, (tokens, NUM_Q_HEADS, HEAD_DIM), dev)
-    lib = load()
-    fn = lib.paged_rope_append_fp8 if fp8 else lib.paged_rope_append
-    with _on(dev):
-        st = fn(SHAPE, rope_theta, _ptr(positions), axes, pair_axis, _ptr(q_norm_weight), _ptr(k_norm_weight),
-                norm_eps, q_out.data_ptr(), q.data_ptr(), q_stride, k_new.data_ptr(), k_stride, v_new.data_ptr(),
-                v_stride, *[t.data_ptr() for t in cache], block_table.data_ptr(), block_table.shape[1],
-                cache[0].shape[0], cu_q_lens.data_ptr(), seq_lens.data_ptr(), num_seqs, tokens,
-                workspace.data_ptr(), workspace.numel(), _stream(stream))
-    _check("paged_rope_append_fp8" if fp8 else "paged_rope_append", st)
+        _need(q_out, "q_out", torch.bfloat16, q_shape, dev)
+    _check(name, _launch(fn, dev, stream, SHAPE, rope_theta, positions, axes, pair_axis, q_norm_weight, k_norm_weight,
+                         norm_eps, q_out.data_ptr(), q.data_ptr(), q_stride, k_new.data_ptr(), k_stride,
+                         v_new.data_ptr(), v_stride, *[t.data_ptr() for t in cache], block_table.data_ptr(), width,
+                         cache[0].shape[0], cu_q_lens.data_ptr(), seq_lens.data_ptr(), num_seqs, tokens,
+                         workspace.data_ptr(), workspace.numel()))
     return q_out
 
 
@@ -385,8 +403,10 @@ def paged_rope_append(q, k_new, v_new, k_pool, v_pool, block_table, cu_q_lens, s
     positions (int32 [T] or [axes, T]) replace the cache positions in the rotation; with several
     axes, pair_axis (rope_pair_axes) names the axis of each of the 64 pairs.  q_out may be q
     itself.  Tokens behind the last sequence are left alone."""
-    return _rope_append(False, q, k_new, v_new, (k_pool, v_pool), block_table, cu_q_lens, seq_lens, workspace,
-                        rope_theta, positions, pair_axis, q_norm_weight, k_norm_weight, norm_eps, q_out, stream)
+    _need_pools(k_pool, v_pool)
+    return _rope_append("paged_rope_append", load().paged_rope_append, q, k_new, v_new, (k_pool, v_pool), block_table,
+                        cu_q_lens, seq_lens, workspace, rope_theta, positions, pair_axis, q_norm_weight, k_norm_weight,
+                        norm_eps, q_out, stream)
 
 
 def paged_rope_append_fp8(q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, block_table, cu_q_lens, seq_lens,
@@ -395,9 +415,11 @@ def paged_rope_append_fp8(q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, b
                           stream=None) -> torch.Tensor:
     """paged_rope_append into the 8-bit cache (fp8_cache): k rows quantised from their rotated
     fp32 values, v rows as kv_append_fp8 does."""
-    return _rope_append(True, q, k_new, v_new, (k_codes, v_codes, k_scale, v_scale), block_table, cu_q_lens,
-                        seq_lens, workspace, rope_theta, positions, pair_axis, q_norm_weight, k_norm_weight,
-                        norm_eps, q_out, stream)
+    _need(k_codes, "k_codes", torch.uint8, _POOL)
+    _need_fp8_cache(k_codes, v_codes, k_scale, v_scale, k_codes.device)
+    return _rope_append("paged_rope_append_fp8", load().paged_rope_append_fp8, q, k_new, v_new,
+                        (k_codes, v_codes, k_scale, v_scale), block_table, cu_q_lens, seq_lens, workspace, rope_theta,
+                        positions, pair_axis, q_norm_weight, k_norm_weight, norm_eps, q_out, stream)
 
 
 def paged_attn_decode(q, k_pool, v_pool, block_table, seq_lens, workspace, *,
@@ -720,18 +742,14 @@ def paged_attn_decode_window(q, k_pool, v_pool, block_table, seq_lens, workspace
     Blocks without a visible token are not touched: their table entries may be -1.
     seq_lens[b] = 0 marks a padded row (zeros out, lse -inf).  split_tokens: visible tokens per
     CTA (multiple of 64), 0 = the library's choice."""
-    dev = q.device
-    _need(q, "q", torch.bfloat16, (None, NUM_Q_HEADS, HEAD_DIM), dev)
-    batch = q.shape[0]
-    _need(k_pool, "k_pool", torch.bfloat16, (None, BLOCK_SIZE, NUM_KV_HEADS, HEAD_DIM), dev)
-    _need(v_pool, "v_pool", torch.bfloat16, tuple(k_pool.shape), dev)
+    _need_pools(k_pool, v_pool)
+    dev = k_pool.device
     out = _need_decode(q, block_table, seq_lens, workspace, out, lse, dev)
-    with _on(dev):
-        st = load().paged_attn_decode_window(SHAPE, out.data_ptr(), _ptr(lse), q.data_ptr(), k_pool.data_ptr(),
-                                             v_pool.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-                                             k_pool.shape[0], seq_lens.data_ptr(), batch, window, sinks, scale,
-                                             split_tokens, workspace.data_ptr(), workspace.numel(), _stream(stream))
-    _check("paged_attn_decode_window", st)
+    _check("paged_attn_decode_window",
+           _launch(load().paged_attn_decode_window, dev, stream, SHAPE, out.data_ptr(), _ptr(lse), q.data_ptr(),
+                   k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), block_table.shape[1], k_pool.shape[0],
+                   seq_lens.data_ptr(), q.shape[0], window, sinks, scale, split_tokens, workspace.data_ptr(),
+                   workspace.numel()))
     return out
 
 
@@ -739,24 +757,23 @@ def paged_attn_decode_window_fp8(q, k_codes, v_codes, k_scale, v_scale, block_ta
                                  window: int, sinks: int = 0, scale: float = DEFAULT_SCALE, out=None, lse=None,
                                  split_tokens: int = 0, stream=None) -> torch.Tensor:
     """paged_attn_decode_window over the 8-bit cache (split_tokens a multiple of 128)."""
-    dev = q.device
-    _need(q, "q", torch.bfloat16, (None, NUM_Q_HEADS, HEAD_DIM), dev)
-    batch = q.shape[0]
+    _need(k_codes, "k_codes", torch.uint8, _POOL)
+    dev = k_codes.device
     _need_fp8_cache(k_codes, v_codes, k_scale, v_scale, dev)
     out = _need_decode(q, block_table, seq_lens, workspace, out, lse, dev)
-    with _on(dev):
-        st = load().paged_attn_decode_window_fp8(SHAPE, out.data_ptr(), _ptr(lse), q.data_ptr(), k_codes.data_ptr(),
-                                                 v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                                 block_table.data_ptr(), block_table.shape[1], k_codes.shape[0],
-                                                 seq_lens.data_ptr(), batch, window, sinks, scale, split_tokens,
-                                                 workspace.data_ptr(), workspace.numel(), _stream(stream))
-    _check("paged_attn_decode_window_fp8", st)
+    _check("paged_attn_decode_window_fp8",
+           _launch(load().paged_attn_decode_window_fp8, dev, stream, SHAPE, out.data_ptr(), _ptr(lse), q.data_ptr(),
+                   k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                   block_table.data_ptr(), block_table.shape[1], k_codes.shape[0], seq_lens.data_ptr(), q.shape[0],
+                   window, sinks, scale, split_tokens, workspace.data_ptr(), workspace.numel()))
     return out
 
 
 def _need_decode(q, block_table, seq_lens, workspace, out, lse, dev):
+    _need(q, "q", torch.bfloat16, (None, NUM_Q_HEADS, HEAD_DIM), dev)
     batch = q.shape[0]
-    _need(block_table, "block_table", torch.int32, (batch, None), dev)
+    if _need_table(block_table, dev)[0] != batch:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, dim 0 must be {batch}")
     _need(seq_lens, "seq_lens", torch.int32, (batch,), dev)
     _need(workspace, "workspace", torch.uint8, None, dev)
     if lse is not None:
@@ -772,12 +789,10 @@ def paged_attn_prefill_window(q, k_pool, v_pool, block_table, cu_q_lens, seq_len
                               stream=None) -> torch.Tensor:
     """paged_attn_prefill where every new token sees the first `sinks` tokens of its sequence and
     the `window` ones up to itself.  Table entries of blocks that no new token sees may be -1."""
-    dev = q.device
+    _need_pools(k_pool, v_pool)
+    dev = k_pool.device
     _need(q, "q", torch.bfloat16, (None, NUM_Q_HEADS, HEAD_DIM), dev)
-    _need(k_pool, "k_pool", torch.bfloat16, (None, BLOCK_SIZE, NUM_KV_HEADS, HEAD_DIM), dev)
-    _need(v_pool, "v_pool", torch.bfloat16, tuple(k_pool.shape), dev)
-    _need(block_table, "block_table", torch.int32, (None, None), dev)
-    num_seqs = block_table.shape[0]
+    num_seqs, width = _need_table(block_table, dev)
     _need(cu_q_lens, "cu_q_lens", torch.int32, (num_seqs + 1,), dev)
     _need(seq_lens, "seq_lens", torch.int32, (num_seqs,), dev)
     _need(workspace, "workspace", torch.uint8, None, dev)
@@ -786,14 +801,12 @@ def paged_attn_prefill_window(q, k_pool, v_pool, block_table, cu_q_lens, seq_len
     if out is None:
         out = torch.empty_like(q)
     else:
-        _need(out, "out", torch.bfloat16, tuple(q.shape), dev)
-    with _on(dev):
-        st = load().paged_attn_prefill_window(SHAPE, out.data_ptr(), _ptr(lse), q.data_ptr(), k_pool.data_ptr(),
-                                              v_pool.data_ptr(), block_table.data_ptr(), block_table.shape[1],
-                                              k_pool.shape[0], cu_q_lens.data_ptr(), seq_lens.data_ptr(), num_seqs,
-                                              q.shape[0], max_q_len, window, sinks, scale, workspace.data_ptr(),
-                                              workspace.numel(), _stream(stream))
-    _check("paged_attn_prefill_window", st)
+        _need(out, "out", torch.bfloat16, q.shape, dev)
+    _check("paged_attn_prefill_window",
+           _launch(load().paged_attn_prefill_window, dev, stream, SHAPE, out.data_ptr(), _ptr(lse), q.data_ptr(),
+                   k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), width, k_pool.shape[0],
+                   cu_q_lens.data_ptr(), seq_lens.data_ptr(), num_seqs, q.shape[0], max_q_len, window, sinks, scale,
+                   workspace.data_ptr(), workspace.numel()))
     return out
 
 

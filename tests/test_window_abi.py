@@ -98,9 +98,9 @@ def test_rope_pair_axes():
 def test_the_binding_refuses_wrong_rows():
     t = torch.zeros(2, 32, 128, dtype=torch.bfloat16)
     with pytest.raises(TypeError):
-        ops._need_rows(t.float(), "q", 32, None, t.device)
+        ops._need_rows(t.float(), "q", (2, 32, 128), t.device)
     with pytest.raises(ValueError):
-        ops._need_rows(t, "q", 32, None, t.device)            # not a CUDA tensor
+        ops._need_rows(t, "q", (2, 32, 128), t.device)        # not a CUDA tensor
 
 
 def test_the_rotation_written_out_keeps_lengths_and_relative_positions():

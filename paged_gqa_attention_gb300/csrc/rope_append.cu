@@ -20,9 +20,15 @@
 //     both dims of 8 rotation pairs, so only the sum of squares (and the 8-bit row's maximum)
 //     crosses lanes, in 3 shuffles for the 4 heads that a warp instruction covers, and every
 //     access is 16 bytes a lane, 128 contiguous bytes a row half;
-//   * a unit of work is a token and some of its 6 groups of 8 heads (4 of q, k, v).  With many
-//     tokens a warp takes all 6, so that the token's lookup and angles are computed once; with
-//     few a warp takes one, so that a token's rows are in flight at the same time.
+//   * a token's 48 heads are 6 groups of 8 (4 of q, k, v).  The batch's groups, in token order,
+//     are cut into one even run per resident warp: a warp looks its token up and computes its
+//     angles when the run enters it, so few tokens spread over warps group by group, and many
+//     leave no SM idle at the end.  (A warp per token took 26.1 us for 4096 tokens into the 8-bit
+//     cache, 4096 tokens on 3648 warps being two rounds; even runs take 19.5 us.)
+// Measured in a graph of calls: 1 token 2.0 us (three dependent loads and a launch), 128 tokens
+// into the 8-bit cache 2.9 us, 4096 tokens into it 19.5 us (92 MB: 4.7 TB/s; the quotients and
+// row maxima hold the warps up), 16381 tokens into the bf16 cache 65.5 us (403 MB: 6.1 TB/s,
+// 92 % of the measured copy rate).
 #include "common.cuh"
 #include "launch.h"
 #include "tokens.cuh"
@@ -32,7 +38,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 3;          // up to 80 registers a thread
+constexpr int kCtasPerSm = 2;          // up to 128 registers a thread; 3 (80, spilling) was slower
 constexpr int kQGroups = kHq / 8;      // groups of 8 heads: 0-3 q, 4 k, 5 v
 constexpr int kGroups = kQGroups + 2;
 constexpr float kPosLimit = 16777216.f;   // positions are exact in fp32 below 2^24
@@ -47,28 +53,51 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
                       pack_bf16x2(x[6], x[7]));
 }
 
+// The fp32 quotient x / s, correctly rounded, from r = 1 / s (correctly rounded): an approximate
+// quotient and one correction by its exact remainder (Markstein 1990, IBM J. Res. Dev. 34(1)).
+// The signs are arranged so that a zero keeps x's.  For s far from overflow and underflow; where
+// the remainder underflows, x / s is far below half the smallest code.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(q, s, -x), -r, q);
+}
+
 // E4M3 codes of 8 values: the fp32 quotient by the row's scale, rounded to nearest even (the
 // rule of kv_append_fp8).
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], float scale) {
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, float r) {
+    float q[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = quotient(x[e], s, r);
     uint2 c;
-    c.x = f32x2_to_e4m3x2(__fdiv_rn(x[0], scale), __fdiv_rn(x[1], scale)) |
-          f32x2_to_e4m3x2(__fdiv_rn(x[2], scale), __fdiv_rn(x[3], scale)) << 16;
-    c.y = f32x2_to_e4m3x2(__fdiv_rn(x[4], scale), __fdiv_rn(x[5], scale)) |
-          f32x2_to_e4m3x2(__fdiv_rn(x[6], scale), __fdiv_rn(x[7], scale)) << 16;
+    c.x = f32x2_to_e4m3x2(q[0], q[1]) | f32x2_to_e4m3x2(q[2], q[3]) << 16;
+    c.y = f32x2_to_e4m3x2(q[4], q[5]) | f32x2_to_e4m3x2(q[6], q[7]) << 16;
     return c;
 }
 
 // One K or V row half-pair of this lane into the 8-bit cache.
-__device__ __forceinline__ void store_row8(uint8_t *codes, float *scale_slot, int j, const float (&lo)[8],
-                                           const float (&hi)[8]) {
+__device__ __forceinline__ void store_row8(uint8_t *codes, float *scale_slot, int j, float (&lo)[8], float (&hi)[8]) {
     float amax = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) amax = fmax3(amax, fabsf(lo[e]), fabsf(hi[e]));
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
     const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
-    *reinterpret_cast<uint2 *>(codes + 8 * j) = codes8(lo, scale);
-    *reinterpret_cast<uint2 *>(codes + kD / 2 + 8 * j) = codes8(hi, scale);
+    // a row of extreme values is brought to the middle of the exponents first, which changes no
+    // quotient; by an infinite scale every finite value gives 0 (s = r = 0 below), inf gives NaN
+    float s = scale;
+    if (!(scale >= 0x1p-100f && scale <= 0x1p100f)) {
+        const float k = scale < 1.f ? 0x1p64f : 0x1p-64f;
+        s *= k;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            lo[e] *= k;
+            hi[e] *= k;
+        }
+    }
+    const float r = __frcp_rn(s);
+    if (r == 0.f) s = 0.f;
+    *reinterpret_cast<uint2 *>(codes + 8 * j) = codes8(lo, s, r);
+    *reinterpret_cast<uint2 *>(codes + kD / 2 + 8 * j) = codes8(hi, s, r);
     if (j == 0) *scale_slot = scale;
 }
 
@@ -117,7 +146,7 @@ __device__ __forceinline__ Place place_of(const RopeAppendArgs &a, int t, int la
 
 template <bool kFp8, bool kNorm>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
-rope_append_kernel(const __grid_constant__ RopeAppendArgs a, int groups_per_warp) {
+rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
     // The next kernel on the stream may start its prologue; it waits for this one to complete
     // before it reads q_out or the cache.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -138,20 +167,41 @@ rope_append_kernel(const __grid_constant__ RopeAppendArgs a, int groups_per_warp
         record_error(a.err, kErrDevice | kErrBadCuQ);
     __syncthreads();
 
-    const int chunks = (kGroups + groups_per_warp - 1) / groups_per_warp;
-    const long long work = (long long)a.total_tokens * chunks;
-    const long long step = (long long)gridDim.x * kWarps;
+    const long long groups = (long long)a.total_tokens * kGroups;
+    const long long warps = (long long)gridDim.x * kWarps;
+    const long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const long long run_end = groups * (w + 1) / warps;
+    long long at = groups * w / warps;
     bool waited = false;
-    for (long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); w < work; w += step) {
-        const int tok = (int)(w / chunks);
-        const int g0 = (int)(w % chunks) * groups_per_warp;
-        const int g1 = min(kGroups, g0 + groups_per_warp);
-        const Place pl = place_of(a, tok, lane, lane == 0 && g0 == 0);
+    while (at < run_end) {
+        const int tok = (int)(at / kGroups);
+        const int g0 = (int)(at - (long long)tok * kGroups);
+        const int g1 = (int)min((long long)kGroups, run_end - (long long)tok * kGroups);
+        at = (long long)tok * kGroups + g1;
+        const Place pl = place_of(a, tok, lane, lane == 0);
         // q, k_new, v_new, positions and gains may come from the kernel just before this one,
         // which may also still read the cache rows and q_out written here
         if (!waited) asm volatile("griddepcontrol.wait;" ::: "memory");
         waited = true;
         if (!pl.live) continue;
+
+        // heads hs and 4 + hs of group g: the next group's rows are on their way while one is
+        // computed, the first one's while the angles are
+        uint4 n_lo[2], n_hi[2];
+        const auto fetch = [&](int g) {
+            const bool is_v = g == kGroups - 1;
+            const __nv_bfloat16 *src =
+                g < kQGroups ? static_cast<const __nv_bfloat16 *>(a.q) + (size_t)tok * a.q_stride + g * 8 * kD
+                             : static_cast<const __nv_bfloat16 *>(is_v ? a.v_new : a.k_new) +
+                                   (size_t)tok * (is_v ? a.v_stride : a.k_stride);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint4 *r = reinterpret_cast<const uint4 *>(src + (4 * u + hs) * kD) + j;
+                n_lo[u] = r[0];
+                n_hi[u] = r[kD / 16];
+            }
+        };
+        fetch(g0);
 
         // cos and sin of this lane's 8 pairs (8j .. 8j+7)
         float c[8], s[8];
@@ -164,7 +214,7 @@ rope_append_kernel(const __grid_constant__ RopeAppendArgs a, int groups_per_warp
                                    : (float)pl.pos;
             if (a.positions) {
                 known = fabsf(p[0]) < kPosLimit && fabsf(p[1]) < kPosLimit && fabsf(p[2]) < kPosLimit;
-                if (!known && lane == 0 && g0 == 0) record_error(a.err, kErrDevice | kErrBadPosition);
+                if (!known && lane == 0) record_error(a.err, kErrDevice | kErrBadPosition);
             } else {
                 known = pl.pos >= 0;
             }
@@ -184,17 +234,8 @@ rope_append_kernel(const __grid_constant__ RopeAppendArgs a, int groups_per_warp
         for (int g = g0; g < g1; ++g) {
             const bool is_q = g < kQGroups, is_v = g == kGroups - 1;
             if (!is_q && !store_kv) break;
-            const __nv_bfloat16 *src =
-                is_q ? static_cast<const __nv_bfloat16 *>(a.q) + (size_t)tok * a.q_stride + g * 8 * kD
-                     : static_cast<const __nv_bfloat16 *>(is_v ? a.v_new : a.k_new) +
-                           (size_t)tok * (is_v ? a.v_stride : a.k_stride);
-            uint4 w_lo[2], w_hi[2];       // heads hs and 4 + hs of the group
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const uint4 *r = reinterpret_cast<const uint4 *>(src + (4 * u + hs) * kD) + j;
-                w_lo[u] = r[0];
-                w_hi[u] = r[kD / 16];
-            }
+            const uint4 w_lo[2] = {n_lo[0], n_lo[1]}, w_hi[2] = {n_hi[0], n_hi[1]};
+            if (g + 1 < g1) fetch(g + 1);
             __nv_bfloat16 *dst =
                 is_q ? static_cast<__nv_bfloat16 *>(a.q_out) + ((size_t)tok * kHq + g * 8) * kD
                      : static_cast<__nv_bfloat16 *>(is_v ? a.v_pool : a.k_pool) + pl.row * (kHkv * kD);
@@ -283,10 +324,7 @@ rope_append_kernel(const __grid_constant__ RopeAppendArgs a, int groups_per_warp
 cudaError_t launch_rope_append(const RopeAppendArgs &a, int num_sms, cudaStream_t stream) {
     if (a.total_tokens == 0) return cudaSuccess;
     const long long ctas = (long long)num_sms * kCtasPerSm;
-    const long long resident = ctas * kWarps;   // warps in one wave
-    const int groups_per_warp = (long long)a.total_tokens * kGroups > 2 * resident ? kGroups : 1;
-    const long long work = (long long)a.total_tokens * ((kGroups + groups_per_warp - 1) / groups_per_warp);
-    const long long need = (work + kWarps - 1) / kWarps;
+    const long long need = ((long long)a.total_tokens * kGroups + kWarps - 1) / kWarps;   // a warp per group
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -297,10 +335,10 @@ cudaError_t launch_rope_append(const RopeAppendArgs &a, int num_sms, cudaStream_
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (a.k_scale)
-        return a.q_norm ? cudaLaunchKernelEx(&cfg, rope_append_kernel<true, true>, a, groups_per_warp)
-                        : cudaLaunchKernelEx(&cfg, rope_append_kernel<true, false>, a, groups_per_warp);
-    return a.q_norm ? cudaLaunchKernelEx(&cfg, rope_append_kernel<false, true>, a, groups_per_warp)
-                    : cudaLaunchKernelEx(&cfg, rope_append_kernel<false, false>, a, groups_per_warp);
+        return a.q_norm ? cudaLaunchKernelEx(&cfg, rope_append_kernel<true, true>, a)
+                        : cudaLaunchKernelEx(&cfg, rope_append_kernel<true, false>, a);
+    return a.q_norm ? cudaLaunchKernelEx(&cfg, rope_append_kernel<false, true>, a)
+                    : cudaLaunchKernelEx(&cfg, rope_append_kernel<false, false>, a);
 }
 
 }  // namespace pa

@@ -297,3 +297,28 @@ def test_on_a_side_stream_and_in_a_graph():
         assert torch.equal(out, want)
         assert torch.equal(pools[0].view(torch.int16), b.k_pool.view(torch.int16))
     ops.check_error(ws)
+
+
+def test_8_bit_rows_of_extreme_and_odd_values_are_those_of_kv_append_fp8():
+    """v rows (and k rows without norm or rotation) from the smallest to the largest bf16, with
+    signed zeros, infinities and NaN: the same codes and scales as kv_append_fp8, bit for bit."""
+    t = 400
+    b = batch_of([t], [t])
+    g = torch.Generator(device="cuda")
+    g.manual_seed(111)
+    x = torch.randn(t, 6144, generator=g, device="cuda")
+    x = x.view(t, 48, 128) * torch.exp2(torch.randint(-132, 127, (t, 48, 1), generator=g, device="cuda").float())
+    x[:, :, ::7] *= 2.0 ** -9
+    x[:, :, 3], x[:, :, 4] = 0.0, -0.0
+    x = x.to(torch.bfloat16)
+    x[5, :, 9], x[6, :, 9], x[7, :, 9] = float("inf"), float("-inf"), float("nan")
+    x[8] = 0.0
+    x[9] = -0.0
+    q, k, v = x[:, :32], x[:, 32:40], x[:, 40:]
+    ws = ops.make_workspace(1, b.max_blocks_per_seq)
+    got, want = ops.fp8_cache(b.num_blocks), ops.fp8_cache(b.num_blocks)
+    ops.paged_rope_append_fp8(q, k, v, *got, b.block_table, b.cu_q_lens, b.seq_lens, ws, rope_theta=0.0)
+    ops.kv_append_fp8(*want, k.contiguous(), v.contiguous(), b.block_table, b.cu_q_lens, b.seq_lens, ws)
+    ops.check_error(ws)
+    for a, c in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), c.view(torch.uint8))

@@ -964,8 +964,11 @@ static pa_status prefill_impl(pa_shape shape, void *out, float *lse, const void 
     if (sms <= 0) return PA_ERR_CUDA;
     if (!get_encoder()) return PA_ERR_CUDA;
     CUtensorMap q_map, k_map, v_map, kn_map, vn_map;
-    if (!encode_q_map(&q_map, q, total_tokens) || !encode_pool_map(&k_map, k_pool, num_blocks, kPrefillKvTile) ||
-        !encode_pool_map(&v_map, v_pool, num_blocks, kPrefillKvTile))
+    const int box = win ? 64 : kPrefillKvTile;
+    if (!encode_q_map(&q_map, q, total_tokens) || !encode_pool_map(&k_map, k_pool, num_blocks, box) ||
+        !encode_pool_map(&v_map, v_pool, num_blocks, box))
+        return PA_ERR_INVALID_ARG;
+    if (win && (!encode_pool_map(&kn_map, k_pool, num_blocks, 16) || !encode_pool_map(&vn_map, v_pool, num_blocks, 16)))
         return PA_ERR_INVALID_ARG;
     if (k_new && (!encode_new_rows_map(&kn_map, k_new, total_tokens) || !encode_new_rows_map(&vn_map, v_new, total_tokens)))
         return PA_ERR_INVALID_ARG;
@@ -998,7 +1001,7 @@ static pa_status prefill_impl(pa_shape shape, void *out, float *lse, const void 
     if (plan_units > 0 && workspace_bytes >= kPartialOffset + (size_t)plan_units * sizeof(int32_t))
         a.order = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + kPartialOffset);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = win     ? launch_prefill_window(a, q_map, k_map, v_map, sms, st)
+    const cudaError_t e = win     ? launch_prefill_window(a, q_map, k_map, v_map, kn_map, vn_map, sms, st)
                           : k_new ? launch_prefill_append(a, q_map, k_map, v_map, kn_map, vn_map, sms, st)
                                   : launch_prefill(a, q_map, k_map, v_map, sms, st);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;

@@ -211,9 +211,10 @@ cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map,
                            const CUtensorMap &k_map, const CUtensorMap &v_map, int num_sms,
                            cudaStream_t stream);
 
-// a.window set.
+// a.window set; k_map / v_map with boxes of 64 rows, k16_map / v16_map of 16.
 cudaError_t launch_prefill_window(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
-                                  const CUtensorMap &v_map, int num_sms, cudaStream_t stream);
+                                  const CUtensorMap &v_map, const CUtensorMap &k16_map, const CUtensorMap &v16_map,
+                                  int num_sms, cudaStream_t stream);
 
 // The prefill with the append of the new tokens fused in (a.k_new set): kn_map / vn_map are
 // 3-D maps (dim, head, token) over k_new / v_new with box {64, 1, 128}.

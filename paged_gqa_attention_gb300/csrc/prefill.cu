@@ -39,8 +39,11 @@
 // max and, only when it grows by more than 2^8, rescales O (lazy rescaling); the row
 // sum accumulates the same bf16-rounded weights the PV product uses.
 // The sliding-window form (kWindow: each query sees the first `sinks` tokens and the `window`
-// ones up to itself) visits the key tiles that any of the unit's 64 positions sees -- those of
-// the sinks, then those of the window -- and masks at most the first and last of each.
+// ones up to itself) takes the keys that any of the unit's 64 positions sees, in groups of 16
+// rows, as one list -- the sinks, then the window -- and cuts that into tiles of 128 rows,
+// fetched in boxes of 64 and 16 rows: a few sinks cost a few rows, not a tile, and the window
+// starts where it starts.  (Tiles at multiples of 128 positions, the sinks' apart, were two more
+// a unit.)  Only tiles at the two ends of the window and the sinks' are masked.
 // Every wait is bounded; on expiry the CTA records PA_ERR_TIMEOUT, unwinds, waits
 // (bounded) for its own copies and MMAs, frees tensor memory and exits.
 #include "common.cuh"
@@ -109,17 +112,9 @@ struct Unit {
     int c0;
     int n_old;
     int tok_base;
-    // Sliding window: the tiles visited are n_sink tiles from 0, then those from w0 on; keys in
-    // [s_end, lo) are seen by none of the unit's queries.
-    int s_end, lo, n_sink, w0;
+    // Sliding window: key tile j holds rows 128j .. 128j + 127 of this list.
+    WindowRows win;
 };
-
-// Key tile visited at step j of a unit.
-template <bool kWindow>
-__device__ __forceinline__ int key_tile(const Unit &t, int j) {
-    if constexpr (kWindow) return j < t.n_sink ? j : t.w0 + (j - t.n_sink);
-    else return t.kt0 + j;
-}
 
 // Position of row 0 of key tile jg and the bound past which its rows are not keys.
 __device__ __forceinline__ void key_tile_span(const Unit &t, int jg, int &base, int &limit) {
@@ -166,12 +161,8 @@ __device__ __forceinline__ Unit unit_at(const PrefillArgs &a, int idx, int qbloc
         t.n_old = t.n_kt;
     }
     if constexpr (kWindow) {
-        const WindowTiles<kKT> wt(a.window, a.sinks, t.pos0, t.pos0 + t.positions - 1);
-        t.s_end = wt.s;
-        t.lo = wt.lo;
-        t.n_sink = wt.n_sink;
-        t.w0 = wt.w0;
-        t.n_kt = wt.n;
+        t.win.set(a.window, a.sinks, t.pos0, t.pos0 + t.positions - 1);
+        t.n_kt = (t.win.rows + kKT - 1) / kKT;
     }
     return t;
 }
@@ -303,6 +294,36 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
     }
 }
 
+// Sliding window: fetch rows c0 .. c0 + 127 of the unit's key list into a tile, as boxes of 64
+// and 16 rows that end at the block's edge or with the sinks.  Rows whose group of 16 lies past
+// the context are not fetched (they are masked, and their V rows zeroed by the softmax warps).
+__device__ __forceinline__ void load_list_tile(const PrefillArgs &a, const Unit &t, const int32_t *bt, int c0,
+                                               uint8_t (*dst)[kHalf], uint32_t bar, const CUtensorMap *map64,
+                                               const CUtensorMap *map16, bool report) {
+    const int rows = min(kKT, ((t.seq_len - t.win.shift + 15) & ~15) - c0);
+    mbar_arrive_expect_tx(bar, (uint32_t)rows * kRowBytes);
+    for (int r = 0; r < rows;) {
+        const int p = t.win.position(c0 + r);
+        int run = min(rows - r, kBlock - p % kBlock);
+        if (c0 + r < t.win.s16) run = min(run, t.win.s16 - c0 - r);
+        int blk = __ldg(bt + p / kBlock);
+        if (blk < 0 || blk >= a.num_blocks) {
+            if (report) record_error(a.err, kErrDevice | kErrBadBlock);
+            blk = 0;   // stay inside the pool; the result is flagged as invalid
+        }
+        int off = p % kBlock;
+        while (run > 0) {
+            const CUtensorMap *m = run >= 64 ? map64 : map16;
+            const int n = run >= 64 ? 64 : 16;
+            tma_load_4d(smem_u32(dst[0] + r * 128), m, bar, 0, t.g, off, blk);
+            tma_load_4d(smem_u32(dst[1] + r * 128), m, bar, 64, t.g, off, blk);
+            r += n;
+            off += n;
+            run -= n;
+        }
+    }
+}
+
 // The fused append's warp: this CTA's share of the new tokens' K and V rows (2 KiB each, all
 // 8 KV heads) copied into their cache slots by the kv_append rule, two tokens at a time with
 // 16-byte accesses.  Nothing in this kernel reads those slots (the attention takes the new
@@ -426,10 +447,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
             if (qk) {
                 tma_prefetch_map(&q_map);
                 tma_prefetch_map(&k_map);
-                if constexpr (kAppend) tma_prefetch_map(&kn_map);
+                if constexpr (kAppend || kWindow) tma_prefetch_map(&kn_map);
             } else {
                 tma_prefetch_map(&v_map);
-                if constexpr (kAppend) tma_prefetch_map(&vn_map);
+                if constexpr (kAppend || kWindow) tma_prefetch_map(&vn_map);
             }
         }
         // The pools may be written by the kernel just before this one on the stream
@@ -468,7 +489,18 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
             const int32_t *bt = a.block_table + (size_t)t.s * a.max_blocks_per_seq;
             for (int j = 0; j < t.n_kt; ++j, ++it) {
                 const int st = it % ns;
-                const int jg = key_tile<kWindow>(t, j);   // key tile within the context
+                const int jg = t.kt0 + j;              // key tile within the context
+                if constexpr (kWindow) {
+                    if (it >= ns &&
+                        !(ok = __all_sync(0xffffffffu, wait_or_abort(smem_u32(&empty[st]), ((it / ns) - 1) & 1,
+                                                                    abort_flag, a.err))))
+                        break;
+                    if (leader) load_list_tile(a, t, bt, jg * kKT, qk ? sm.k[st] : sm.v[st], smem_u32(&full[st]), map,
+                                               new_map, qk);
+                    __syncwarp();
+                    ++kv_issued;
+                    continue;
+                }
                 const bool cache_tile = !kAppend || jg < t.n_old;
                 int blk = cache_tile ? __ldg(bt + (jg >> 1)) : 0;
                 if (blk < 0 || blk >= a.num_blocks) {
@@ -660,8 +692,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 // mask of the keys past each row's last visible key and of the tile's rows that
                 // are no keys (past its span; only on tiles reaching past either) and the row
                 // maximum of the raw scores
-                const int jg = key_tile<kWindow>(t, j);    // key tile within the context
+                const int jg = t.kt0 + j;                  // key tile within the context
                 int base = jg * kKT, kv_valid = t.seq_len - jg * kKT;   // rows 0 .. kv_valid-1 are keys
+                // window: list row r beyond the sinks holds position r + win.shift; bounds on
+                // positions become bounds on rows by subtracting it
+                if constexpr (kWindow) kv_valid -= t.win.shift;
+                const int shift = kWindow ? t.win.shift : 0;
                 if constexpr (kAppend) {
                     int limit;
                     key_tile_span(t, jg, base, limit);
@@ -671,13 +707,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 // position, so the causal mask covers them)
                 // window: the tile's rows that some query of this MMA tile may not see lie past its
                 // first position, or before its last one's window and behind the sinks
-                const bool edge = base + kKT - 1 > pos_first || (kAppend && kv_valid < kKT) ||
-                                  (kWindow && base <= pos_first + kTilePos - 1 - a.window && base + kKT > a.sinks);
+                const bool edge =
+                    base + kKT - 1 > pos_first - shift || (kAppend && kv_valid < kKT) ||
+                    (kWindow && base + shift <= pos_first + kTilePos - 1 - a.window && base + kKT > a.sinks);
                 if (edge) {
                     if constexpr (kWindow) {
                         // a bit per column, 32 columns at a time: up to the row's position, and in
                         // its window or among the sinks
-                        const int hi = pos - base + 1;               // columns below hi
+                        const int hi = pos - shift - base + 1;       // columns below hi
                         const int lo = hi - min(a.window, hi + kKT);   // columns from lo on
                         const int sk = a.sinks - base;               // or below sk
                         const auto below = [](int n) {               // bits 0 .. n-1
@@ -754,12 +791,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 // reader) zeroes them.
                 // (window: also the rows before every query's window and behind the sinks, which
                 // may have been dropped)
-                const bool hidden = kWindow && base < t.lo && base + kKT > t.s_end;
+                const bool hidden = kWindow && base + shift < t.win.lo && base + kKT > t.win.s;
                 if (x == 0 && (kv_valid < kKT || hidden)) {
                     const int vs = it % kVStages;
                     ok = wait_or_abort(smem_u32(&sm.v_full[vs]), (it / kVStages) & 1, abort_flag, a.err);
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    if (row >= kv_valid || (hidden && base + row < t.lo && base + row >= t.s_end)) {
+                    if (row >= kv_valid || (hidden && base + row + shift < t.win.lo && base + row >= t.win.s)) {
                         uint4 *r0 = reinterpret_cast<uint4 *>(sm.v[vs][0] + row * 128);
                         uint4 *r1 = reinterpret_cast<uint4 *>(sm.v[vs][1] + row * 128);
 #pragma unroll
@@ -921,11 +958,12 @@ cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map, const
 }
 
 cudaError_t launch_prefill_window(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
-                                  const CUtensorMap &v_map, int num_sms, cudaStream_t stream) {
+                                  const CUtensorMap &v_map, const CUtensorMap &k16_map, const CUtensorMap &v16_map,
+                                  int num_sms, cudaStream_t stream) {
     if (a.num_seqs == 0 || a.max_q_len == 0 || a.total_tokens == 0) return cudaSuccess;
     if (a.order)
-        return launch_prefill_mode<false, true, false, true>(a, q_map, k_map, v_map, k_map, v_map, num_sms, stream);
-    return launch_prefill_mode<false, false, false, true>(a, q_map, k_map, v_map, k_map, v_map, num_sms, stream);
+        return launch_prefill_mode<false, true, false, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
+    return launch_prefill_mode<false, false, false, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
 }
 
 cudaError_t launch_prefill_append(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,

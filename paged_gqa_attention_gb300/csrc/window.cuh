@@ -33,4 +33,25 @@ struct WindowTiles {
     __device__ __forceinline__ bool sees_any(int p, int len) const { return p < s || p + len > lo; }
 };
 
+// The same tokens as one list of rows: the sinks, rounded up to groups of 16, then the window from
+// the group of 16 that holds its first token on.
+struct WindowRows {
+    int s, lo;      // as above; rows in between (at the ends of the groups) are seen by no query
+    int s16;        // rows of the sinks (0 when the list is one range from position 0)
+    int shift;      // row r >= s16 is position r + shift
+    int rows;       // up to the last query's own position
+
+    __device__ __forceinline__ void set(int window, int sinks, int first, int last) {
+        lo = max(0, first - window + 1);
+        s = sinks;
+        if (s >= lo) s = lo = 0;
+        s16 = (s + 15) & ~15;
+        const int lo16 = lo & ~15;
+        if (s16 >= lo16) s16 = shift = 0;   // nothing to leave out
+        else shift = lo16 - s16;
+        rows = last + 1 - shift;
+    }
+    __device__ __forceinline__ int position(int r) const { return r < s16 ? r : r + shift; }
+};
+
 }  // namespace pa

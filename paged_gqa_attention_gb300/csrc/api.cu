@@ -157,12 +157,40 @@ long long window_tiles_bound(int window, int sinks, int max_blocks_per_seq, int 
     return n < all ? n : all;
 }
 
-// Tiles per split of a windowed decode, whose sequences hold up to `tiles` each.
-int auto_window_split(int batch, long long tiles, int num_sms) {
+// Tiles per split of a windowed decode, whose sequences hold up to `tiles` each: the number of
+// splits n for which a model of its time, fitted to sweeps on GB300, is smallest.  One CTA walks
+// its tiles at the latency of its ring (tile_us each, times `crowded` when CTAs share SMs); all
+// tiles together take at least their bytes' time (stream_us each); the shorter of the two hides
+// about three quarters under the longer.  A merge costs cluster_us within a cluster, else
+// merge_us + merge_each_us a split.  Never more CTAs than two an SM: those past one wave start
+// when others end, and cost more than any split saves (20 sequences, 2048-token window: 28.1 us
+// unsplit, 36.1 us as 320 CTAs).  Measured, in bf16: one sequence and 1024 tokens 4.9 us in 6
+// (unsplit 9.6, in 18 6.1), 8 sequences and 4096 tokens 23.7 us in 4 (unsplit 35.1, in 10 29.9); in 8
+// bits: one sequence and 32768 tokens 22.3 us in 16 (in 8 33.2, in 37 23.6).
+struct SplitCost {
+    double tile_us, crowded, stream_us, cluster_us, merge_us, merge_each_us;
+};
+constexpr SplitCost kSplitCost = {0.42, 1.0, 0.0049, 1.4, 1.9, 0.07};      // 64 tokens in bf16
+constexpr SplitCost kSplitCostFp8 = {0.78, 1.5, 0.0068, 1e9, 2.3, 0.15};   // 128 in 8 bits (no cluster merge)
+
+int auto_window_split(int batch, long long tiles, int num_sms, const SplitCost &c) {
     const long long pairs = (long long)batch * kHkv;
-    long long n = (2LL * num_sms + pairs - 1) / pairs;   // splits of a pair: one wave of CTAs
-    if (n > tiles) n = tiles;
-    return (int)((tiles + n - 1) / n);
+    const double stream = c.stream_us * (double)pairs * (double)tiles;
+    long long best = tiles;
+    double best_us = 0.;
+    for (long long n = 1; n <= tiles && (n == 1 || pairs * n <= 2LL * num_sms); ++n) {
+        const long long per = (tiles + n - 1) / n;
+        const long long splits = (tiles + per - 1) / per;
+        const double walk = c.tile_us * (pairs * splits > num_sms ? c.crowded : 1.0) * (double)per;
+        double us = walk > stream ? walk + 0.25 * stream : stream + 0.25 * walk;
+        if (splits > 1)
+            us += splits <= 8 && c.cluster_us < c.merge_us ? c.cluster_us : c.merge_us + c.merge_each_us * (double)splits;
+        if (n == 1 || us < best_us) {
+            best = per;
+            best_us = us;
+        }
+    }
+    return (int)best;
 }
 
 size_t partial_entries_bound(int max_batch, int max_blocks_per_seq) {
@@ -246,7 +274,7 @@ pa_status decode_impl(pa_shape shape, void *out, float *lse, const void *q, cons
         win ? kDecodeTileTokens * window_tiles_bound(win->window, win->sinks, max_blocks_per_seq, kDecodeTileTokens)
             : (long long)(max_blocks_per_seq - skip_blocks) * kBlock;
     const int split = split_tokens ? split_tokens
-                      : win ? kDecodeTileTokens * auto_window_split(batch, max_tokens / kDecodeTileTokens, sms)
+                      : win ? kDecodeTileTokens * auto_window_split(batch, max_tokens / kDecodeTileTokens, sms, kSplitCost)
                             : auto_split_tokens(batch, max_blocks_per_seq - skip_blocks, sms);
     const long long nsplit = (max_tokens + split - 1) / split;
     if (nsplit > 65535) return PA_ERR_INVALID_ARG;
@@ -666,7 +694,7 @@ static pa_status decode_fp8_impl(pa_shape shape, void *out, float *lse, const vo
             : (long long)max_blocks_per_seq * kBlock;
     // the library's split rounded up to whole 128-token stages
     const int split = split_tokens ? split_tokens
-                      : win ? kDecodeFp8TileTokens * auto_window_split(batch, max_tokens / kDecodeFp8TileTokens, sms)
+                      : win ? kDecodeFp8TileTokens * auto_window_split(batch, max_tokens / kDecodeFp8TileTokens, sms, kSplitCostFp8)
                             : (auto_split_tokens(batch, max_blocks_per_seq, sms) + kDecodeFp8TileTokens - 1) /
                                   kDecodeFp8TileTokens * kDecodeFp8TileTokens;
     const long long nsplit = (max_tokens + split - 1) / split;

@@ -8,6 +8,7 @@ if the library is missing or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 
@@ -141,6 +142,31 @@ def load() -> ctypes.CDLL:
     lib.pa_selftest_wait_timeout.restype = ctypes.c_int
     _lib = lib
     return lib
+
+
+_binding = None
+
+
+def _usual():
+    """The compiled binding (csrc/binding.cpp): each of its functions makes a call in its usual
+    case and returns None for any other, which the checks below then judge; raise if absent."""
+    global _binding
+    if _binding is None:
+        load()
+        path = os.path.join(os.path.dirname(_LIB_PATH), "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -m paged_gqa_attention_gb300.build`")
+        spec = importlib.util.spec_from_file_location("_binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _binding = module
+    return _binding
+
+
+def _int32(**named):
+    for name, x in named.items():
+        if not isinstance(x, int) or not -2 ** 31 <= x < 2 ** 31:
+            raise ValueError(f"{name} must be a 32-bit integer, got {x!r}")
 
 
 def _check(fn: str, status: int):
@@ -371,10 +397,8 @@ def _rope_append(name, fn, q, k_new, v_new, cache, block_table, cu_q_lens, seq_l
         axes = positions.shape[0] if positions.dim() > 1 else 1
         _need(positions, "positions", torch.int32, (axes, tokens) if positions.dim() > 1 else (tokens,), dev)
         positions = positions.data_ptr()
-    if pair_axis is not None:
-        pair_axis = bytes(pair_axis)
-        if len(pair_axis) != ROPE_PAIRS:
-            raise ValueError(f"pair_axis must name {ROPE_PAIRS} axes")
+    if pair_axis is not None and len(pair_axis) != ROPE_PAIRS:
+        raise ValueError(f"pair_axis must name {ROPE_PAIRS} axes")
     if q_norm_weight is not None and k_norm_weight is not None:
         _need(q_norm_weight, "q_norm_weight", torch.bfloat16, (HEAD_DIM,), dev)
         _need(k_norm_weight, "k_norm_weight", torch.bfloat16, (HEAD_DIM,), dev)
@@ -403,6 +427,14 @@ def paged_rope_append(q, k_new, v_new, k_pool, v_pool, block_table, cu_q_lens, s
     positions (int32 [T] or [axes, T]) replace the cache positions in the rotation; with several
     axes, pair_axis (rope_pair_axes) names the axis of each of the 64 pairs.  q_out may be q
     itself.  Tokens behind the last sequence are left alone."""
+    if pair_axis is not None:
+        pair_axis = bytes(pair_axis)
+    if stream is None:
+        got = (_binding or _usual()).rope_append(False, q, k_new, v_new, k_pool, v_pool, None, None, block_table,
+                                                 cu_q_lens, seq_lens, workspace, rope_theta, positions, pair_axis,
+                                                 q_norm_weight, k_norm_weight, norm_eps, q_out)
+        if got is not None:
+            return got if type(got) is not int else _check("paged_rope_append", got)
     _need_pools(k_pool, v_pool)
     return _rope_append("paged_rope_append", load().paged_rope_append, q, k_new, v_new, (k_pool, v_pool), block_table,
                         cu_q_lens, seq_lens, workspace, rope_theta, positions, pair_axis, q_norm_weight, k_norm_weight,
@@ -415,6 +447,14 @@ def paged_rope_append_fp8(q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, b
                           stream=None) -> torch.Tensor:
     """paged_rope_append into the 8-bit cache (fp8_cache): k rows quantised from their rotated
     fp32 values, v rows as kv_append_fp8 does."""
+    if pair_axis is not None:
+        pair_axis = bytes(pair_axis)
+    if stream is None:
+        got = (_binding or _usual()).rope_append(True, q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, block_table,
+                                                 cu_q_lens, seq_lens, workspace, rope_theta, positions, pair_axis,
+                                                 q_norm_weight, k_norm_weight, norm_eps, q_out)
+        if got is not None:
+            return got if type(got) is not int else _check("paged_rope_append_fp8", got)
     _need(k_codes, "k_codes", torch.uint8, _POOL)
     _need_fp8_cache(k_codes, v_codes, k_scale, v_scale, k_codes.device)
     return _rope_append("paged_rope_append_fp8", load().paged_rope_append_fp8, q, k_new, v_new,
@@ -742,6 +782,12 @@ def paged_attn_decode_window(q, k_pool, v_pool, block_table, seq_lens, workspace
     Blocks without a visible token are not touched: their table entries may be -1.
     seq_lens[b] = 0 marks a padded row (zeros out, lse -inf).  split_tokens: visible tokens per
     CTA (multiple of 64), 0 = the library's choice."""
+    if stream is None:
+        got = (_binding or _usual()).decode_window(False, q, k_pool, v_pool, None, None, block_table, seq_lens,
+                                                   workspace, window, sinks, scale, split_tokens, out, lse)
+        if got is not None:
+            return got if type(got) is not int else _check("paged_attn_decode_window", got)
+    _int32(window=window, sinks=sinks, split_tokens=split_tokens)
     _need_pools(k_pool, v_pool)
     dev = k_pool.device
     out = _need_decode(q, block_table, seq_lens, workspace, out, lse, dev)
@@ -757,6 +803,12 @@ def paged_attn_decode_window_fp8(q, k_codes, v_codes, k_scale, v_scale, block_ta
                                  window: int, sinks: int = 0, scale: float = DEFAULT_SCALE, out=None, lse=None,
                                  split_tokens: int = 0, stream=None) -> torch.Tensor:
     """paged_attn_decode_window over the 8-bit cache (split_tokens a multiple of 128)."""
+    if stream is None:
+        got = (_binding or _usual()).decode_window(True, q, k_codes, v_codes, k_scale, v_scale, block_table, seq_lens,
+                                                   workspace, window, sinks, scale, split_tokens, out, lse)
+        if got is not None:
+            return got if type(got) is not int else _check("paged_attn_decode_window_fp8", got)
+    _int32(window=window, sinks=sinks, split_tokens=split_tokens)
     _need(k_codes, "k_codes", torch.uint8, _POOL)
     dev = k_codes.device
     _need_fp8_cache(k_codes, v_codes, k_scale, v_scale, dev)
@@ -789,6 +841,12 @@ def paged_attn_prefill_window(q, k_pool, v_pool, block_table, cu_q_lens, seq_len
                               stream=None) -> torch.Tensor:
     """paged_attn_prefill where every new token sees the first `sinks` tokens of its sequence and
     the `window` ones up to itself.  Table entries of blocks that no new token sees may be -1."""
+    if stream is None:
+        got = (_binding or _usual()).prefill_window(q, k_pool, v_pool, block_table, cu_q_lens, seq_lens, max_q_len,
+                                                    workspace, window, sinks, scale, out, lse)
+        if got is not None:
+            return got if type(got) is not int else _check("paged_attn_prefill_window", got)
+    _int32(max_q_len=max_q_len, window=window, sinks=sinks)
     _need_pools(k_pool, v_pool)
     dev = k_pool.device
     _need(q, "q", torch.bfloat16, (None, NUM_Q_HEADS, HEAD_DIM), dev)

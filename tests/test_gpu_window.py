@@ -331,3 +331,41 @@ def test_chat_with_a_window_end_to_end():
             compare(out8, keys8, values8, True)
         ops.check_error(ws)
         compare(out, keys, values, False)
+
+
+# ------------------------------------------------------------------ the binding
+
+def test_wrong_arguments_are_refused_with_their_names():
+    """The public calls on the GPU with one argument wrong at a time: the error names it."""
+    c = Cache([300, 20], [1, 1], 100, 4, 51).upload()
+    ws = ops.make_workspace(2, c.bt.shape[1])
+    good = dict(q=c.qd, k_pool=c.pools[0], v_pool=c.pools[1], block_table=c.bt, seq_lens=c.lens, workspace=ws)
+    ops.paged_attn_decode_window(**good, window=100)
+    for name, bad in (("q", c.qd.float()), ("q", c.qd[:, :8]), ("q", c.qd.transpose(0, 1)), ("k_pool", c.pools[0][:, :100]),
+                      ("v_pool", c.pools[1][:2]), ("block_table", c.bt[0]), ("block_table", c.bt.long()),
+                      ("seq_lens", c.lens[:1]), ("seq_lens", c.lens.cpu()), ("workspace", ws.view(torch.int32))):
+        with pytest.raises((TypeError, ValueError), match=name):
+            ops.paged_attn_decode_window(**{**good, name: bad}, window=100)
+    for extra in (dict(out=c.qd[:1]), dict(lse=torch.empty(2, 8, device="cuda")), dict(out=c.qd.float())):
+        with pytest.raises((TypeError, ValueError), match=next(iter(extra))):
+            ops.paged_attn_decode_window(**good, window=100, **extra)
+    for window, sinks, split in ((0, 0, 0), (-3, 0, 0), (5, -1, 0), (5, 0, 63)):
+        with pytest.raises(ops.PagedAttnError) as e:
+            ops.paged_attn_decode_window(**good, window=window, sinks=sinks, split_tokens=split)
+        assert e.value.status == 1
+    with pytest.raises(ops.PagedAttnError) as e:       # a workspace too small for the splits
+        ops.paged_attn_decode_window(**{**good, "workspace": ws[:300000]}, window=4096, split_tokens=64)
+    assert e.value.status == 6
+    ops.check_error(ws)
+
+
+def test_numbers_may_be_whole_and_the_output_given():
+    c = Cache([300, 20], [1, 1], 100, 4, 53).upload()
+    ws = ops.make_workspace(2, c.bt.shape[1])
+    out = torch.empty_like(c.qd)
+    a = ops.paged_attn_decode_window(c.qd, *c.pools, c.bt, c.lens, ws, window=100, sinks=4, scale=1, out=out)
+    b = ops.paged_attn_decode_window(c.qd, *c.pools, c.bt, c.lens, ws, window=100, sinks=4, scale=1.0,
+                                     stream=torch.cuda.current_stream())
+    assert a.data_ptr() == out.data_ptr() and torch.equal(a, b)
+    c.qd.requires_grad_()                               # the calls know no gradients: the result has none
+    assert not ops.paged_attn_decode_window(c.qd, *c.pools, c.bt, c.lens, ws, window=100).requires_grad

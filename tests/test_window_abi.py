@@ -187,3 +187,28 @@ def test_the_window_written_out_is_full_attention_when_long():
     out, _ = definitions.window_attention(q, [k], [v], [3], [9], 2, 1, scale)
     few, _ = definitions.window_attention(q[1:2], [k[[0, 6, 7]]], [v[[0, 6, 7]]], [1], [3], 9, 0, scale)
     assert torch.allclose(out[1:2], few)
+
+
+def test_the_compiled_binding_leaves_odd_cases_to_the_checks(lib):
+    """It makes a call only for plain CUDA tensors in the right number of arguments; host tensors,
+    other objects and other counts are answered with None, and ops' checks say what is wrong."""
+    b = ops._usual()
+    t = torch.zeros(1, 32, 128, dtype=torch.bfloat16)
+    for fn, n in ((b.rope_append, 19), (b.decode_window, 15), (b.prefill_window, 13)):
+        for x in (None, t, 3, "x", torch.nn.Parameter(t)):
+            assert fn(*[x] * n) is None
+        assert fn() is None and fn(*[t] * (n + 1)) is None
+    for window in (2 ** 31, -2 ** 31 - 1, 1.5):
+        with pytest.raises(ValueError, match="window must be a 32-bit integer"):
+            ops.paged_attn_decode_window(t, t, t, t, t, t, window=window)
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        ops.paged_attn_decode_window(t, t, t, t, t, t, window=3)
+    with pytest.raises(TypeError):
+        ops.paged_attn_prefill_window(t, None, t, t, t, t, 3, t, window=3)
+
+
+def test_the_binding_fails_loudly_when_it_is_missing(lib, monkeypatch, tmp_path):
+    monkeypatch.setattr(ops, "_binding", None)
+    monkeypatch.setattr(ops, "_LIB_PATH", str(tmp_path / "missing.so"))
+    with pytest.raises(RuntimeError, match="_binding.so is missing"):
+        ops._usual()

@@ -1,5 +1,6 @@
 // api.cu -- the extern "C" entry points declared in include/pagedattn.h: argument
 // validation, tensor-map encoding, the decode split choice and kernel launches.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <mutex>
@@ -1029,7 +1030,12 @@ static pa_status prefill_impl(pa_shape shape, void *out, float *lse, const void 
     if (plan_units > 0 && workspace_bytes >= kPartialOffset + (size_t)plan_units * sizeof(int32_t))
         a.order = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + kPartialOffset);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = win     ? launch_prefill_window(a, q_map, k_map, v_map, kn_map, vn_map, sms, st)
+    // keys a work unit's 64 positions may see, in tiles: sinks and window in groups of 16 rows
+    const long long rows = win ? std::min((long long)max_blocks_per_seq * kBlock,
+                                          (long long)win->sinks + 15 + win->window + 2 * kPrefillQPositions + 15)
+                               : 0;
+    const long long tiles = (rows + kPrefillKvTile - 1) / kPrefillKvTile;
+    const cudaError_t e = win     ? launch_prefill_window(a, tiles, q_map, k_map, v_map, kn_map, vn_map, sms, st)
                           : k_new ? launch_prefill_append(a, q_map, k_map, v_map, kn_map, vn_map, sms, st)
                                   : launch_prefill(a, q_map, k_map, v_map, sms, st);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;

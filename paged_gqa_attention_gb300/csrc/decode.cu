@@ -40,6 +40,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "cluster.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "window.cuh"
@@ -113,33 +114,6 @@ __device__ __forceinline__ void store_out4(__nv_bfloat16 *dst, const float (&v)[
 }
 
 // ------------------------------------------------------------------ cluster merge
-// Every thread of every CTA of the cluster (a pair's splits).
-__device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// The same shared-memory variable in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t peer_addr(uint32_t local, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
-    return r;
-}
-
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 // kCluster: the splits of one (sequence, KV head) form a thread-block cluster (at most 8,
 // launched when the whole grid fits in one wave).  Split 0 merges the pair's partials straight
 // from its peers' shared memory after a cluster barrier, instead of through the workspace and

@@ -104,6 +104,7 @@ struct PrefillArgs {
     // j < sinks or j > p - window.
     int32_t window;
     int32_t sinks;
+    int32_t unit_ctas;   // CTAs that share a work unit (chosen by launch_prefill_window)
 };
 
 constexpr int kRopePairs = 64;   // rotated pairs of a 128-dim head
@@ -211,8 +212,9 @@ cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map,
                            const CUtensorMap &k_map, const CUtensorMap &v_map, int num_sms,
                            cudaStream_t stream);
 
-// a.window set; k_map / v_map with boxes of 64 rows, k16_map / v16_map of 16.
-cudaError_t launch_prefill_window(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
+// a.window set; k_map / v_map with boxes of 64 rows, k16_map / v16_map of 16.  tiles: key tiles
+// that one work unit may visit.
+cudaError_t launch_prefill_window(PrefillArgs a, long long tiles, const CUtensorMap &q_map, const CUtensorMap &k_map,
                                   const CUtensorMap &v_map, const CUtensorMap &k16_map, const CUtensorMap &v16_map,
                                   int num_sms, cudaStream_t stream);
 

@@ -44,8 +44,17 @@
 // fetched in boxes of 64 and 16 rows: a few sinks cost a few rows, not a tile, and the window
 // starts where it starts.  (Tiles at multiples of 128 positions, the sinks' apart, were two more
 // a unit.)  Only tiles at the two ends of the window and the sinks' are masked.
+// With too few units to fill the GPU (kSplit), a cluster of CTAs shares each unit: every one takes a
+// run of its key tiles, leaves its unnormalised O with the rows' maxima and sums in its shared
+// memory (over Q and K, which are done with), and the CTAs merge a share of the rows each from all
+// of them by log-sum-exp.  129 tokens over a 512-token window: 24 units of 5 tiles, 14.6 us in 24
+// CTAs; SPLIT_MEASURED.
 // Every wait is bounded; on expiry the CTA records PA_ERR_TIMEOUT, unwinds, waits
 // (bounded) for its own copies and MMAs, frees tensor memory and exits.
+#include <atomic>
+#include <cstddef>
+
+#include "cluster.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "window.cuh"
@@ -90,7 +99,11 @@ struct PrefillSmem {
     uint64_t mma_idle;
     uint32_t tmem_base;
     int abort;
+    float ml[2 * kRows][2];          // kSplit: running maximum and sum of every row
 };
+// kSplit: O of the 256 rows, fp32, over q and k
+static_assert(offsetof(PrefillSmem, k) == sizeof(PrefillSmem::q) &&
+              sizeof(PrefillSmem::q) + sizeof(PrefillSmem::k) == 2 * kRows * kD * sizeof(float), "split merge area");
 
 constexpr size_t kSmemBytes = sizeof(PrefillSmem) + 1024;
 
@@ -192,8 +205,18 @@ __device__ __forceinline__ Unit unit_at_prefix(const PrefillArgs &a, int idx, in
     return t;
 }
 
-template <bool kPrefix, bool kPlanned, bool kAppend, bool kWindow>
+template <bool kPrefix, bool kPlanned, bool kAppend, bool kWindow, bool kSplit>
 __device__ __forceinline__ Unit unit_for(const PrefillArgs &a, int idx, int qblocks) {
+    if constexpr (kSplit) {
+        // this CTA's run of the unit's key tiles (none: it only takes part in the merge)
+        Unit t = unit_at<kAppend, kWindow>(a, idx, qblocks);
+        if (!t.run) return t;
+        const int len = (t.n_kt + a.unit_ctas - 1) / a.unit_ctas;
+        t.kt0 = (int)(blockIdx.x % a.unit_ctas) * len;
+        t.n_kt = min(len, t.n_kt - t.kt0);
+        if (t.n_kt <= 0) t.run = false;
+        return t;
+    }
     if constexpr (kPrefix) return unit_at_prefix(a, idx, qblocks);
     else if constexpr (kPlanned) return unit_at<kAppend, kWindow>(a, __ldg(a.order + idx), qblocks);
     else return unit_at<kAppend, kWindow>(a, idx, qblocks);
@@ -270,8 +293,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const Pre
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Index of this CTA's r-th unit in the snake order (or -1 past the end).
-__device__ __forceinline__ int snake(int r, int total) {
+// Index of this CTA's r-th unit in the snake order (or -1 past the end); kSplit: the cluster's one.
+template <bool kSplit>
+__device__ __forceinline__ int snake(const PrefillArgs &a, int r, int total) {
+    if constexpr (kSplit) return r == 0 ? (int)(blockIdx.x / a.unit_ctas) : -1;
     const int G = gridDim.x;
     const int idx = r * G + ((r & 1) ? (G - 1 - (int)blockIdx.x) : (int)blockIdx.x);
     return idx < total ? idx : -1;
@@ -392,7 +417,49 @@ __device__ __forceinline__ void append_share(const PrefillArgs &a, int lane) {
     }
 }
 
-template <bool kPrefix, bool kPlanned, bool kAppend, bool kWindow>
+// kSplit: merge a share of the unit's rows from the O, m and l that every CTA of the cluster left
+// in its shared memory (a row whose l is 0 saw no key there), and write their outputs.  Warp w takes
+// rows rank + ctas (w + 8i); a lane 4 dims.
+__device__ __forceinline__ void merge_rows(const PrefillArgs &a, const Unit &t, PrefillSmem &sm, int warp, int lane) {
+    const int ctas = a.unit_ctas, rank = (int)(blockIdx.x % ctas);
+    const uint32_t o_base = smem_u32(sm.q), ml_base = smem_u32(sm.ml);
+    for (int row = rank + ctas * warp; row < 2 * kRows; row += ctas * kSoftmaxWarps) {
+        const int x = row >> 7, pl = (row & (kRows - 1)) >> 2, hl = row & 3;   // tile, position, head
+        if (x * kTilePos + pl >= t.positions) continue;
+        const uint32_t o_at = o_base + (uint32_t)(row * kD * 4 + ((lane ^ (row & 7)) << 4));
+        float m[8], l[8], M = -INFINITY;
+        float4 o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k >= ctas) break;
+            m[k] = ld_cluster_f32(peer_addr(ml_base + row * 8, (uint32_t)k));
+            l[k] = ld_cluster_f32(peer_addr(ml_base + row * 8 + 4, (uint32_t)k));
+            o[k] = ld_cluster_f4(peer_addr(o_at, (uint32_t)k));
+            M = fmaxf(M, m[k]);
+        }
+        float L = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k >= ctas) break;
+            if (l[k] == 0.f) continue;
+            const float e = fast_exp2(m[k] - M);
+            L = __fmaf_rn(l[k], e, L);
+            v[0] = __fmaf_rn(o[k].x, e, v[0]);
+            v[1] = __fmaf_rn(o[k].y, e, v[1]);
+            v[2] = __fmaf_rn(o[k].z, e, v[2]);
+            v[3] = __fmaf_rn(o[k].w, e, v[3]);
+        }
+        const float inv = 1.f / L;
+        const size_t orow = (size_t)(t.tok0 + x * kTilePos + pl) * kHq + t.g * kGroup + hl;
+        uint2 w;
+        w.x = pack_bf16x2(v[0] * inv, v[1] * inv);
+        w.y = pack_bf16x2(v[2] * inv, v[3] * inv);
+        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + orow * kD + lane * 4) = w;
+        if (a.lse && lane == 0) a.lse[orow] = (M + __log2f(L)) * kLn2;
+    }
+}
+
+template <bool kPrefix, bool kPlanned, bool kAppend, bool kWindow, bool kSplit>
 __global__ void __launch_bounds__(kAppend ? kThreadsAppend : kThreads, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap kn_map,
@@ -465,9 +532,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         int q_issued = 0, kv_issued = 0;
         bool ok = true;
         for (int r = 0; ok; ++r) {
-            const int idx = snake(r, total);
+            const int idx = snake<kSplit>(a, r, total);
             if (idx < 0) break;
-            const Unit t = unit_for<kPrefix, kPlanned, kAppend, kWindow>(a, idx, qblocks);
+            const Unit t = unit_for<kPrefix, kPlanned, kAppend, kWindow, kSplit>(a, idx, qblocks);
             if (qk && leader && t.error) record_error(a.err, kErrDevice | kErrQLen);
             if (!t.run) continue;
             if (qk) {
@@ -611,9 +678,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
             return true;
         };
         for (int r = 0; ok; ++r) {
-            const int idx = snake(r, total);
+            const int idx = snake<kSplit>(a, r, total);
             if (idx < 0) break;
-            const Unit t = unit_for<kPrefix, kPlanned, kAppend, kWindow>(a, idx, qblocks);
+            const Unit t = unit_for<kPrefix, kPlanned, kAppend, kWindow, kSplit>(a, idx, qblocks);
             if (!t.run) continue;
             if (!(ok = wait_all(&sm.q_full, tcount & 1))) break;
             for (int j = 0; j < t.n_kt; ++j, ++it) {
@@ -650,9 +717,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         // O += P V product (if it has any unit to compute; bounded, then it copies anyway).
         bool has_unit = false;
         for (int r = 0; !has_unit; ++r) {
-            const int idx = snake(r, total);
+            const int idx = snake<kSplit>(a, r, total);
             if (idx < 0) break;
-            has_unit = unit_for<kPrefix, kPlanned, kAppend, kWindow>(a, idx, qblocks).run;
+            has_unit = unit_for<kPrefix, kPlanned, kAppend, kWindow, kSplit>(a, idx, qblocks).run;
         }
         if (has_unit) mbar_wait(smem_u32(&sm.o_done[0]), 0, 200000ull);
         append_share(a, lane);
@@ -669,10 +736,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         const float sl2 = a.scale_log2;
         int it = 0;
         bool ok = true;
+        float split_m = -INFINITY, split_l = 0.f;   // kSplit: no key seen so far
+        bool split_done = false;
         for (int r = 0; ok; ++r) {
-            const int idx = snake(r, total);
+            const int idx = snake<kSplit>(a, r, total);
             if (idx < 0) break;
-            const Unit t = unit_for<kPrefix, kPlanned, kAppend, kWindow>(a, idx, qblocks);
+            const Unit t = unit_for<kPrefix, kPlanned, kAppend, kWindow, kSplit>(a, idx, qblocks);
             if (!t.run) continue;
             // the last key each row may see: its own position (causal), or the whole prefix
             const int pos_first = kPrefix ? t.seq_len - 1 : t.pos0 + x * kTilePos;
@@ -844,6 +913,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
             ok = wait_or_abort(smem_u32(&sm.o_done[x]), (it - 1) & 1, abort_flag, a.err);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
+            if constexpr (kSplit) {
+                split_m = m;
+                split_l = l;
+                split_done = true;
+                continue;
+            }
             const float inv_l = 1.f / l;
             const bool row_ok = x * kTilePos + pl < t.positions;
             // shared-prefix mode: fp32 partials of key split ks, [ks][token][32][128]
@@ -880,6 +955,43 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
             if (row_ok && a.lse) a.lse[orow] = (m + __log2f(l)) * kLn2;
             tc_fence_before();
         }
+        if constexpr (kSplit) {
+            // Once both tiles' products are done, their reads of Q and K are too, and this CTA's O
+            // goes over them, row by row, the 16-byte pieces of a row permuted by its low bits so that
+            // neither these stores nor the merge's loads meet on a bank.  (All softmax warps come to
+            // this barrier, also those that gave up.)
+            named_barrier(1, kSoftmaxWarps * 32);
+            const int rr = x * kRows + row;
+            if (split_done) {
+                uint8_t *dst = sm.q[0][0] + rr * (kD * 4);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(lane_base + o_col + c * 32, o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        *reinterpret_cast<uint4 *>(dst + (((c * 8 + v) ^ (rr & 7)) << 4)) =
+                            make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                }
+                tc_fence_before();
+            }
+            sm.ml[rr][0] = split_m;
+            sm.ml[rr][1] = split_l;
+        }
+    }
+
+    if constexpr (kSplit) {
+        // every CTA's part is in its shared memory, merged by all, and stays until all have read it
+        // (after an abort too: every wait above is bounded, so every CTA comes here)
+        __syncwarp();
+        cluster_sync_all();
+        if (warp < kSoftmaxWarps) {
+            const Unit t = unit_at<kAppend, kWindow>(a, (int)(blockIdx.x / a.unit_ctas), qblocks);
+            if (t.run) merge_rows(a, t, sm, warp, lane);
+        }
+        __syncwarp();
+        cluster_sync_all();
     }
 
     // ---------------------------------------------------------------- teardown
@@ -902,7 +1014,24 @@ __global__ void wait_selftest_kernel(uint32_t *err, uint64_t limit_ns) {
     if (threadIdx.x == 0 && !mbar_wait(smem_u32(&bar), 0, limit_ns)) record_error(err, kErrTimeout);
 }
 
-template <bool kPrefix, bool kPlanned, bool kAppend, bool kWindow = false>
+// CTAs that share a unit (a cluster) in a windowed prefill of `units` units of up to `tiles` key
+// tiles: 1 unless all clusters fit on the GPU at once.  Of the sizes that do, the one with the
+// shortest run of tiles, the merge counted as one more tile and a half.
+int unit_ctas_for(long long units, long long tiles, int num_sms, const int (&max_clusters)[9]) {
+    int best = 1;
+    double best_cost = (double)tiles;
+    for (int c = 2; c <= 8 && units * c <= num_sms; ++c) {
+        if (max_clusters[c] < units) continue;
+        const double cost = (double)((tiles + c - 1) / c) + 1.5;
+        if (cost < best_cost) {
+            best = c;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
+template <bool kPrefix, bool kPlanned, bool kAppend, bool kWindow = false, bool kSplit = false>
 cudaError_t launch_prefill_mode(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
                                 const CUtensorMap &v_map, const CUtensorMap &kn_map, const CUtensorMap &vn_map,
                                 int num_sms, cudaStream_t stream) {
@@ -911,23 +1040,27 @@ cudaError_t launch_prefill_mode(const PrefillArgs &a, const CUtensorMap &q_map, 
     if (e != cudaSuccess) return e;
     static bool configured[64] = {};
     if (dev < 0 || dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(prefill_kernel<kPrefix, kPlanned, kAppend, kWindow>,
+        e = cudaFuncSetAttribute(prefill_kernel<kPrefix, kPlanned, kAppend, kWindow, kSplit>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
     const long long qblocks = (a.max_q_len + kUnitPos - 1) / kUnitPos;
     const long long units = kPrefix ? kHkv * qblocks * a.n_kv_splits : (long long)a.num_seqs * kHkv * qblocks;
-    const int grid = (int)(units < num_sms ? units : num_sms);
+    const int grid = kSplit ? (int)units * a.unit_ctas : (int)(units < num_sms ? units : num_sms);
     // Programmatic dependent launch: the producers wait (griddepcontrol.wait) before their
     // first load, so the launch and prologue may overlap the previous kernel on the stream.
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;   // kSplit only
+    attr[1].val.clusterDim.x = kSplit ? (unsigned)a.unit_ctas : 1u;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = kSplit ? 2 : 1;
     if constexpr (kPlanned) {
         cfg.gridDim = dim3(1);
         cfg.blockDim = dim3(kPlanThreads);
@@ -938,8 +1071,8 @@ cudaError_t launch_prefill_mode(const PrefillArgs &a, const CUtensorMap &q_map, 
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kAppend ? kThreadsAppend : kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
-    return cudaLaunchKernelEx(&cfg, prefill_kernel<kPrefix, kPlanned, kAppend, kWindow>, q_map, k_map, v_map, kn_map,
-                              vn_map, a);
+    return cudaLaunchKernelEx(&cfg, prefill_kernel<kPrefix, kPlanned, kAppend, kWindow, kSplit>, q_map, k_map, v_map,
+                              kn_map, vn_map, a);
 }
 
 }  // namespace
@@ -957,10 +1090,58 @@ cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map, const
     return launch_prefill_mode<false, false, false>(a, q_map, k_map, v_map, k_map, v_map, num_sms, stream);
 }
 
-cudaError_t launch_prefill_window(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
+// How many clusters of c CTAs of the split kernel fit on the current device at once, c = 2 .. 8
+// (looked up on the first call per device).
+static cudaError_t split_clusters(int (&out)[9]) {
+    static std::atomic<int> known[64][9];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const auto kernel = prefill_kernel<false, false, false, true, true>;
+    for (int c = 2; c <= 8; ++c) {
+        int n = known[dev][c].load();
+        if (n == 0) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+            if (e != cudaSuccess) return e;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = (unsigned)c;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)c);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = kSmemBytes;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();   // this size is not to be had: it is not used
+                n = 0;
+            }
+            n = n > 0 ? n : -1;
+            known[dev][c].store(n);
+        }
+        out[c] = n;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_prefill_window(PrefillArgs a, long long tiles, const CUtensorMap &q_map, const CUtensorMap &k_map,
                                   const CUtensorMap &v_map, const CUtensorMap &k16_map, const CUtensorMap &v16_map,
                                   int num_sms, cudaStream_t stream) {
     if (a.num_seqs == 0 || a.max_q_len == 0 || a.total_tokens == 0) return cudaSuccess;
+    const long long units = (long long)a.num_seqs * kHkv * ((a.max_q_len + kUnitPos - 1) / kUnitPos);
+    a.unit_ctas = 1;
+    if (units * 2 <= num_sms) {
+        int clusters[9] = {};
+        const cudaError_t e = split_clusters(clusters);
+        if (e != cudaSuccess) return e;
+        a.unit_ctas = unit_ctas_for(units, tiles, num_sms, clusters);
+    }
+    if (a.unit_ctas > 1)
+        return launch_prefill_mode<false, false, false, true, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms,
+                                                                    stream);
     if (a.order)
         return launch_prefill_mode<false, true, false, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
     return launch_prefill_mode<false, false, false, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);

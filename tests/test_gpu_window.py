@@ -369,3 +369,38 @@ def test_numbers_may_be_whole_and_the_output_given():
     assert a.data_ptr() == out.data_ptr() and torch.equal(a, b)
     c.qd.requires_grad_()                               # the calls know no gradients: the result has none
     assert not ops.paged_attn_decode_window(c.qd, *c.pools, c.bt, c.lens, ws, window=100).requires_grad
+
+
+# few tokens over a wide window: a cluster of CTAs shares each work unit (2 to 8 of them)
+@pytest.mark.parametrize("window,sinks", [(1 << 30, 0), (1000, 100), (300, 4), (2000, 0)])
+@pytest.mark.parametrize("lens,q_lens", [([3000], [1]), ([3000], [65]), ([2500, 40], [64, 40]), ([2000, 2000, 100], [5, 0, 70]),
+                                         ([1500], [400])])
+def test_prefill_of_few_tokens(lens, q_lens, window, sinks):
+    c = Cache(lens, q_lens, window, sinks, 37).upload()
+    out, lse = prefill(c)
+    ref, ref_lse, tol = c.reference()
+    check(out, ref, tol, "out")
+    assert_lse_close(lse, ref_lse.numpy(), "window lse")
+    again, _ = prefill(c)
+    assert torch.equal(out, again)
+
+
+def test_prefill_of_few_tokens_with_a_bad_block_and_captured():
+    c = Cache([3000, 2000], [20, 33], 1500, 70, 39).upload()
+    want, _ = prefill(c)
+    ws = ops.make_workspace(2, c.bt.shape[1])
+    table = c.bt.clone()
+    table[1, 6] = c.blocks + 5
+    out = ops.paged_attn_prefill_window(c.qd, *c.pools, table, c.cu, c.lens, 33, ws, window=1500, sinks=70)
+    with pytest.raises(ops.PagedAttnError) as e:
+        ops.check_error(ws)
+    assert e.value.status == 4 and torch.equal(out[:20], want[:20])
+    out = torch.empty_like(want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        ops.paged_attn_prefill_window(c.qd, *c.pools, c.bt, c.cu, c.lens, 33, ws, window=1500, sinks=70, out=out)
+    for _ in range(2):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+    ops.check_error(ws)

@@ -47,10 +47,14 @@
 // With too few units to fill the GPU (kSplit), a cluster of CTAs shares each unit: every one takes a
 // run of its key tiles, leaves its unnormalised O with the rows' maxima and sums in its shared
 // memory (over Q and K, which are done with), and the CTAs merge a share of the rows each from all
-// of them by log-sum-exp.  129 tokens over a 512-token window: 24 units of 5 tiles, 14.6 us in 24
-// CTAs; SPLIT_MEASURED.
+// of them by log-sum-exp.  Over a 4096-token window (33 or 34 tiles): 1 token 53.6 us in 8 CTAs,
+// 15.6 in 64; 64 tokens 55.2 and 20.6 us; 512 tokens 57.0 and 39.5 us (64 and 128 CTAs).  The merge
+// takes about 1.6 us, and 5.2 more for 64 positions: 128 KiB a CTA from its peers' shared memory at
+// some 14 bytes a clock.  (Storing each row to its merger instead, 16 bytes a lane, took 2 to 3 us
+// longer.)
 // Every wait is bounded; on expiry the CTA records PA_ERR_TIMEOUT, unwinds, waits
 // (bounded) for its own copies and MMAs, frees tensor memory and exits.
+#include <algorithm>
 #include <atomic>
 #include <cstddef>
 
@@ -1015,17 +1019,18 @@ __global__ void wait_selftest_kernel(uint32_t *err, uint64_t limit_ns) {
 }
 
 // CTAs that share a unit (a cluster) in a windowed prefill of `units` units of up to `tiles` key
-// tiles: 1 unless all clusters fit on the GPU at once.  Of the sizes that do, the one with the
-// shortest run of tiles, the merge counted as one more tile and a half.
-int unit_ctas_for(long long units, long long tiles, int num_sms, const int (&max_clusters)[9]) {
+// tiles and `positions` query positions: 1 unless all clusters fit on the GPU at once.  Of the
+// sizes that do, the one whose run of tiles (1.5 us each) and merge take least.
+int unit_ctas_for(long long units, long long tiles, int positions, int num_sms, const int (&max_clusters)[9]) {
+    const double merge_us = 1.6 + 5.2 * positions / kUnitPos;
     int best = 1;
-    double best_cost = (double)tiles;
+    double best_us = 1.5 * (double)tiles;
     for (int c = 2; c <= 8 && units * c <= num_sms; ++c) {
         if (max_clusters[c] < units) continue;
-        const double cost = (double)((tiles + c - 1) / c) + 1.5;
-        if (cost < best_cost) {
+        const double us = 1.5 * (double)((tiles + c - 1) / c) + merge_us;
+        if (us < best_us) {
             best = c;
-            best_cost = cost;
+            best_us = us;
         }
     }
     return best;
@@ -1137,7 +1142,7 @@ cudaError_t launch_prefill_window(PrefillArgs a, long long tiles, const CUtensor
         int clusters[9] = {};
         const cudaError_t e = split_clusters(clusters);
         if (e != cudaSuccess) return e;
-        a.unit_ctas = unit_ctas_for(units, tiles, num_sms, clusters);
+        a.unit_ctas = unit_ctas_for(units, tiles, std::min(a.max_q_len, kUnitPos), num_sms, clusters);
     }
     if (a.unit_ctas > 1)
         return launch_prefill_mode<false, false, false, true, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms,

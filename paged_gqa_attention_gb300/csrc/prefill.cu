@@ -103,7 +103,10 @@ struct PrefillSmem {
     uint64_t mma_idle;
     uint32_t tmem_base;
     int abort;
-    float ml[2 * kRows][2];          // kSplit: running maximum and sum of every row
+    union {
+        float ml[2 * kRows][2];                // kSplit: running maximum and sum of every row
+        uint8_t stage[kSoftmaxWarps][32 * 128];   // kWindow: a warp's 32 output rows, 64 dims at a time
+    };
 };
 // kSplit: O of the 256 rows, fp32, over q and k
 static_assert(offsetof(PrefillSmem, k) == sizeof(PrefillSmem::q) &&
@@ -248,10 +251,14 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const Pre
     __shared__ int hist[kPlanMaxKeys];
     __shared__ int warp_sum[kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // The prefill may start its prologue now; it waits for this kernel before it reads the order.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // the key of this thread's first unit is needed twice and kept
+    const int key0 = tid < total ? min(plan_key<kAppend, kWindow>(a, tid, qblocks), nk - 1) : 0;
     for (int k = tid; k < nk; k += kPlanThreads) hist[k] = 0;
     __syncthreads();
     for (int idx = tid; idx < total; idx += kPlanThreads)
-        atomicAdd(&hist[min(plan_key<kAppend, kWindow>(a, idx, qblocks), nk - 1)], 1);
+        atomicAdd(&hist[idx == tid ? key0 : min(plan_key<kAppend, kWindow>(a, idx, qblocks), nk - 1)], 1);
     __syncthreads();
     // hist[k] <- first rank of key k = number of units with more key tiles.  Thread t owns
     // the keys hi, hi - 1, ..., hi - per + 1 counted from the top.
@@ -289,7 +296,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const Pre
     }
     __syncthreads();
     for (int idx = tid; idx < total; idx += kPlanThreads) {
-        const int rank = atomicAdd(&hist[min(plan_key<kAppend, kWindow>(a, idx, qblocks), nk - 1)], 1);
+        const int rank = atomicAdd(&hist[idx == tid ? key0 : min(plan_key<kAppend, kWindow>(a, idx, qblocks), nk - 1)], 1);
         a.order[rank] = idx;
     }
     // Complete only after the kernel before this one on the stream (kv_append lets its
@@ -742,10 +749,16 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         bool ok = true;
         float split_m = -INFINITY, split_l = 0.f;   // kSplit: no key seen so far
         bool split_done = false;
+        // (window: a unit's lengths are looked up before the epilogue of the one before it, whose
+        // stores they would otherwise queue behind)
+        Unit next;
+        next.run = false;
+        bool fetched = false;
         for (int r = 0; ok; ++r) {
             const int idx = snake<kSplit>(a, r, total);
             if (idx < 0) break;
-            const Unit t = unit_for<kPrefix, kPlanned, kAppend, kWindow, kSplit>(a, idx, qblocks);
+            const Unit t = fetched ? next : unit_for<kPrefix, kPlanned, kAppend, kWindow, kSplit>(a, idx, qblocks);
+            fetched = false;
             if (!t.run) continue;
             // the last key each row may see: its own position (causal), or the whole prefix
             const int pos_first = kPrefix ? t.seq_len - 1 : t.pos0 + x * kTilePos;
@@ -796,6 +809,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             const uint32_t see = below(hi - c * 32) & (~below(lo - c * 32) | below(sk - c * 32));
+                            // (a warp's 8 positions differ in few columns: most chunks are all seen)
+                            if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
                                 if (!(see >> e & 1u)) s[c][e] = __float_as_uint(-INFINITY);
@@ -914,6 +929,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
             if (!ok) break;
 
             // ------------------------------------------------------------ epilogue
+            if constexpr (kWindow && !kSplit) {
+                const int idx_next = snake<kSplit>(a, r + 1, total);
+                if (idx_next >= 0) {
+                    next = unit_for<kPrefix, kPlanned, kAppend, kWindow, kSplit>(a, idx_next, qblocks);
+                    fetched = true;
+                }
+            }
             ok = wait_or_abort(smem_u32(&sm.o_done[x]), (it - 1) & 1, abort_flag, a.err);
             if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
@@ -925,6 +947,46 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
             }
             const float inv_l = 1.f / l;
             const bool row_ok = x * kTilePos + pl < t.positions;
+            if constexpr (kWindow) {
+                // Through shared memory, 64 dims at a time, so that a warp's store writes the four
+                // heads' rows of one position, 128 contiguous bytes each: a thread storing its own row
+                // touches 32 lines an instruction, and the stores of a unit took 2300 clk (a tile's
+                // products take 1024, and a short window leaves only a few of them).
+                uint8_t *stg = sm.stage[warp];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(lane_base + o_col + h * 64 + c * 32, o);
+                        tmem_wait_ld(o);
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2)
+                            w[e / 2] = pack_bf16x2(__uint_as_float(o[e]) * inv_l, __uint_as_float(o[e + 1]) * inv_l);
+#pragma unroll
+                        for (int v = 0; v < 4; ++v)
+                            *reinterpret_cast<uint4 *>(stg + sw128(lane, c * 4 + v)) =
+                                make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+                    }
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int p = x * kTilePos + (warp & 3) * 8 + i;   // position in the unit
+                        const uint4 w = *reinterpret_cast<const uint4 *>(stg + sw128(i * 4 + (lane >> 3), lane & 7));
+                        if (p < t.positions)
+                            *reinterpret_cast<uint4 *>(
+                                static_cast<__nv_bfloat16 *>(a.out) +
+                                ((size_t)(t.tok0 + p) * kHq + t.g * kGroup + (lane >> 3)) * kD + h * 64 +
+                                (lane & 7) * 8) = w;
+                    }
+                    __syncwarp();
+                }
+                if (row_ok && a.lse)
+                    a.lse[(size_t)(t.tok0 + x * kTilePos + pl) * kHq + t.g * kGroup + hl] = (m + __log2f(l)) * kLn2;
+                tc_fence_before();
+                continue;
+            }
             // shared-prefix mode: fp32 partials of key split ks, [ks][token][32][128]
             const size_t orow = (size_t)t.ks * a.total_tokens * kHq +
                                 (size_t)(t.tok0 + x * kTilePos + pl) * kHq + t.g * kGroup + hl;

@@ -43,9 +43,9 @@
  *
  * Streams.  `stream` is a cudaStream_t (NULL = the legacy default stream).  Calls
  * are asynchronous and stream-ordered; PA_OK means "validated and launched".  The
- * decode, prefill and projection kernels are launched as programmatic dependents of the
- * kernel before them on the stream: they may start before it has finished, and wait for
- * it before touching q, x, k_new, v_new, the pools, out or lse.  block_table, seq_lens and
+ * decode, prefill, projection and rotated-append kernels are launched as programmatic dependents
+ * of the kernel before them on the stream: they may start before it has finished, and wait for
+ * it before touching q, x, k_new, v_new, positions, gains, the pools, out or lse.  block_table, seq_lens and
  * cu_q_lens may be read earlier, so a kernel that writes them immediately before a
  * call must not let its dependents start early (griddepcontrol.launch_dependents).
  *
@@ -329,10 +329,11 @@ pa_status paged_attn_decode_fp8_split(pa_shape shape, void *out, float *lse, con
  *
  * paged_attn_decode_window, paged_attn_decode_window_fp8: paged_attn_decode and
  * paged_attn_decode_fp8 with a window, p = seq_lens[b] - 1.  Append first
- * (paged_rope_append, kv_append).  seq_lens[b] = 0 is a padded row of the batch: its output
+ * (paged_rope_append, kv_append); over the 8-bit cache |q| < 65504.  seq_lens[b] = 0 is a padded row of the batch: its output
  * is zeros, its lse -infinity.  split_tokens: visible tokens one CTA handles (a positive
  * multiple of 64, of 128 over the 8-bit cache), 0 = the library's choice; results depend on it
- * only by rounding.  The workspace of pa_workspace_bytes() suits the library's choice.
+ * only by rounding.  The workspace of pa_workspace_bytes() suits the library's choice; a choice of
+ * the caller's needs batch * 8 * splits entries, as for paged_attn_decode_split.
  */
 pa_status paged_attn_decode_window(pa_shape shape, void *out, float *lse, const void *q,
                                    const void *k_pool, const void *v_pool,
@@ -506,7 +507,8 @@ pa_status paged_attn_prefill(pa_shape shape, void *out, float *lse, const void *
 /*
  * paged_attn_prefill_window: paged_attn_prefill with a sliding window and sinks (the rule above,
  * p each new token's position).  Arguments, workspace and errors as for paged_attn_prefill; the
- * table entries of blocks that none of a sequence's new tokens sees are not used.  A NaN or
+ * table entries of blocks that none of a sequence's new tokens sees are not used.  With few
+ * tokens a cluster of CTAs shares each work unit and merges by log-sum-exp.  A NaN or
  * infinity in a V row that some of the 64 positions of a work unit see and others do not may
  * reach the outputs of all 64.
  */

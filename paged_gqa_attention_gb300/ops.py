@@ -180,6 +180,15 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
+def _empty(shape, dev, stream) -> torch.Tensor:
+    """A new bf16 tensor for a call on `stream` (its memory then comes from that stream's share of
+    the allocator, so nothing still running on the current one can be using it)."""
+    if stream is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=torch.bfloat16, device=dev)
+
+
 def _launch(fn, dev, stream, *args) -> int:
     """fn(*args, stream) with dev current (a launch goes to the current device); the stream is
     dev's current one unless given.  torch.cuda's own functions for this cost more host time
@@ -394,6 +403,8 @@ def _rope_append(name, fn, q, k_new, v_new, cache, block_table, cu_q_lens, seq_l
     _need(workspace, "workspace", torch.uint8, None, dev)
     axes = 1
     if positions is not None:
+        if not isinstance(positions, torch.Tensor):
+            raise TypeError("positions must be a torch.Tensor")
         axes = positions.shape[0] if positions.dim() > 1 else 1
         _need(positions, "positions", torch.int32, (axes, tokens) if positions.dim() > 1 else (tokens,), dev)
         positions = positions.data_ptr()
@@ -406,7 +417,7 @@ def _rope_append(name, fn, q, k_new, v_new, cache, block_table, cu_q_lens, seq_l
     elif q_norm_weight is not None or k_norm_weight is not None:
         raise ValueError("QK-norm takes both q_norm_weight and k_norm_weight")
     if q_out is None:
-        q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=dev)
+        q_out = _empty(q_shape, dev, stream)
     else:
         _need(q_out, "q_out", torch.bfloat16, q_shape, dev)
     _check(name, _launch(fn, dev, stream, SHAPE, rope_theta, positions, axes, pair_axis, q_norm_weight, k_norm_weight,
@@ -790,7 +801,7 @@ def paged_attn_decode_window(q, k_pool, v_pool, block_table, seq_lens, workspace
     _int32(window=window, sinks=sinks, split_tokens=split_tokens)
     _need_pools(k_pool, v_pool)
     dev = k_pool.device
-    out = _need_decode(q, block_table, seq_lens, workspace, out, lse, dev)
+    out = _need_decode(q, block_table, seq_lens, workspace, out, lse, dev, stream)
     _check("paged_attn_decode_window",
            _launch(load().paged_attn_decode_window, dev, stream, SHAPE, out.data_ptr(), _ptr(lse), q.data_ptr(),
                    k_pool.data_ptr(), v_pool.data_ptr(), block_table.data_ptr(), block_table.shape[1], k_pool.shape[0],
@@ -812,7 +823,7 @@ def paged_attn_decode_window_fp8(q, k_codes, v_codes, k_scale, v_scale, block_ta
     _need(k_codes, "k_codes", torch.uint8, _POOL)
     dev = k_codes.device
     _need_fp8_cache(k_codes, v_codes, k_scale, v_scale, dev)
-    out = _need_decode(q, block_table, seq_lens, workspace, out, lse, dev)
+    out = _need_decode(q, block_table, seq_lens, workspace, out, lse, dev, stream)
     _check("paged_attn_decode_window_fp8",
            _launch(load().paged_attn_decode_window_fp8, dev, stream, SHAPE, out.data_ptr(), _ptr(lse), q.data_ptr(),
                    k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
@@ -821,7 +832,7 @@ def paged_attn_decode_window_fp8(q, k_codes, v_codes, k_scale, v_scale, block_ta
     return out
 
 
-def _need_decode(q, block_table, seq_lens, workspace, out, lse, dev):
+def _need_decode(q, block_table, seq_lens, workspace, out, lse, dev, stream):
     _need(q, "q", torch.bfloat16, (None, NUM_Q_HEADS, HEAD_DIM), dev)
     batch = q.shape[0]
     if _need_table(block_table, dev)[0] != batch:
@@ -831,7 +842,7 @@ def _need_decode(q, block_table, seq_lens, workspace, out, lse, dev):
     if lse is not None:
         _need(lse, "lse", torch.float32, (batch, NUM_Q_HEADS), dev)
     if out is None:
-        return torch.empty_like(q)
+        return _empty(q.shape, dev, stream)
     _need(out, "out", torch.bfloat16, tuple(q.shape), dev)
     return out
 
@@ -857,7 +868,7 @@ def paged_attn_prefill_window(q, k_pool, v_pool, block_table, cu_q_lens, seq_len
     if lse is not None:
         _need(lse, "lse", torch.float32, (q.shape[0], NUM_Q_HEADS), dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, dev, stream)
     else:
         _need(out, "out", torch.bfloat16, q.shape, dev)
     _check("paged_attn_prefill_window",

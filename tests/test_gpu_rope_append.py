@@ -177,6 +177,31 @@ def test_in_place(tokens):
     assert out.data_ptr() == q.data_ptr()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_far_in_the_pool(fp8):
+    """Rows whose offset in the pool passes 2^31 elements."""
+    b = batch_of([300], [100])
+    q, k, v = operands(100, 55, merged=True)
+    blocks = 9000                                # 9000 * 262144 elements
+    table = torch.full_like(b.block_table, -1)
+    table[0, 0], table[0, 1] = blocks - 1, blocks - 3
+    if fp8:
+        cache = [torch.zeros(blocks, 256, 8, 128, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        cache += [torch.zeros(blocks, 8, 256, device="cuda") for _ in range(2)]
+    else:
+        cache = [torch.zeros(blocks, 256, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    small = [t[:b.num_blocks].clone() for t in cache]
+    ws = ops.make_workspace(1, b.max_blocks_per_seq)
+    fn = ops.paged_rope_append_fp8 if fp8 else ops.paged_rope_append
+    fn(q, k, v, *cache, table, b.cu_q_lens, b.seq_lens, ws, rope_theta=THETA)
+    fn(q, k, v, *small, b.block_table, b.cu_q_lens, b.seq_lens, ws, rope_theta=THETA)
+    ops.check_error(ws)
+    for far, near in zip(cache, small):
+        for j, blk in enumerate((blocks - 1, blocks - 3)):
+            assert torch.equal(far[blk].view(torch.uint8), near[int(b.block_table[0, j])].view(torch.uint8))
+        assert not far[:blocks - 3].any() and not far[blocks - 2].any()
+
+
 def test_zero_rows_and_8_bit_scale_of_one():
     b = batch_of([20], [2])
     q, k, v = operands(2, 61, merged=True)

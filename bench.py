@@ -51,17 +51,17 @@ HEAD_START_CYCLES = 200_000      # ~0.1 ms spin so a step's launches are all que
 # whose sources changed since reports traffic null.
 TRAFFIC = {
     # one ncu capture of the batched decode step (32 sequences, 243.9 MB of K/V)
-    "decode": {"bytes_per_launch": 249650432 + 4694272, "sources": ("decode.cu", "common.cuh"),
-               "sha": "8933af376eb543b1", "workload": "batched_decode"},
+    "decode": {"bytes_per_launch": 249668864 + 3982848, "sources": ("decode.cu", "cluster.cuh", "common.cuh", "window.cuh"),
+               "sha": "4ca59ac25fa8f5db", "workload": "batched_decode"},
     # one ncu capture of the fused 8-bit decode step (batch 32, 126 MB of 8-bit K/V)
-    "decode_fp8": {"bytes_per_launch": 131116800 + 4321280, "sources": ("decode_fp8.cu", "common.cuh"),
-                   "sha": "fa1e86d11026bb58", "workload": "batched_decode_fp8"},
+    "decode_fp8": {"bytes_per_launch": 131120640 + 3318016, "sources": ("decode_fp8.cu", "common.cuh", "window.cuh"),
+                   "sha": "65191282a7f4f255", "workload": "batched_decode_fp8"},
     # one ncu capture of the causal prefill of 4096 tokens with the prompt's append fused in
-    "prefill": {"bytes_per_launch": 50459392 + 14682880, "sources": ("prefill.cu", "common.cuh"),
-                "sha": "fec1d9b4cc5c409b", "workload": "causal_prefill"},
+    "prefill": {"bytes_per_launch": 50501120 + 14481664, "sources": ("prefill.cu", "cluster.cuh", "common.cuh", "window.cuh"),
+                "sha": "3c1a1fe95a675dd0", "workload": "causal_prefill"},
     # one ncu capture of the merged Q/K/V projection of 4096 tokens (hidden 4096)
-    "qkv": {"bytes_per_launch": 117790208 + 35780352, "sources": ("qkv.cu", "common.cuh"),
-            "sha": "2966bd0ce22b6d05", "workload": "qkv_append"},
+    "qkv": {"bytes_per_launch": 119868416 + 36024576, "sources": ("qkv.cu", "common.cuh", "tokens.cuh"),
+            "sha": "f9d463300a0b1958", "workload": "qkv_append"},
 }
 
 

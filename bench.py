@@ -57,8 +57,8 @@ TRAFFIC = {
     "decode_fp8": {"bytes_per_launch": 131120640 + 3318016, "sources": ("decode_fp8.cu", "common.cuh", "window.cuh"),
                    "sha": "65191282a7f4f255", "workload": "batched_decode_fp8"},
     # one ncu capture of the causal prefill of 4096 tokens with the prompt's append fused in
-    "prefill": {"bytes_per_launch": 50501120 + 14481664, "sources": ("prefill.cu", "cluster.cuh", "common.cuh", "window.cuh"),
-                "sha": "3c1a1fe95a675dd0", "workload": "causal_prefill"},
+    "prefill": {"bytes_per_launch": 50473216 + 14664192, "sources": ("prefill.cu", "cluster.cuh", "common.cuh", "window.cuh"),
+                "sha": "9dedbf1b6c52a1f1", "workload": "causal_prefill"},
     # one ncu capture of the merged Q/K/V projection of 4096 tokens (hidden 4096)
     "qkv": {"bytes_per_launch": 119868416 + 36024576, "sources": ("qkv.cu", "common.cuh", "tokens.cuh"),
             "sha": "f9d463300a0b1958", "workload": "qkv_append"},

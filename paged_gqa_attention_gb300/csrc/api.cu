@@ -161,31 +161,48 @@ long long window_tiles_bound(int window, int sinks, int max_blocks_per_seq, int 
 // Tiles per split of a windowed decode, whose sequences hold up to `tiles` each: the number of
 // splits n for which a model of its time, fitted to sweeps on GB300, is smallest.  One CTA walks
 // its tiles at the latency of its ring (tile_us each, times `crowded` when CTAs share SMs); all
-// tiles together take at least their bytes' time (stream_us each); the shorter of the two hides
-// about three quarters under the longer.  A merge costs cluster_us within a cluster, else
-// merge_us + merge_each_us a split.  Never more CTAs than two an SM: those past one wave start
-// when others end, and cost more than any split saves (20 sequences, 2048-token window: 28.1 us
-// unsplit, 36.1 us as 320 CTAs).  Measured, in bf16: one sequence and 1024 tokens 4.9 us in 6
-// (unsplit 9.6, in 18 6.1), 8 sequences and 4096 tokens 23.7 us in 4 (unsplit 35.1, in 10 29.9); in 8
-// bits: one sequence and 32768 tokens 22.3 us in 16 (in 8 33.2, in 37 23.6).
+// tiles together take at least their bytes' time (stream_us each).
+//   One wave (two CTAs an SM) or less: the shorter of the two hides about three quarters under the
+// longer.  A merge costs cluster_us within a cluster, else merge_us + merge_each_us a split.
+// Measured, in bf16: one sequence and 1024 tokens 4.9 us in 6 (unsplit 9.6, in 18 6.1), 8 sequences
+// and 4096 tokens 23.7 us in 4 (unsplit 35.1, in 10 29.9); 20 sequences and 2048 tokens 28.1 us
+// unsplit (in 2, 320 CTAs, 36.1); in 8 bits: one sequence and 32768 tokens 22.3 us in 16 (in 8 33.2,
+// in 37 23.6).
+//   More CTAs than that run in waves: the full ones at the rate of their bytes, the last one at least
+// as long as a walk, every one wave_us to start.  So many sequences are split only where few CTAs
+// would be left for a last wave of long walks: 39 sequences and 4096 tokens 103.9 us in 4 (unsplit,
+// 304 CTAs and 8 more, 116.4), but 56 sequences 134.4 unsplit (in 2 137.5) and 40 with 512 tokens
+// 21.5 (in 2 23.8).  Over the 8-bit cache splits saved at most 5 % there and are not tried.
 struct SplitCost {
-    double tile_us, crowded, stream_us, cluster_us, merge_us, merge_each_us;
+    double tile_us, crowded, stream_us, cluster_us, merge_us, merge_each_us, wave_us;
+    int most_waved;      // splits tried where even unsplit sequences fill more than one wave
 };
-constexpr SplitCost kSplitCost = {0.42, 1.0, 0.0049, 1.4, 1.9, 0.07};      // 64 tokens in bf16
-constexpr SplitCost kSplitCostFp8 = {0.78, 1.5, 0.0068, 1e9, 2.3, 0.15};   // 128 in 8 bits (no cluster merge)
+constexpr SplitCost kSplitCost = {0.42, 1.0, 0.0049, 1.4, 1.9, 0.07, 1.5, 5};          // 64 tokens in bf16
+constexpr SplitCost kSplitCostFp8 = {0.78, 1.5, 0.0068, 1e9, 2.3, 0.15, 1.5, 1};       // 128 in 8 bits (no cluster merge)
 
 int auto_window_split(int batch, long long tiles, int num_sms, const SplitCost &c) {
-    const long long pairs = (long long)batch * kHkv;
+    const long long pairs = (long long)batch * kHkv, places = 2LL * num_sms;
     const double stream = c.stream_us * (double)pairs * (double)tiles;
+    const bool waves = pairs > places;
     long long best = tiles;
     double best_us = 0.;
-    for (long long n = 1; n <= tiles && (n == 1 || pairs * n <= 2LL * num_sms); ++n) {
+    for (long long n = 1; n <= tiles && (n == 1 || (waves ? n <= c.most_waved : pairs * n <= places)); ++n) {
         const long long per = (tiles + n - 1) / n;
         const long long splits = (tiles + per - 1) / per;
-        const double walk = c.tile_us * (pairs * splits > num_sms ? c.crowded : 1.0) * (double)per;
-        double us = walk > stream ? walk + 0.25 * stream : stream + 0.25 * walk;
+        const long long ctas = pairs * splits;
+        if (splits > 1 && ctas > kDecodeCtaCap) break;   // what a workspace provides for
+        const double walk = c.tile_us * (ctas > num_sms ? c.crowded : 1.0) * (double)per;
+        double us;
+        if (waves) {
+            const double last = stream * (double)(ctas % places) / (double)ctas;
+            us = stream - last + (ctas % places == 0 ? 0. : walk > last ? walk : last) +
+                 c.wave_us * (double)((ctas + places - 1) / places);
+        } else {
+            us = walk > stream ? walk + 0.25 * stream : stream + 0.25 * walk;
+        }
         if (splits > 1)
-            us += splits <= 8 && c.cluster_us < c.merge_us ? c.cluster_us : c.merge_us + c.merge_each_us * (double)splits;
+            us += !waves && splits <= 8 && c.cluster_us < c.merge_us ? c.cluster_us
+                                                                     : c.merge_us + c.merge_each_us * (double)splits;
         if (n == 1 || us < best_us) {
             best = per;
             best_us = us;

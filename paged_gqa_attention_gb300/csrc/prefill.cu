@@ -103,16 +103,21 @@ struct PrefillSmem {
     uint64_t mma_idle;
     uint32_t tmem_base;
     int abort;
-    union {
-        float ml[2 * kRows][2];                // kSplit: running maximum and sum of every row
-        uint8_t stage[kSoftmaxWarps][32 * 128];   // kWindow: a warp's 32 output rows, 64 dims at a time
-    };
+};
+// After it, in the windowed form only (a larger block of shared memory leaves less L1):
+union WindowSmem {
+    float ml[2 * kRows][2];                   // kSplit: running maximum and sum of every row
+    uint8_t stage[kSoftmaxWarps][32 * 128];   // else: a warp's 32 output rows, 64 dims at a time
 };
 // kSplit: O of the 256 rows, fp32, over q and k
 static_assert(offsetof(PrefillSmem, k) == sizeof(PrefillSmem::q) &&
               sizeof(PrefillSmem::q) + sizeof(PrefillSmem::k) == 2 * kRows * kD * sizeof(float), "split merge area");
 
-constexpr size_t kSmemBytes = sizeof(PrefillSmem) + 1024;
+template <bool kWindow>
+constexpr size_t prefill_smem_bytes() {
+    return sizeof(PrefillSmem) + (kWindow ? sizeof(WindowSmem) : 0) + 1024;
+}
+static_assert(prefill_smem_bytes<true>() <= 232448 && sizeof(PrefillSmem) % 16 == 0, "shared memory");
 
 struct Unit {
     bool run;       // has work
@@ -431,9 +436,10 @@ __device__ __forceinline__ void append_share(const PrefillArgs &a, int lane) {
 // kSplit: merge a share of the unit's rows from the O, m and l that every CTA of the cluster left
 // in its shared memory (a row whose l is 0 saw no key there), and write their outputs.  Warp w takes
 // rows rank + ctas (w + 8i); a lane 4 dims.
-__device__ __forceinline__ void merge_rows(const PrefillArgs &a, const Unit &t, PrefillSmem &sm, int warp, int lane) {
+__device__ __forceinline__ void merge_rows(const PrefillArgs &a, const Unit &t, PrefillSmem &sm, WindowSmem &ws, int warp,
+                                           int lane) {
     const int ctas = a.unit_ctas, rank = (int)(blockIdx.x % ctas);
-    const uint32_t o_base = smem_u32(sm.q), ml_base = smem_u32(sm.ml);
+    const uint32_t o_base = smem_u32(sm.q), ml_base = smem_u32(ws.ml);
     for (int row = rank + ctas * warp; row < 2 * kRows; row += ctas * kSoftmaxWarps) {
         const int x = row >> 7, pl = (row & (kRows - 1)) >> 2, hl = row & 3;   // tile, position, head
         if (x * kTilePos + pl >= t.positions) continue;
@@ -478,6 +484,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
     extern __shared__ uint8_t smem_raw[];
     PrefillSmem &sm = *reinterpret_cast<PrefillSmem *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    WindowSmem &ws = *reinterpret_cast<WindowSmem *>(&sm + 1);   // kWindow only
     volatile int *abort_flag = &sm.abort;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -750,15 +757,23 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         float split_m = -INFINITY, split_l = 0.f;   // kSplit: no key seen so far
         bool split_done = false;
         // (window: a unit's lengths are looked up before the epilogue of the one before it, whose
-        // stores they would otherwise queue behind)
-        Unit next;
+        // stores they would otherwise queue behind; the other forms are compiled without this, which
+        // cost them 0.3 %)
+        [[maybe_unused]] Unit next;
+        [[maybe_unused]] bool fetched = false;
         next.run = false;
-        bool fetched = false;
         for (int r = 0; ok; ++r) {
             const int idx = snake<kSplit>(a, r, total);
             if (idx < 0) break;
-            const Unit t = fetched ? next : unit_for<kPrefix, kPlanned, kAppend, kWindow, kSplit>(a, idx, qblocks);
-            fetched = false;
+            const Unit t = [&]() -> Unit {
+                if constexpr (kWindow && !kSplit) {
+                    const bool have = fetched;
+                    fetched = false;
+                    return have ? next : unit_for<kPrefix, kPlanned, kAppend, kWindow, kSplit>(a, idx, qblocks);
+                } else {
+                    return unit_for<kPrefix, kPlanned, kAppend, kWindow, kSplit>(a, idx, qblocks);
+                }
+            }();
             if (!t.run) continue;
             // the last key each row may see: its own position (causal), or the whole prefix
             const int pos_first = kPrefix ? t.seq_len - 1 : t.pos0 + x * kTilePos;
@@ -952,7 +967,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 // heads' rows of one position, 128 contiguous bytes each: a thread storing its own row
                 // touches 32 lines an instruction, and the stores of a unit took 2300 clk (a tile's
                 // products take 1024, and a short window leaves only a few of them).
-                uint8_t *stg = sm.stage[warp];
+                uint8_t *stg = ws.stage[warp];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
 #pragma unroll
@@ -1042,8 +1057,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 }
                 tc_fence_before();
             }
-            sm.ml[rr][0] = split_m;
-            sm.ml[rr][1] = split_l;
+            ws.ml[rr][0] = split_m;
+            ws.ml[rr][1] = split_l;
         }
     }
 
@@ -1054,7 +1069,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         cluster_sync_all();
         if (warp < kSoftmaxWarps) {
             const Unit t = unit_at<kAppend, kWindow>(a, (int)(blockIdx.x / a.unit_ctas), qblocks);
-            if (t.run) merge_rows(a, t, sm, warp, lane);
+            if (t.run) merge_rows(a, t, sm, ws, warp, lane);
         }
         __syncwarp();
         cluster_sync_all();
@@ -1108,7 +1123,7 @@ cudaError_t launch_prefill_mode(const PrefillArgs &a, const CUtensorMap &q_map, 
     static bool configured[64] = {};
     if (dev < 0 || dev >= 64 || !configured[dev]) {
         e = cudaFuncSetAttribute(prefill_kernel<kPrefix, kPlanned, kAppend, kWindow, kSplit>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prefill_smem_bytes<kWindow>());
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev] = true;
     }
@@ -1137,7 +1152,7 @@ cudaError_t launch_prefill_mode(const PrefillArgs &a, const CUtensorMap &q_map, 
     }
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(kAppend ? kThreadsAppend : kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.dynamicSmemBytes = prefill_smem_bytes<kWindow>();
     return cudaLaunchKernelEx(&cfg, prefill_kernel<kPrefix, kPlanned, kAppend, kWindow, kSplit>, q_map, k_map, v_map,
                               kn_map, vn_map, a);
 }
@@ -1169,7 +1184,7 @@ static cudaError_t split_clusters(int (&out)[9]) {
     for (int c = 2; c <= 8; ++c) {
         int n = known[dev][c].load();
         if (n == 0) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)prefill_smem_bytes<true>());
             if (e != cudaSuccess) return e;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1179,7 +1194,7 @@ static cudaError_t split_clusters(int (&out)[9]) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3((unsigned)c);
             cfg.blockDim = dim3(kThreads);
-            cfg.dynamicSmemBytes = kSmemBytes;
+            cfg.dynamicSmemBytes = prefill_smem_bytes<true>();
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {

@@ -77,6 +77,18 @@ def test_decode_batches_and_padded_rows(batch, fp8):
         assert_lse_close(lse[live.cuda()], ref_lse.numpy(), "window lse")
 
 
+def test_decode_of_more_sequences_than_a_wave_holds():
+    """39 sequences of up to 2500 tokens: 312 (sequence, KV head) pairs on 304 places, which the
+    library splits (a plain workspace is enough)."""
+    lens = [(977 * i + 313) % 2500 + 1 for i in range(38)] + [2500]
+    c = Cache(lens, [1] * 39, 2400, 3, 57).upload()
+    out, lse = decode(c)
+    ref, ref_lse, tol = c.reference()
+    check(out, ref, tol, "out")
+    assert_lse_close(lse, ref_lse.numpy(), "window lse")
+    assert torch.equal(out, decode(c)[0])
+
+
 def test_decode_equals_the_full_decode_under_a_long_window():
     c = Cache([1000, 300, 2000], [1] * 3, 1 << 20, 0, 13).upload()
     ws = ops.make_workspace(3, c.bt.shape[1])

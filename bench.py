@@ -51,11 +51,13 @@ HEAD_START_CYCLES = 200_000      # ~0.1 ms spin so a step's launches are all que
 # whose sources changed since reports traffic null.
 TRAFFIC = {
     # one ncu capture of the batched decode step (32 sequences, 243.9 MB of K/V)
-    "decode": {"bytes_per_launch": 249668864 + 3982848, "sources": ("decode.cu", "cluster.cuh", "common.cuh", "window.cuh"),
+    "decode": {"bytes_per_launch": 249668864 + 3982848,
+               "sources": ("decode.cu", "cluster.cuh", "common.cuh", "window.cuh"),
                "sha": "4ca59ac25fa8f5db", "workload": "batched_decode"},
     # one ncu capture of the fused 8-bit decode step (batch 32, 126 MB of 8-bit K/V)
-    "decode_fp8": {"bytes_per_launch": 131120640 + 3318016, "sources": ("decode_fp8.cu", "common.cuh", "window.cuh"),
-                   "sha": "65191282a7f4f255", "workload": "batched_decode_fp8"},
+    "decode_fp8": {"bytes_per_launch": 131123712 + 3672064,
+                   "sources": ("decode_fp8.cu", "cluster.cuh", "common.cuh", "window.cuh"),
+                   "sha": "e4605bbad48a3bf7", "workload": "batched_decode_fp8"},
     # one ncu capture of the causal prefill of 4096 tokens with the prompt's append fused in
     "prefill": {"bytes_per_launch": 50473216 + 14664192, "sources": ("prefill.cu", "cluster.cuh", "common.cuh", "window.cuh"),
                 "sha": "9dedbf1b6c52a1f1", "workload": "causal_prefill"},

@@ -166,8 +166,9 @@ long long window_tiles_bound(int window, int sinks, int max_blocks_per_seq, int 
 // longer.  A merge costs cluster_us within a cluster, else merge_us + merge_each_us a split.
 // Measured, in bf16: one sequence and 1024 tokens 4.9 us in 6 (unsplit 9.6, in 18 6.1), 8 sequences
 // and 4096 tokens 23.7 us in 4 (unsplit 35.1, in 10 29.9); 20 sequences and 2048 tokens 28.1 us
-// unsplit (in 2, 320 CTAs, 36.1); in 8 bits: one sequence and 32768 tokens 22.3 us in 16 (in 8 33.2,
-// in 37 23.6).
+// unsplit (in 2, 320 CTAs, 36.1); in 8 bits: one sequence and 1024 tokens 6.1 us in 5 (unsplit 10.6, in
+// 10, without a cluster, 7.7), 32768 tokens 21.9 us in 16 (in 8 32.9, in 20 25.2), 16 and 4096 28.7 us
+// in 2 (unsplit 31.8).
 //   More CTAs than that run in waves: the full ones at the rate of their bytes, the last one at least
 // as long as a walk, every one wave_us to start.  So many sequences are split only where few CTAs
 // would be left for a last wave of long walks: 39 sequences and 4096 tokens 103.9 us in 4 (unsplit,
@@ -178,7 +179,7 @@ struct SplitCost {
     int most_waved;      // splits tried where even unsplit sequences fill more than one wave
 };
 constexpr SplitCost kSplitCost = {0.42, 1.0, 0.0049, 1.4, 1.9, 0.07, 1.5, 5};          // 64 tokens in bf16
-constexpr SplitCost kSplitCostFp8 = {0.78, 1.5, 0.0068, 1e9, 2.3, 0.15, 1.5, 1};       // 128 in 8 bits (no cluster merge)
+constexpr SplitCost kSplitCostFp8 = {0.78, 1.8, 0.0053, 1.7, 2.3, 0.15, 1.5, 1};       // 128 tokens in 8 bits
 
 int auto_window_split(int batch, long long tiles, int num_sms, const SplitCost &c) {
     const long long pairs = (long long)batch * kHkv, places = 2LL * num_sms;
@@ -201,8 +202,7 @@ int auto_window_split(int batch, long long tiles, int num_sms, const SplitCost &
             us = walk > stream ? walk + 0.25 * stream : stream + 0.25 * walk;
         }
         if (splits > 1)
-            us += !waves && splits <= 8 && c.cluster_us < c.merge_us ? c.cluster_us
-                                                                     : c.merge_us + c.merge_each_us * (double)splits;
+            us += !waves && splits <= 8 ? c.cluster_us : c.merge_us + c.merge_each_us * (double)splits;
         if (n == 1 || us < best_us) {
             best = per;
             best_us = us;
@@ -754,6 +754,7 @@ static pa_status decode_fp8_impl(pa_shape shape, void *out, float *lse, const vo
     if (win) {
         a.window = win->window;
         a.sinks = win->sinks;
+        a.cluster_merge = nsplit > 1 && nsplit <= 8 && (long long)batch * kHkv * nsplit <= 2LL * sms ? 1 : 0;
         CUtensorMap k16_map, v16_map;
         if (!encode_code_map(&k16_map, k_codes, num_blocks, 16) || !encode_code_map(&v16_map, v_codes, num_blocks, 16))
             return PA_ERR_INVALID_ARG;

@@ -37,6 +37,7 @@
 // 4096 55.9 against 48.9, 1 x 4096 10.1 against 8.7 us).
 #include <atomic>
 
+#include "cluster.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "window.cuh"
@@ -71,6 +72,7 @@ struct DecodeFp8Smem {
     uint64_t empty[kStages];
     int last_cta;
     int poison;
+    float cl_ml[kGroup][2];                    // cluster merge: this split's (m, l) per head
 };
 
 constexpr size_t kSmemBytes = sizeof(DecodeFp8Smem) + 1024;
@@ -88,8 +90,10 @@ __device__ __forceinline__ void v_pairs(uint32_t r, uint32_t &lo, uint32_t &hi) 
     e4m3x4_to_f16x2x2(__byte_perm(r, 0u, 0x3120), lo, hi);
 }
 
-// kWindow: k16_map / v16_map have boxes of 16 rows.
-template <bool kWindow>
+// kWindow: k16_map / v16_map have boxes of 16 rows.  kCluster: the splits of a pair form a cluster
+// and split 0 merges them from its peers' shared memory, as in decode.cu (every CTA, also one
+// without work, meets the others at both barriers).
+template <bool kWindow, bool kCluster>
 __device__ __forceinline__ void decode_fp8_body(const CUtensorMap &k_map, const CUtensorMap &v_map,
                                                 const CUtensorMap &k16_map, const CUtensorMap &v16_map,
                                                 const DecodeArgs &a) {
@@ -101,7 +105,14 @@ __device__ __forceinline__ void decode_fp8_body(const CUtensorMap &k_map, const 
     const int b = pair / kHkv;
     const int g = pair % kHkv;
     // the highest splits start first (longest work first, as in decode.cu)
-    const int split = (int)(gridDim.y - 1 - blockIdx.y);
+    const int split = kCluster ? (int)blockIdx.y : (int)(gridDim.y - 1 - blockIdx.y);
+    const auto leave = [] {
+        if constexpr (kCluster) {
+            __syncwarp();
+            cluster_sync_all();
+            cluster_sync_all();
+        }
+    };
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
@@ -128,6 +139,7 @@ __device__ __forceinline__ void decode_fp8_body(const CUtensorMap &k_map, const 
                 store_out4(static_cast<__nv_bfloat16 *>(a.out) + ((size_t)b * kHq + qh) * kD + lane * 4, zero, 0.f);
                 if (a.lse && lane == 0) a.lse[(size_t)b * kHq + qh] = -INFINITY;
             }
+            leave();
             return;
         }
     }
@@ -135,13 +147,17 @@ __device__ __forceinline__ void decode_fp8_body(const CUtensorMap &k_map, const 
         if (split == 0 && g == 0 && threadIdx.x == 0) record_error(a.err, kErrDevice | kErrBadSeqLen);
         // (a kernel whose CTAs all left here must not complete before the one it depends on)
         if constexpr (kWindow) asm volatile("griddepcontrol.wait;" ::: "memory");
+        leave();
         return;
     }
     const WindowTiles<kTile> wt(kWindow ? a.window : seq_len, kWindow ? a.sinks : 0, seq_len - 1, seq_len - 1);
     const int per_split = a.split_tokens / kTile;
     const int nsplit_b = kWindow ? (wt.n + per_split - 1) / per_split
                                  : (seq_len + a.split_tokens - 1) / a.split_tokens;
-    if (split >= nsplit_b) return;        // past the context
+    if (split >= nsplit_b) {              // past the context
+        leave();
+        return;
+    }
     const int t_begin = split * a.split_tokens;
     const int t_end = min(t_begin + a.split_tokens, seq_len);
     // (window: tiles v_begin .. v_begin + n_tiles - 1 of the list of visible ones)
@@ -209,6 +225,7 @@ __device__ __forceinline__ void decode_fp8_body(const CUtensorMap &k_map, const 
             for (int i = max(0, issued - kStages); i < issued; ++i)
                 mbar_wait(smem_u32(&sm.full[i % kStages]), (i / kStages) & 1);
         }
+        leave();
         return;
     }
 
@@ -470,7 +487,9 @@ __device__ __forceinline__ void decode_fp8_body(const CUtensorMap &k_map, const 
     const int c = threadIdx.x;
     if (c >= kGroup * 32) {
         // the others only take part in the partials' barriers below
-        if (nsplit_b > 1) {
+        if (kCluster) {
+            leave();
+        } else if (nsplit_b > 1) {
             named_barrier(2, kConsumerWarps * 32);
             named_barrier(2, kConsumerWarps * 32);
         }
@@ -497,6 +516,39 @@ __device__ __forceinline__ void decode_fp8_body(const CUtensorMap &k_map, const 
     }
     const int qh = g * kGroup + h;      // query head
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((size_t)b * kHq + qh) * kD + d0;
+
+    if constexpr (kCluster) {
+        // this split's partial into its own shared memory: thread c alone read entries
+        // [.][h][d0 .. d0+3] of the merge arrays, so it may overwrite warp 0's
+        *reinterpret_cast<float4 *>(&sm.mg.o[0][h][d0]) = make_float4(o4[0], o4[1], o4[2], o4[3]);
+        if ((c & 31) == 0) {
+            sm.cl_ml[h][0] = M;
+            sm.cl_ml[h][1] = L;
+        }
+        cluster_sync_all();   // every split's partial is in place
+        if (split == 0) {
+            float GM = M;
+            for (int k = 1; k < nsplit_b; ++k)
+                GM = fmaxf(GM, ld_cluster_f32(peer_addr(smem_u32(&sm.cl_ml[h][0]), (uint32_t)k)));
+            float GL = 0.f, go[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < nsplit_b; ++k) {
+                const float mk = ld_cluster_f32(peer_addr(smem_u32(&sm.cl_ml[h][0]), (uint32_t)k));
+                const float lk = ld_cluster_f32(peer_addr(smem_u32(&sm.cl_ml[h][1]), (uint32_t)k));
+                const float4 ok = ld_cluster_f4(peer_addr(smem_u32(&sm.mg.o[0][h][d0]), (uint32_t)k));
+                const float e = fast_exp2(mk - GM);
+                GL += lk * e;
+                go[0] += ok.x * e;
+                go[1] += ok.y * e;
+                go[2] += ok.z * e;
+                go[3] += ok.w * e;
+            }
+            if (nsplit_b > 1 && !(GL == GL)) GM = GL;   // a poisoned split (its NaN maximum loses in fmaxf)
+            store_out4(out, go, 1.f / GL);
+            if (a.lse && (c & 31) == 0) a.lse[(size_t)b * kHq + qh] = (GM + __log2f(GL)) * kLn2;
+        }
+        cluster_sync_all();   // the peers' shared memory stays until split 0 has read it
+        return;
+    }
 
     if (nsplit_b == 1) {
         store_out4(out, o4, 1.f / L);
@@ -546,14 +598,15 @@ __device__ __forceinline__ void decode_fp8_body(const CUtensorMap &k_map, const 
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 decode_fp8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                   const DecodeArgs a) {
-    decode_fp8_body<false>(k_map, v_map, k_map, v_map, a);
+    decode_fp8_body<false, false>(k_map, v_map, k_map, v_map, a);
 }
 
+template <bool kCluster>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 decode_window_fp8_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
                          const __grid_constant__ CUtensorMap k16_map, const __grid_constant__ CUtensorMap v16_map,
                          const DecodeArgs a) {
-    decode_fp8_body<true>(k_map, v_map, k16_map, v16_map, a);
+    decode_fp8_body<true, kCluster>(k_map, v_map, k16_map, v16_map, a);
 }
 
 cudaError_t launch_fp8(bool window, const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
@@ -566,7 +619,10 @@ cudaError_t launch_fp8(bool window, const DecodeArgs &a, const CUtensorMap &k_ma
     if (dev < 0 || dev >= 64 || !configured[dev].load()) {
         e = cudaFuncSetAttribute(decode_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(decode_window_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(decode_window_fp8_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)kSmemBytes);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(decode_window_fp8_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)kSmemBytes);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(true);
@@ -576,12 +632,26 @@ cudaError_t launch_fp8(bool window, const DecodeArgs &a, const CUtensorMap &k_ma
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return window ? cudaLaunchKernelEx(&cfg, decode_window_fp8_kernel, k_map, v_map, k16_map, v16_map, a)
+    if (window && a.cluster_merge) {
+        if (a.nsplit < 1 || a.nsplit > 8) return cudaErrorInvalidValue;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 1;
+        attr[1].val.clusterDim.y = (unsigned)a.nsplit;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+        e = cudaLaunchKernelEx(&cfg, decode_window_fp8_kernel<true>, k_map, v_map, k16_map, v16_map, a);
+        if (e != cudaErrorLaunchOutOfResources && e != cudaErrorInvalidClusterSize && e != cudaErrorNotSupported &&
+            e != cudaErrorCooperativeLaunchTooLarge)
+            return e;
+        cudaGetLastError();   // the cluster was refused: merge through the workspace instead
+        cfg.numAttrs = 1;
+    }
+    return window ? cudaLaunchKernelEx(&cfg, decode_window_fp8_kernel<false>, k_map, v_map, k16_map, v16_map, a)
                   : cudaLaunchKernelEx(&cfg, decode_fp8_kernel, k_map, v_map, a);
 }
 

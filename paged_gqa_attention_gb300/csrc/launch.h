@@ -64,7 +64,7 @@ struct DecodeArgs {
     // that hold a visible token, split_tokens / tile of them a CTA.
     int32_t window;
     int32_t sinks;
-    // Decode kernel only: 1 = the splits of a (sequence, KV head) form a cluster (nsplit <= 8)
+    // bf16 and windowed decode only: 1 = the splits of a (sequence, KV head) form a cluster (nsplit <= 8)
     // and merge through its shared memory; the counters and partials are not used.
     int32_t cluster_merge;
 };

@@ -59,8 +59,9 @@ TRAFFIC = {
                    "sources": ("decode_fp8.cu", "cluster.cuh", "common.cuh", "window.cuh"),
                    "sha": "e4605bbad48a3bf7", "workload": "batched_decode_fp8"},
     # one ncu capture of the causal prefill of 4096 tokens with the prompt's append fused in
-    "prefill": {"bytes_per_launch": 50473216 + 14664192, "sources": ("prefill.cu", "cluster.cuh", "common.cuh", "window.cuh"),
-                "sha": "9dedbf1b6c52a1f1", "workload": "causal_prefill"},
+    "prefill": {"bytes_per_launch": 50471168 + 14542080,
+                "sources": ("prefill.cu", "cluster.cuh", "common.cuh", "window.cuh"),
+                "sha": "71f3e00f364ce573", "workload": "causal_prefill"},
     # one ncu capture of the merged Q/K/V projection of 4096 tokens (hidden 4096)
     "qkv": {"bytes_per_launch": 119868416 + 36024576, "sources": ("qkv.cu", "common.cuh", "tokens.cuh"),
             "sha": "f9d463300a0b1958", "workload": "qkv_append"},

@@ -1224,7 +1224,9 @@ cudaError_t launch_prefill_window(PrefillArgs a, long long tiles, const CUtensor
     if (a.unit_ctas > 1)
         return launch_prefill_mode<false, false, false, true, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms,
                                                                     stream);
-    if (a.order)
+    // units that all start at once need no order: 4 x 16 tokens, window 64, 6.9 us (8.7 with the
+    // planning kernel)
+    if (a.order && units > num_sms)
         return launch_prefill_mode<false, true, false, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
     return launch_prefill_mode<false, false, false, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
 }

@@ -416,3 +416,35 @@ def test_prefill_of_few_tokens_with_a_bad_block_and_captured():
         g.replay()
         assert torch.equal(out, want)
     ops.check_error(ws)
+
+
+def test_calls_on_two_streams_at_once():
+    """Decode, prefill and append on two streams, each with a workspace of its own, again and again:
+    the results of the same calls made one after another."""
+    a = Cache([1000, 0, 700, 2000], [1] * 4, 300, 5, 61).upload()
+    b = Cache([1500, 900], [200, 70], 400, 33, 63).upload()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(65)
+    y = torch.randn(270, 6144, generator=g, device="cuda").to(torch.bfloat16)
+    rows = [y[:, lo:hi].view(270, -1, 128) for lo, hi in ((0, 4096), (4096, 5120), (5120, 6144))]
+    pools = [[p.clone() for p in b.pools] for _ in range(2)]
+    ws = [ops.make_workspace(4, 16) for _ in range(2)]
+
+    def calls(i):
+        q = ops.paged_rope_append(*rows, *pools[i], b.bt, b.cu, b.lens, ws[i], rope_theta=1e6)
+        return (ops.paged_attn_decode_window(a.qd, *a.pools, a.bt, a.lens, ws[i], window=300, sinks=5),
+                ops.paged_attn_prefill_window(q, *pools[i], b.bt, b.cu, b.lens, 200, ws[i], window=400, sinks=33), q)
+
+    want = calls(0)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(calls(i))
+    torch.cuda.synchronize()
+    for out in got[0] + got[1]:
+        assert all(torch.equal(x, y) for x, y in zip(out, want))
+    for w in ws:
+        ops.check_error(w)

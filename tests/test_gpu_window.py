@@ -448,3 +448,26 @@ def test_calls_on_two_streams_at_once():
         assert all(torch.equal(x, y) for x, y in zip(out, want))
     for w in ws:
         ops.check_error(w)
+
+
+# at most 32 new tokens a sequence: one of a CTA's two row tiles, or a part of one
+@pytest.mark.parametrize("window,sinks", [(1, 0), (100, 4), (128, 0), (300, 16), (513, 200), (1 << 30, 0), (3, 1 << 30)])
+@pytest.mark.parametrize("lens,q_lens", [([1], [1]), ([32], [32]), ([700], [1]), ([1500], [31]),
+                                         ([129, 3000, 5, 257, 64], [32, 17, 0, 1, 32])])
+def test_prefill_of_32_tokens_at_most(lens, q_lens, window, sinks):
+    c = Cache(lens, q_lens, window, sinks, 67).upload()
+    out, lse = prefill(c)
+    ref, ref_lse, tol = c.reference()
+    check(out, ref, tol, "out")
+    assert_lse_close(lse, ref_lse.numpy(), "window lse")
+    assert torch.equal(out, prefill(c)[0])
+
+
+def test_prefill_of_32_tokens_at_most_in_more_sequences_than_sms():
+    """25 sequences x 8 KV heads are more units than SMs: they are dealt to persistent CTAs."""
+    lens = [(977 * i + 313) % 900 + 32 for i in range(25)]
+    c = Cache(lens, [(7 * i) % 33 for i in range(25)], 200, 5, 69).upload()
+    out, lse = prefill(c)
+    ref, ref_lse, tol = c.reference()
+    check(out, ref, tol, "out")
+    assert_lse_close(lse, ref_lse.numpy(), "window lse")

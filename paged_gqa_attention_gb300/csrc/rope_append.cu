@@ -203,10 +203,11 @@ rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
         };
         fetch(g0);
 
-        // cos and sin of this lane's 8 pairs (8j .. 8j+7)
+        // cos and sin of this lane's 8 pairs (8j .. 8j+7).  The positions are checked for every run,
+        // also one that begins at v: v's row goes with k's.
         float c[8], s[8];
         bool known = true;            // the rotation's positions are known and in range
-        if (a.rope && g0 <= kQGroups) {
+        if (a.rope) {
             float p[kMaxRopeAxes];
 #pragma unroll
             for (int x = 0; x < kMaxRopeAxes; ++x)
@@ -218,11 +219,13 @@ rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
             } else {
                 known = pl.pos >= 0;
             }
+            if (g0 <= kQGroups) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 f = freq[8 * j + e];
-                const int ax = axis[8 * j + e];
-                angle_cos_sin(ax == 0 ? p[0] : ax == 1 ? p[1] : p[2], f.x, f.y, c[e], s[e]);
+                for (int e = 0; e < 8; ++e) {
+                    const float2 f = freq[8 * j + e];
+                    const int ax = axis[8 * j + e];
+                    angle_cos_sin(ax == 0 ? p[0] : ax == 1 ? p[1] : p[2], f.x, f.y, c[e], s[e]);
+                }
             }
         }
         if (!known) {

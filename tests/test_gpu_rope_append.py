@@ -347,3 +347,80 @@ def test_8_bit_rows_of_extreme_and_odd_values_are_those_of_kv_append_fp8():
     ops.check_error(ws)
     for a, c in zip(got, want):
         assert torch.equal(a.view(torch.uint8), c.view(torch.uint8))
+
+
+def rows_of(cache, blk, slot, fp8):
+    """The bytes of the cache's rows at (blk, slot), by tensor."""
+    out = []
+    for i, t in enumerate(cache):
+        t = t.transpose(1, 2) if fp8 and i >= 2 else t          # scales are [block][head][slot]
+        out.append(to_cpu(t)[blk, slot].contiguous().view(torch.uint8))
+    return out
+
+
+def random_cache(b, fp8, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    if not fp8:
+        return [torch.randn(t.shape, generator=g, device="cuda").to(torch.bfloat16) for t in (b.k_pool, b.v_pool)]
+    codes, _, scales, _ = ops.fp8_cache(b.num_blocks)
+    return ([torch.randint(0, 120, codes.shape, generator=g, device="cuda", dtype=torch.uint8) for _ in range(2)]
+            + [torch.rand(scales.shape, generator=g, device="cuda") for _ in range(2)])
+
+
+def append_with_an_error(b, q, k, v, cache, fp8, cu=None, lens=None, **kw):
+    """(q_out, error word) of a call whose device-side check records an error."""
+    ws = ops.make_workspace(b.num_seqs, b.max_blocks_per_seq)
+    fn = ops.paged_rope_append_fp8 if fp8 else ops.paged_rope_append
+    out = fn(q, k, v, *cache, b.block_table, b.cu_q_lens if cu is None else cu, b.seq_lens if lens is None else lens,
+             ws, rope_theta=THETA, **kw)
+    with pytest.raises(ops.PagedAttnError) as e:
+        ops.check_error(ws)
+    assert e.value.status == 4
+    return out, e.value.detail
+
+
+def check_only_good_rows_moved(b, before, cache, want, good, fp8):
+    """Rows of the good tokens are those of `want`, a cache that a call without errors wrote; every
+    other byte is what it was."""
+    at = definitions.places(b.block_table.tolist(), b.q_lens_host, b.seq_lens_host)
+    blk, slot = torch.tensor([x[2] for x in at]), torch.tensor([x[3] for x in at])
+    for got, ref in zip(rows_of(cache, blk[good], slot[good], fp8), rows_of(want, blk[good], slot[good], fp8)):
+        assert torch.equal(got, ref), "a good token's row"
+    for i, (was, now) in enumerate(zip(before, cache)):
+        scale = fp8 and i >= 2
+        was, now = (to_cpu(t).transpose(1, 2) if scale else to_cpu(t) for t in (was, now))
+        keep = torch.ones(now.shape[0], 256, dtype=torch.bool)
+        keep[blk[good], slot[good]] = False
+        assert torch.equal(was[keep].contiguous().view(torch.uint8), now[keep].contiguous().view(torch.uint8)), \
+            "bytes outside the good tokens' rows"
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("tokens", [1, 4, 405, 1500])
+def test_a_position_out_of_range_moves_no_cache_byte(tokens, fp8):
+    """Neither the K nor the V row of such a token is written, however the batch is cut into runs
+    (one group a warp up to 405 tokens; at 1500 the runs begin at every group)."""
+    b = batch_of([tokens + 30], [tokens])
+    q, k, v = operands(tokens, 121, merged=True)
+    g = torch.Generator().manual_seed(122)
+    pos = torch.randint(0, 100000, (3, tokens), generator=g, dtype=torch.int32)
+    bad = torch.rand(tokens, generator=g) < 0.4
+    bad[0] = True
+    axis = torch.randint(0, 3, (tokens,), generator=g)
+    far = torch.tensor([2 ** 24, -(2 ** 24), 2 ** 31 - 1, -(2 ** 31)], dtype=torch.int32)
+    wrong = pos.clone()
+    wrong[axis[bad], bad.nonzero().flatten()] = far[torch.arange(int(bad.sum())) % 4]
+    kw = dict(pair_axis=ops.rope_pair_axes((16, 24, 24)))
+    cache = random_cache(b, fp8, 123)
+    before = [t.clone() for t in cache]
+    want = [t.clone() for t in cache]
+    fn = ops.paged_rope_append_fp8 if fp8 else ops.paged_rope_append
+    ws = ops.make_workspace(1, b.max_blocks_per_seq)
+    q_want = fn(q, k, v, *want, b.block_table, b.cu_q_lens, b.seq_lens, ws, rope_theta=THETA, positions=pos.cuda(), **kw)
+    ops.check_error(ws)
+    out, word = append_with_an_error(b, q, k, v, cache, fp8, positions=wrong.cuda(), **kw)
+    good = ~bad
+    assert word & (1 << 12)
+    assert to_cpu(out)[bad].isnan().all() and torch.equal(to_cpu(out)[good], to_cpu(q_want)[good])
+    check_only_good_rows_moved(b, before, cache, want, good, fp8)

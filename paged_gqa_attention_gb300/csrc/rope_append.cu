@@ -125,11 +125,12 @@ __device__ __forceinline__ Place place_of(const RopeAppendArgs &a, int t, int la
         q1 = __ldg(a.cu_q_lens + s + 1);
         seq_len = __ldg(a.seq_lens + s);
     }
-    const int q_len = q1 - q0;
-    if (t < q0 || t >= q1) {
+    // (offsets outside the batch first: with q0 near -2^31 the differences below would wrap)
+    if (q0 < 0 || q1 > a.total_tokens || t < q0 || t >= q1) {
         if (report) record_error(a.err, kErrDevice | kErrBadCuQ);
         return pl;
     }
+    const int q_len = q1 - q0;
     if (seq_len < q_len || seq_len > a.max_blocks_per_seq * kBlock) {
         if (report) record_error(a.err, kErrDevice | kErrBadSeqLen);
         return pl;
@@ -162,9 +163,10 @@ rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
         freq[threadIdx.x] = make_float2(a.freq_hi[threadIdx.x], a.freq_lo[threadIdx.x]);
         axis[threadIdx.x] = a.pair_axis[threadIdx.x];
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0 &&
-        (__ldg(a.cu_q_lens) != 0 || __ldg(a.cu_q_lens + a.num_seqs) > a.total_tokens))
-        record_error(a.err, kErrDevice | kErrBadCuQ);
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        const int end = __ldg(a.cu_q_lens + a.num_seqs);
+        if (__ldg(a.cu_q_lens) != 0 || end < 0 || end > a.total_tokens) record_error(a.err, kErrDevice | kErrBadCuQ);
+    }
     __syncthreads();
 
     const long long groups = (long long)a.total_tokens * kGroups;

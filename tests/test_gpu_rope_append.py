@@ -424,3 +424,45 @@ def test_a_position_out_of_range_moves_no_cache_byte(tokens, fp8):
     assert word & (1 << 12)
     assert to_cpu(out)[bad].isnan().all() and torch.equal(to_cpu(out)[good], to_cpu(q_want)[good])
     check_only_good_rows_moved(b, before, cache, want, good, fp8)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_inconsistent_lengths_and_offsets_move_no_other_cache_byte(fp8):
+    """Tokens of a sequence whose length or whose offsets are inconsistent get a NaN q row and no
+    cache row; the other tokens' rows are as in a batch without errors."""
+    b = batch_of([300, 300], [2, 2])
+    q, k, v = operands(4, 141, merged=True)
+    start = random_cache(b, fp8, 142)
+    want = [t.clone() for t in start]
+    fn = ops.paged_rope_append_fp8 if fp8 else ops.paged_rope_append
+    ws = ops.make_workspace(2, b.max_blocks_per_seq)
+    q_want = fn(q, k, v, *want, b.block_table, b.cu_q_lens, b.seq_lens, ws, rope_theta=THETA)
+    ops.check_error(ws)
+    low, high = -(2 ** 31), 2 ** 31 - 1
+    cases = [(dict(lens=[300, n]), 1 << 9, [True, True, False, False]) for n in (1, 0, -5, 257 * 256, low, high)]
+    first, second = [False, False, True, True], [True, True, False, False]
+    cases += [(dict(cu=[0, 2, 9]), 1 << 10, second), (dict(cu=[0, 2, high]), 1 << 10, second),
+              (dict(cu=[-1, 2, 4]), 1 << 10, first), (dict(cu=[low, 2, 4]), 1 << 10, first),
+              (dict(cu=[low, 2, 4], lens=[1, 300]), 1 << 10, first),
+              (dict(cu=[low + 500, 2, 4], lens=[low + 1, 300]), 1 << 10, first)]
+    for change, bit, good in cases:
+        change = {n: torch.tensor(x, dtype=torch.int32, device="cuda") for n, x in change.items()}
+        cache = [t.clone() for t in start]
+        out, word = append_with_an_error(b, q, k, v, cache, fp8, **change)
+        good = torch.tensor(good)
+        assert word & bit, change
+        assert to_cpu(out)[~good].isnan().all() and torch.equal(to_cpu(out)[good], to_cpu(q_want)[good]), change
+        check_only_good_rows_moved(b, start, cache, want, good, fp8)
+
+
+def test_a_negative_end_of_the_batch_is_an_error():
+    b = batch_of([300, 300], [2, 2])
+    q, k, v = operands(4, 151, merged=True)
+    for last in (-1, -(2 ** 31)):
+        cache = random_cache(b, False, 152)
+        before = [t.clone() for t in cache]
+        cu = torch.tensor([0, 0, last], dtype=torch.int32, device="cuda")
+        out = torch.full((4, 32, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        _, word = append_with_an_error(b, q, k, v, cache, False, cu=cu, q_out=out)
+        assert word & (1 << 10)
+        assert all(torch.equal(x, y) for x, y in zip(cache, before)) and (out == 7.0).all()

@@ -212,7 +212,7 @@ pa_status paged_qkv_append_qknorm(pa_shape shape, int32_t hidden, float rope_the
  * and records PA_ERR_DEVICE; one whose sequence data are inconsistent gets no K/V row either
  * and, where the cache position is its rotation's, a NaN q row.
  * paged_rope_append_fp8 writes the 8-bit cache (below): a k row is quantised from its rotated
- * fp32 values, a v row as kv_append_fp8 does.
+ * fp32 values (a scale that would round to 0 is 2^-149 instead), a v row as kv_append_fp8 does.
  */
 pa_status paged_rope_append(pa_shape shape, float rope_theta, const int32_t *positions, int32_t axes,
                             const uint8_t *pair_axis, const void *q_norm_weight,

@@ -81,7 +81,9 @@ __device__ __forceinline__ void store_row8(uint8_t *codes, float *scale_slot, in
     for (int e = 0; e < 8; ++e) amax = fmax3(amax, fabsf(lo[e]), fabsf(hi[e]));
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+    // (a normalised k row of at most 2^-141.2 would get the scale 0, and NaN codes: it gets the
+    // smallest scale there is, by which its values are at most 224)
+    const float scale = amax > 0.f ? fmaxf(__fdiv_rn(amax, 448.f), 0x1p-149f) : 1.f;
     // a row of extreme values is brought to the middle of the exponents first, which changes no
     // quotient; by an infinite scale every finite value gives 0 (s = r = 0 below), inf gives NaN
     float s = scale;

@@ -466,3 +466,33 @@ def test_a_negative_end_of_the_batch_is_an_error():
         _, word = append_with_an_error(b, q, k, v, cache, False, cu=cu, q_out=out)
         assert word & (1 << 10)
         assert all(torch.equal(x, y) for x, y in zip(cache, before)) and (out == 7.0).all()
+
+
+def test_a_k_row_too_small_for_its_scale_is_kept():
+    """Normalised K rows of at most 2^-141.2, whose maximum / 448 rounds to 0 in fp32: no NaN codes.
+    Such a row is quantised by the smallest scale there is, 2^-149.  A value is off by its code's
+    half step, 2^-4 of it, and by fp32's at its size: y = x * factor * gain is rounded to a
+    multiple of 2^-149 once, on top of FP32's relative error."""
+    t = 6
+    b = batch_of([t + 9], [t])
+    q, k, v = operands(t, 131, merged=False)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(132)
+    size = torch.tensor([0.0, 1.0, 3.0, 30.0, 100.0, 200.0], device="cuda")     # of the largest, in 2^-149
+    x = torch.rand(t, 8, 128, generator=g, device="cuda") * 2 - 1
+    x[..., 5], x[..., 100], x[..., 7] = 1.0, -1.0, 0.0
+    # x * 2^-120 * (1 / sqrt(eps = 1)) * 2^-29: the mean square of 2^-120 vanishes beside eps
+    k.copy_((x * size[:, None, None] * 2.0 ** -120).to(torch.bfloat16))
+    gain = torch.full((128,), 2.0 ** -29, dtype=torch.bfloat16, device="cuda")
+    cache = ops.fp8_cache(b.num_blocks)
+    ws = ops.make_workspace(1, b.max_blocks_per_seq)
+    ops.paged_rope_append_fp8(q, k, v, *cache, b.block_table, b.cu_q_lens, b.seq_lens, ws, rope_theta=0.0,
+                              q_norm_weight=gain, k_norm_weight=gain, norm_eps=1.0)
+    ops.check_error(ws)
+    at = definitions.places(b.block_table.tolist(), b.q_lens_host, b.seq_lens_host)
+    blk, slot = torch.tensor([x[2] for x in at]), torch.tensor([x[3] for x in at])
+    ref, _ = definitions.rotated(to_cpu(k), torch.zeros(t), 0.0, gain=to_cpu(gain), eps=1.0)
+    scale = to_cpu(cache[2])[blk, :, slot].double()
+    got = to_cpu(cache[0])[blk, slot].view(torch.float8_e4m3fn).double() * scale[..., None]
+    assert (scale[0] == 1).all() and (scale[1:] == 2.0 ** -149).all()
+    assert ((got - ref).abs() <= 2.0 ** -4 * ref.abs() + (1 + 2.0 ** -4) * (2.0 ** -150 + FP32 * ref.abs())).all()

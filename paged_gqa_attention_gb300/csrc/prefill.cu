@@ -1173,7 +1173,7 @@ cudaError_t launch_prefill(const PrefillArgs &a, const CUtensorMap &q_map, const
 }
 
 // How many clusters of c CTAs of the split kernel fit on the current device at once, c = 2 .. 8
-// (looked up on the first call per device).
+// (looked up once per device; a lookup that failed counts as none and is made again next time).
 static cudaError_t split_clusters(int (&out)[9]) {
     static std::atomic<int> known[64][9];
     int dev = 0;
@@ -1198,8 +1198,9 @@ static cudaError_t split_clusters(int (&out)[9]) {
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
-                cudaGetLastError();   // this size is not to be had: it is not used
-                n = 0;
+                cudaGetLastError();
+                out[c] = 0;
+                continue;
             }
             n = n > 0 ? n : -1;
             known[dev][c].store(n);
@@ -1221,9 +1222,15 @@ cudaError_t launch_prefill_window(PrefillArgs a, long long tiles, const CUtensor
         if (e != cudaSuccess) return e;
         a.unit_ctas = unit_ctas_for(units, tiles, std::min(a.max_q_len, kUnitPos), num_sms, clusters);
     }
-    if (a.unit_ctas > 1)
-        return launch_prefill_mode<false, false, false, true, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms,
-                                                                    stream);
+    if (a.unit_ctas > 1) {
+        const cudaError_t e = launch_prefill_mode<false, false, false, true, true>(a, q_map, k_map, v_map, k16_map,
+                                                                                   v16_map, num_sms, stream);
+        if (e != cudaErrorLaunchOutOfResources && e != cudaErrorInvalidClusterSize && e != cudaErrorNotSupported &&
+            e != cudaErrorCooperativeLaunchTooLarge)
+            return e;
+        cudaGetLastError();   // the clusters were refused: one CTA a unit instead
+        a.unit_ctas = 1;
+    }
     // units that all start at once need no order: 4 x 16 tokens, window 64, 6.9 us (8.7 with the
     // planning kernel)
     if (a.order && units > num_sms)

@@ -14,6 +14,8 @@ import os
 
 import torch
 
+from . import build
+
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpagedattn.so")
 
 NUM_Q_HEADS, NUM_KV_HEADS, HEAD_DIM, BLOCK_SIZE = 32, 8, 128, 256
@@ -156,6 +158,11 @@ def _usual():
         path = os.path.join(os.path.dirname(_LIB_PATH), "_binding.so")
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing: build it with `python -m paged_gqa_attention_gb300.build`")
+        abi = os.path.splitext(path)[0] + ".abi"
+        built_for = open(abi).read() if os.path.exists(abi) else "an unknown PyTorch"
+        if built_for != build.binding_abi():
+            raise RuntimeError(f"{path} was built for {built_for}, this is {build.binding_abi()}: build it again with "
+                               "`python -m paged_gqa_attention_gb300.build`")
         spec = importlib.util.spec_from_file_location("_binding", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

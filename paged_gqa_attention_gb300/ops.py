@@ -365,6 +365,22 @@ def rope_pair_axes(sections, interleaved: bool = False) -> bytes:
     return axes
 
 
+def _pair_axes(pair_axis) -> bytes | None:
+    """pair_axis (bytes or any sequence of 64 axes) as bytes."""
+    if pair_axis is None:
+        return None
+    if type(pair_axis) is not bytes:
+        try:
+            pair_axis = bytes(list(pair_axis))      # (bytes(n) of an integer would be n zeros)
+        except TypeError:
+            raise TypeError(f"pair_axis must be a sequence of {ROPE_PAIRS} axes, got {pair_axis!r}") from None
+        except ValueError:
+            raise ValueError(f"pair_axis must name axes 0 to 2, got {pair_axis!r}") from None
+    if len(pair_axis) != ROPE_PAIRS:
+        raise ValueError(f"pair_axis must name {ROPE_PAIRS} axes, got {len(pair_axis)}")
+    return pair_axis
+
+
 def _need_table(block_table, dev):
     """(sequences, width) of a block table."""
     _need(block_table, "block_table", torch.int32, None, dev)
@@ -415,8 +431,6 @@ def _rope_append(name, fn, q, k_new, v_new, cache, block_table, cu_q_lens, seq_l
         axes = positions.shape[0] if positions.dim() > 1 else 1
         _need(positions, "positions", torch.int32, (axes, tokens) if positions.dim() > 1 else (tokens,), dev)
         positions = positions.data_ptr()
-    if pair_axis is not None and len(pair_axis) != ROPE_PAIRS:
-        raise ValueError(f"pair_axis must name {ROPE_PAIRS} axes")
     if q_norm_weight is not None and k_norm_weight is not None:
         _need(q_norm_weight, "q_norm_weight", torch.bfloat16, (HEAD_DIM,), dev)
         _need(k_norm_weight, "k_norm_weight", torch.bfloat16, (HEAD_DIM,), dev)
@@ -445,8 +459,7 @@ def paged_rope_append(q, k_new, v_new, k_pool, v_pool, block_table, cu_q_lens, s
     positions (int32 [T] or [axes, T]) replace the cache positions in the rotation; with several
     axes, pair_axis (rope_pair_axes) names the axis of each of the 64 pairs.  q_out may be q
     itself.  Tokens behind the last sequence are left alone."""
-    if pair_axis is not None:
-        pair_axis = bytes(pair_axis)
+    pair_axis = _pair_axes(pair_axis)
     if stream is None:
         got = (_binding or _usual()).rope_append(False, q, k_new, v_new, k_pool, v_pool, None, None, block_table,
                                                  cu_q_lens, seq_lens, workspace, rope_theta, positions, pair_axis,
@@ -465,8 +478,7 @@ def paged_rope_append_fp8(q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, b
                           stream=None) -> torch.Tensor:
     """paged_rope_append into the 8-bit cache (fp8_cache): k rows quantised from their rotated
     fp32 values, v rows as kv_append_fp8 does."""
-    if pair_axis is not None:
-        pair_axis = bytes(pair_axis)
+    pair_axis = _pair_axes(pair_axis)
     if stream is None:
         got = (_binding or _usual()).rope_append(True, q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, block_table,
                                                  cu_q_lens, seq_lens, workspace, rope_theta, positions, pair_axis,

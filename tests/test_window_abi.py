@@ -212,3 +212,18 @@ def test_the_binding_fails_loudly_when_it_is_missing(lib, monkeypatch, tmp_path)
     monkeypatch.setattr(ops, "_LIB_PATH", str(tmp_path / "missing.so"))
     with pytest.raises(RuntimeError, match="_binding.so is missing"):
         ops._usual()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("axes", [64, True, 0, -1], ids=str)
+def test_pair_axis_must_name_the_axes(axes, fp8):
+    """An integer is refused, not taken as that many zeros."""
+    t = torch.zeros(1, 32, 128, dtype=torch.bfloat16)
+    cache = [t] * (4 if fp8 else 2)
+    fn = ops.paged_rope_append_fp8 if fp8 else ops.paged_rope_append
+    with pytest.raises(TypeError, match="pair_axis"):
+        fn(t, t, t, *cache, t, t, t, t, rope_theta=1e6, positions=t, pair_axis=axes)
+    with pytest.raises(ValueError, match="pair_axis"):
+        fn(t, t, t, *cache, t, t, t, t, rope_theta=1e6, positions=t, pair_axis=[0] * 63)
+    with pytest.raises(ValueError, match="pair_axis"):
+        fn(t, t, t, *cache, t, t, t, t, rope_theta=1e6, positions=t, pair_axis=[0] * 63 + [256])

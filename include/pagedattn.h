@@ -508,9 +508,10 @@ pa_status paged_attn_prefill(pa_shape shape, void *out, float *lse, const void *
  * paged_attn_prefill_window: paged_attn_prefill with a sliding window and sinks (the rule above,
  * p each new token's position).  Arguments, workspace and errors as for paged_attn_prefill; the
  * table entries of blocks that none of a sequence's new tokens sees are not used.  With few
- * tokens a cluster of CTAs shares each work unit and merges by log-sum-exp.  A NaN or
- * infinity in a V row that some of the 64 positions of a work unit see and others do not may
- * reach the outputs of all 64.
+ * tokens a cluster of CTAs shares each work unit and merges by log-sum-exp.  A work unit is 64
+ * consecutive new tokens of a sequence, counted from its first one.  A NaN or infinity in a V row
+ * that some of a unit's tokens see and others do not may reach the outputs of all 64; what none of
+ * them sees reaches none.
  */
 pa_status paged_attn_prefill_window(pa_shape shape, void *out, float *lse, const void *q,
                                     const void *k_pool, const void *v_pool,

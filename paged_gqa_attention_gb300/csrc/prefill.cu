@@ -105,9 +105,12 @@ struct PrefillSmem {
     int abort;
 };
 // After it, in the windowed form only (a larger block of shared memory leaves less L1):
-union WindowSmem {
-    float ml[2 * kRows][2];                   // kSplit: running maximum and sum of every row
-    uint8_t stage[kSoftmaxWarps][32 * 128];   // else: a warp's 32 output rows, 64 dims at a time
+struct WindowSmem {
+    union {
+        float ml[2 * kRows][2];                   // kSplit: running maximum and sum of every row
+        uint8_t stage[kSoftmaxWarps][32 * 128];   // else: a warp's 32 output rows, 64 dims at a time
+    };
+    uint64_t v_landed;                            // a V tile with dead rows is there (load_list_tile)
 };
 // kSplit: O of the 256 rows, fp32, over q and k
 static_assert(offsetof(PrefillSmem, k) == sizeof(PrefillSmem::q) &&
@@ -337,11 +340,12 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
 
 // Sliding window: fetch rows c0 .. c0 + 127 of the unit's key list into a tile, as boxes of 64
 // and 16 rows that end at the block's edge or with the sinks.  Rows whose group of 16 lies past
-// the context are not fetched (they are masked, and their V rows zeroed by the softmax warps).
+// the unit's last position are not fetched; those and the others that no position of the unit sees
+// (dead rows) are masked in the scores and zeroed in V (zero_dead_rows).
 __device__ __forceinline__ void load_list_tile(const PrefillArgs &a, const Unit &t, const int32_t *bt, int c0,
                                                uint8_t (*dst)[kHalf], uint32_t bar, const CUtensorMap *map64,
                                                const CUtensorMap *map16, bool report) {
-    const int rows = min(kKT, ((t.seq_len - t.win.shift + 15) & ~15) - c0);
+    const int rows = min(kKT, ((t.win.rows + 15) & ~15) - c0);
     mbar_arrive_expect_tx(bar, (uint32_t)rows * kRowBytes);
     for (int r = 0; r < rows;) {
         const int p = t.win.position(c0 + r);
@@ -363,6 +367,34 @@ __device__ __forceinline__ void load_list_tile(const PrefillArgs &a, const Unit 
             run -= n;
         }
     }
+}
+
+// The rows of a tile of the list that no position of the unit sees: from `tail` on (past the last
+// position), and lo .. hi - 1 (behind the sinks and before every position's window).  Their V rows
+// may hold anything, NaN included; P is 0 there, but 0 * NaN is not.
+struct DeadRows {
+    int lo, hi, tail;
+
+    __device__ __forceinline__ DeadRows(const WindowRows &w, int c0) {
+        lo = max(w.s - c0, 0);
+        hi = min(w.lo - w.shift - c0, kKT);
+        tail = min(w.rows - c0, kKT);
+    }
+    __device__ __forceinline__ bool any() const { return lo < hi || tail < kKT; }
+};
+
+// One warp, 512 contiguous bytes (4 rows' halves) an access.
+__device__ __forceinline__ void zero_dead_rows(const DeadRows &d, uint8_t (*v)[kHalf], int lane) {
+    const auto zero = [&](int from, int to) {
+        for (int r = from + (lane >> 3); r < to; r += 4) {
+            const int at = r * 128 + (lane & 7) * 16;
+            *reinterpret_cast<uint4 *>(v[0] + at) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4 *>(v[1] + at) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    zero(d.lo, d.hi);
+    zero(d.tail, kKT);
+    fence_proxy_async_smem();   // generic writes -> visible to the MMA's reads
 }
 
 // The fused append's warp: this CTA's share of the new tokens' K and V rows (2 KiB each, all
@@ -509,6 +541,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
             mbar_init(smem_u32(&sm.o_done[x]), 1);
         }
         mbar_init(smem_u32(&sm.mma_idle), 1);
+        if constexpr (kWindow) mbar_init(smem_u32(&ws.v_landed), 1);
         sm.abort = 0;
         fence_barrier_init();
     }
@@ -548,6 +581,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
         const CUtensorMap *new_map = qk ? &kn_map : &vn_map;
         int tcount = 0, it = 0;              // units / key tiles started
         int q_issued = 0, kv_issued = 0;
+        [[maybe_unused]] int landed = 0;     // V tiles with dead rows
         bool ok = true;
         for (int r = 0; ok; ++r) {
             const int idx = snake<kSplit>(a, r, total);
@@ -580,9 +614,25 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                         !(ok = __all_sync(0xffffffffu, wait_or_abort(smem_u32(&empty[st]), ((it / ns) - 1) & 1,
                                                                     abort_flag, a.err))))
                         break;
-                    if (leader) load_list_tile(a, t, bt, jg * kKT, qk ? sm.k[st] : sm.v[st], smem_u32(&full[st]), map,
-                                               new_map, qk);
+                    // A V tile with dead rows (nearly every unit's last one) lands on a barrier of its
+                    // own; its readers are let in when this warp has zeroed them.  Zeroed by the softmax
+                    // warps, whose chain every tile waits for, they cost 1 us a unit: 16384 tokens
+                    // 237 us at window 1024 and 638 at 4096, here 213 and 587.
+                    const DeadRows dead(t.win, jg * kKT);
+                    const bool clean = qk || !dead.any();
+                    const uint32_t bar = smem_u32(clean ? &full[st] : &ws.v_landed);
+                    if (leader) load_list_tile(a, t, bt, jg * kKT, qk ? sm.k[st] : sm.v[st], bar, map, new_map, qk);
                     __syncwarp();
+                    if (!clean) {
+                        const uint32_t parity = landed++ & 1;
+                        if (!(ok = __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, a.err)))) {
+                            mbar_wait(bar, parity);   // drain, as below
+                            break;
+                        }
+                        zero_dead_rows(dead, sm.v[st], lane);
+                        __syncwarp();
+                        if (leader) mbar_arrive(smem_u32(&full[st]));
+                    }
                     ++kv_issued;
                     continue;
                 }
@@ -797,7 +847,6 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 int base = jg * kKT, kv_valid = t.seq_len - jg * kKT;   // rows 0 .. kv_valid-1 are keys
                 // window: list row r beyond the sinks holds position r + win.shift; bounds on
                 // positions become bounds on rows by subtracting it
-                if constexpr (kWindow) kv_valid -= t.win.shift;
                 const int shift = kWindow ? t.win.shift : 0;
                 if constexpr (kAppend) {
                     int limit;
@@ -892,14 +941,12 @@ prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant_
                 // positions, or rows of another sequence in k_new) may hold anything, NaN
                 // included; P is 0 there but 0 * NaN is not, so tile A (the V tile's first
                 // reader) zeroes them.
-                // (window: also the rows before every query's window and behind the sinks, which
-                // may have been dropped)
-                const bool hidden = kWindow && base + shift < t.win.lo && base + kKT > t.win.s;
-                if (x == 0 && (kv_valid < kKT || hidden)) {
+                // (window: the V producer has zeroed them)
+                if (!kWindow && x == 0 && kv_valid < kKT) {
                     const int vs = it % kVStages;
                     ok = wait_or_abort(smem_u32(&sm.v_full[vs]), (it / kVStages) & 1, abort_flag, a.err);
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-                    if (row >= kv_valid || (hidden && base + row + shift < t.win.lo && base + row >= t.win.s)) {
+                    if (row >= kv_valid) {
                         uint4 *r0 = reinterpret_cast<uint4 *>(sm.v[vs][0] + row * 128);
                         uint4 *r1 = reinterpret_cast<uint4 *>(sm.v[vs][1] + row * 128);
 #pragma unroll

@@ -471,3 +471,59 @@ def test_prefill_of_32_tokens_at_most_in_more_sequences_than_sms():
     ref, ref_lse, tol = c.reference()
     check(out, ref, tol, "out")
     assert_lse_close(lse, ref_lse.numpy(), "window lse")
+
+
+# new tokens' sequences: one whose units a cluster shares each, one of many units, several in a planned order
+NAN_CASES = [([300], [130], 40, 4), ([900], [700], 200, 5), ([700], [700], 1 << 30, 0), ([700], [700], 64, 100),
+             ([1500, 900, 800], [700, 640, 333], 129, 17)]
+
+
+def nan_rows(c, s, p, keys, values):
+    """Pools with the K and / or V row of sequence s at position p set to NaN."""
+    pools = [t.clone() for t in c.pools]
+    for t, on in zip(pools, (keys, values)):
+        if on:
+            t[int(c.table[s, p // 256]), p % 256] = float("nan")
+    return pools
+
+
+def prefill_of(c, pools):
+    ws = ops.make_workspace(len(c.seq_lens), c.bt.shape[1])
+    out = ops.paged_attn_prefill_window(c.qd, *pools, c.bt, c.cu, c.lens, max(c.q_lens), ws, window=c.window, sinks=c.sinks)
+    ops.check_error(ws)
+    return out
+
+
+@pytest.mark.parametrize("lens,q_lens,window,sinks", NAN_CASES)
+def test_prefill_nan_rows_reach_no_unit_that_does_not_see_them(lens, q_lens, window, sinks):
+    """K and V of one new token are NaN: the outputs of every 64 new tokens of which none sees it keep
+    their bits, those of its own sequence before it and behind its window, and the other sequences'."""
+    c = Cache(lens, q_lens, window, sinks, 171).upload()
+    clean = prefill_of(c, c.pools)
+    for s, (n, m) in enumerate(zip(lens, q_lens)):
+        for i in sorted({x for x in (0, 2, 63, 64, 65, 127, 128, 191, 200, m // 2, m - 2, m - 1) if x < m}):
+            p = n - m + i
+            out = prefill_of(c, nan_rows(c, s, p, True, True))
+            sees = torch.zeros(sum(q_lens), dtype=torch.bool)
+            t0 = sum(q_lens[:s])
+            for u in range(0, m, 64):
+                first, last = n - m + u, n - m + min(u + 64, m) - 1
+                if last >= p and (p < sinks or first < p + window):
+                    sees[t0 + u:t0 + min(u + 64, m)] = True
+            assert torch.equal(out[~sees.cuda()], clean[~sees.cuda()]), (s, p)
+            assert out[t0 + i].isnan().all()
+
+
+@pytest.mark.parametrize("lens,q_lens,window,sinks", NAN_CASES)
+def test_prefill_nan_keys_reach_no_position_that_does_not_see_them(lens, q_lens, window, sinks):
+    c = Cache(lens, q_lens, window, sinks, 172).upload()
+    clean = prefill_of(c, c.pools)
+    for s, (n, m) in enumerate(zip(lens, q_lens)):
+        for i in sorted({x for x in (0, 2, 63, 64, 65, 127, 128, 191, 200, m // 2, m - 2, m - 1) if x < m}):
+            p = n - m + i
+            out = prefill_of(c, nan_rows(c, s, p, True, False))
+            sees = torch.zeros(sum(q_lens), dtype=torch.bool)
+            at = torch.arange(n - m, n)
+            sees[sum(q_lens[:s]):sum(q_lens[:s + 1])] = (at >= p) & ((p < sinks) | (at < p + window))
+            assert torch.equal(out[~sees.cuda()], clean[~sees.cuda()]), (s, p)
+            assert out[sees.cuda()].isnan().all()

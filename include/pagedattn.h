@@ -487,7 +487,8 @@ pa_status paged_attn_decode_static(pa_shape shape, void *out, float *lse, const 
  * [P1 §4.4.1; P3 §3.3].  New token i of sequence s sits at absolute position
  * p = seq_lens[s] - q_len + i and attends to context positions 0..p (its own key
  * included).  A sequence with q_len 0 is skipped.  max_q_len must bound every
- * q_len (checked on the device).  lse may be NULL.
+ * q_len (checked on the device).  lse may be NULL.  scale > 0 (else PA_ERR_INVALID_ARG, as in
+ * the other prefill calls: masked scores are -infinity before they are scaled).
  * The workspace needs only its error word (256 bytes).  With several sequences and a
  * workspace of pa_workspace_bytes() size, a planning kernel first sorts the work
  * units (64 positions x one KV head) by the number of key tiles they visit, into the

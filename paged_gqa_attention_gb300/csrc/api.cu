@@ -993,7 +993,7 @@ static pa_status prefill_impl(pa_shape shape, void *out, float *lse, const void 
                               const Window *win = nullptr) {
     if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
     if (num_seqs < 0 || total_tokens < 0 || max_q_len < 0 || max_blocks_per_seq < 1 || num_blocks < 1 ||
-        !std::isfinite(scale) || (num_seqs == 0 && total_tokens != 0) || max_q_len > total_tokens ||
+        !std::isfinite(scale) || !(scale > 0.f) || (num_seqs == 0 && total_tokens != 0) || max_q_len > total_tokens ||
         (total_tokens > 0 && max_q_len == 0))
         return PA_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < kHeaderBytes || !aligned16(workspace)) return PA_ERR_INVALID_ARG;

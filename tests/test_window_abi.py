@@ -227,3 +227,14 @@ def test_pair_axis_must_name_the_axes(axes, fp8):
         fn(t, t, t, *cache, t, t, t, t, rope_theta=1e6, positions=t, pair_axis=[0] * 63)
     with pytest.raises(ValueError, match="pair_axis"):
         fn(t, t, t, *cache, t, t, t, t, rope_theta=1e6, positions=t, pair_axis=[0] * 63 + [256])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.0, -0.1, -1e-30, float("inf"), float("-inf")])
+def test_prefill_refuses_a_scale_that_is_not_positive(lib, scale):
+    """Its masked scores are -infinity before they are scaled."""
+    p = Addresses()
+    base = [p(4), 1, 1, p(5), p(6), 1, 4, 4]                          # block table .. max_q_len
+    tail = [scale, p(7), 1024, None]
+    assert lib.paged_attn_prefill_window(ops.SHAPE, p(0), None, p(1), p(2), p(3), *base, 4, 1, *tail) == 1
+    assert lib.paged_attn_prefill(ops.SHAPE, p(0), None, p(1), p(2), p(3), *base, *tail) == 1
+    assert lib.paged_attn_prefill_append(ops.SHAPE, p(0), None, p(1), p(8), p(9), p(2), p(3), *base, *tail) == 1

@@ -55,13 +55,13 @@ TRAFFIC = {
                "sources": ("decode.cu", "cluster.cuh", "common.cuh", "window.cuh"),
                "sha": "4ca59ac25fa8f5db", "workload": "batched_decode"},
     # one ncu capture of the fused 8-bit decode step (batch 32, 126 MB of 8-bit K/V)
-    "decode_fp8": {"bytes_per_launch": 131123712 + 3672064,
+    "decode_fp8": {"bytes_per_launch": 131144960 + 3577600,
                    "sources": ("decode_fp8.cu", "cluster.cuh", "common.cuh", "window.cuh"),
-                   "sha": "e4605bbad48a3bf7", "workload": "batched_decode_fp8"},
+                   "sha": "790e2d839b28aa14", "workload": "batched_decode_fp8"},
     # one ncu capture of the causal prefill of 4096 tokens with the prompt's append fused in
-    "prefill": {"bytes_per_launch": 50471168 + 14542080,
+    "prefill": {"bytes_per_launch": 50455296 + 13154048,
                 "sources": ("prefill.cu", "cluster.cuh", "common.cuh", "window.cuh"),
-                "sha": "71f3e00f364ce573", "workload": "causal_prefill"},
+                "sha": "45d0d28affcc5537", "workload": "causal_prefill"},
     # one ncu capture of the merged Q/K/V projection of 4096 tokens (hidden 4096)
     "qkv": {"bytes_per_launch": 119868416 + 36024576, "sources": ("qkv.cu", "common.cuh", "tokens.cuh"),
             "sha": "f9d463300a0b1958", "workload": "qkv_append"},

@@ -29,12 +29,14 @@
 //     warp merge multiplies by sigma back.
 // The sliding-window form (kWindow) walks the list of stages that hold a visible token, as in
 // decode.cu: a stage that is visible only in part gets its 16-row groups one by one.  Measured: 64
-// sequences of U{1..16384} tokens, 2048-token window, 52.5 us for 253 MB (4.8 TB/s): while they run
-// the SMs draw 76 % of the memory's nominal rate, but 512 CTAs on 304 places leave them idle for a
-// quarter of the time, and shorter splits cost more in CTA starts than they level (2 splits 62 us).
-// 32 sequences of 1024 tokens, one wave, 18.0 us.  Stages of 64 tokens with four CTAs an SM were
-// faster for 128 x 1024 (53.5 against 58.5 us) and slower for fewer sequences (32 x 1024 20.0, 32 x
-// 4096 55.9 against 48.9, 1 x 4096 10.1 against 8.7 us).
+// sequences of U{1..16384} tokens, 2048-token window, 52.5 us for 253 MB (4.8 TB/s), held back by two
+// things of about the same weight.  One is a tail: 512 CTAs on 304 places leave SMs idle for a
+// quarter of the time (while they run they draw 76 % of the memory's nominal rate), and shorter
+// splits cost more in CTA starts than they level (2 splits 62 us).  The other is the work per stage:
+// every code of K and V is converted to f16 (ALU pipe half busy), for products that use 4 of their 8
+// columns.  Stages of 64 tokens with four CTAs an SM hold all 512 CTAs at once, without that tail, and
+// took 53.1 us.  They were faster for 128 x 1024 (53.5 against 58.5 us) and slower for fewer sequences
+// (32 x 1024 20.0 against 18.0, 32 x 4096 55.9 against 48.9, 1 x 4096 10.1 against 8.7 us).
 #include <atomic>
 
 #include "cluster.cuh"

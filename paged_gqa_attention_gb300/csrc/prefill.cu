@@ -28,7 +28,8 @@
 //   warps 4-7   softmax + epilogue of tile B
 //   warp 8      TMA producer of Q and K (ring of 2 slots)
 //   warp 9      TMEM allocator and the single-thread tcgen05.mma issuer
-//   warp 10     TMA producer of V (ring of 2 slots)
+//   warp 10     TMA producer of V (ring of 2 slots); with a window it also zeroes the V rows that
+//               no position of the unit sees
 // Tensor memory (512 columns): S_A, S_B (fp32 scores), O_A, O_B (fp32 output), 128
 // columns each.  P (bf16, packed in pairs) is written over the first 64 columns of its
 // own S buffer.  Per key tile j the MMA thread issues, in this order,
@@ -47,8 +48,8 @@
 // With too few units to fill the GPU (kSplit), a cluster of CTAs shares each unit: every one takes a
 // run of its key tiles, leaves its unnormalised O with the rows' maxima and sums in its shared
 // memory (over Q and K, which are done with), and the CTAs merge a share of the rows each from all
-// of them by log-sum-exp.  Over a 4096-token window (33 or 34 tiles): 1 token 53.6 us in 8 CTAs,
-// 15.6 in 64; 64 tokens 55.2 and 20.6 us; 512 tokens 57.0 and 39.5 us (64 and 128 CTAs).  The merge
+// of them by log-sum-exp.  Over a 4096-token window (33 or 34 tiles): 1 token 51.1 us in 8 CTAs,
+// 14.6 in 64; 64 tokens 51.5 and 19.9 us; 512 tokens 51.9 and 36.7 us (64 and 128 CTAs).  The merge
 // takes about 1.6 us, and 5.2 more for 64 positions: 128 KiB a CTA from its peers' shared memory at
 // some 14 bytes a clock.  (Storing each row to its merger instead, 16 bytes a lane, took 2 to 3 us
 // longer.)
@@ -1278,7 +1279,7 @@ cudaError_t launch_prefill_window(PrefillArgs a, long long tiles, const CUtensor
         cudaGetLastError();   // the clusters were refused: one CTA a unit instead
         a.unit_ctas = 1;
     }
-    // units that all start at once need no order: 4 x 16 tokens, window 64, 6.9 us (8.7 with the
+    // units that all start at once need no order: 4 x 16 tokens, window 64, 6.5 us (8.5 with the
     // planning kernel)
     if (a.order && units > num_sms)
         return launch_prefill_mode<false, true, false, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);

@@ -26,9 +26,11 @@
 //     leave no SM idle at the end.  (A warp per token took 26.1 us for 4096 tokens into the 8-bit
 //     cache, 4096 tokens on 3648 warps being two rounds; even runs take 19.5 us.)
 // Measured in a graph of calls: 1 token 2.0 us (three dependent loads and a launch), 128 tokens
-// into the 8-bit cache 2.9 us, 4096 tokens into it 19.5 us (92 MB: 4.7 TB/s; the quotients and
-// row maxima hold the warps up), 16381 tokens into the bf16 cache 65.5 us (403 MB: 6.1 TB/s,
-// 92 % of the measured copy rate).
+// into the 8-bit cache 2.8 us, 4096 tokens into it 19.3 us (92 MB: 4.8 TB/s), 16381 tokens into the
+// bf16 cache 65.1 us (403 MB: 6.2 TB/s, 93 % of the measured copy rate).  What the 8-bit rows wait for
+// is a chain (row maximum, scale, reciprocal, quotients, codes) with one group's rows on their way
+// meanwhile and 16 warps an SM at 124 registers to cover it; that is where this form stands, not
+// shown to be a limit (the one form tried with more warps spilled its prefetched rows).
 #include "common.cuh"
 #include "launch.h"
 #include "tokens.cuh"

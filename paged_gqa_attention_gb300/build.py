@@ -56,6 +56,15 @@ def binding_abi() -> str | None:
     return torch and f"torch {torch.__version__} {sysconfig.get_config_var('EXT_SUFFIX')}"
 
 
+def _recorded_abi() -> str | None:
+    """What the binding in place was built for, None where that is not known."""
+    try:
+        with open(BINDING_ABI_PATH) as f:
+            return f.read()
+    except FileNotFoundError:
+        return None
+
+
 def _older(path: str, inputs) -> bool:
     """Whether path is missing or older than one of the files that it is made of."""
     if not os.path.exists(path):
@@ -73,11 +82,7 @@ def binding_up_to_date() -> bool:
     if _older(BINDING_PATH, [os.path.join(CSRC, BINDING_SOURCE), os.path.join(INCLUDE, "pagedattn.h"),
                              os.path.abspath(__file__)]):
         return False
-    try:
-        with open(BINDING_ABI_PATH) as f:
-            return f.read() == binding_abi()
-    except FileNotFoundError:
-        return False
+    return _recorded_abi() == binding_abi()
 
 
 def _run(cmd, what: str, verbose: bool = False):
@@ -128,8 +133,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         _run([gxx, "-shared", "-o", tmp, bound.result(), "-L", os.path.dirname(LIB_PATH),
               "-l:" + os.path.basename(LIB_PATH), "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
               "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib], "linking _binding.so")
-        if os.path.exists(BINDING_ABI_PATH):
-            os.remove(BINDING_ABI_PATH)      # while it might name another binding's
+        if _recorded_abi() not in (None, binding_abi()):
+            os.remove(BINDING_ABI_PATH)      # (it names the old one)
         os.replace(tmp, BINDING_PATH)
         tmp = BINDING_ABI_PATH + f".tmp{os.getpid()}"
         with open(tmp, "w") as f:

@@ -58,3 +58,16 @@ def test_a_binding_of_another_pytorch_is_not_loaded(monkeypatch):
     with pytest.raises(RuntimeError, match="_binding.so was built for torch .* this is torch 0.0.1"):
         ops._usual()
     assert ops._binding is None
+
+
+def test_a_second_build_beside_a_first_leaves_its_record_in_place(elsewhere, monkeypatch):
+    """Two processes that build at once: the record of the binding is never away once one is done."""
+    small = elsewhere / "binding.cpp"
+    small.write_text("extern \"C\" int nothing() { return 0; }\n")
+    monkeypatch.setattr(pa_build, "BINDING_SOURCE", str(small))
+    pa_build.build()
+    assert pa_build.binding_up_to_date()
+    removed = []
+    monkeypatch.setattr(os, "remove", removed.append)
+    pa_build.build(force=True)
+    assert pa_build.binding_up_to_date() and not removed

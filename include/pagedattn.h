@@ -353,6 +353,107 @@ pa_status paged_attn_decode_window_fp8(pa_shape shape, void *out, float *lse, co
                                        size_t workspace_bytes, void *stream);
 
 /*
+ * paged_attn_prefill_fp8: paged_attn_prefill_window over the 8-bit cache: causal attention of each sequence's
+ * new tokens over its cached context and themselves, appended before (kv_append_fp8, paged_rope_append_fp8);
+ * a window as long as the context (INT32_MAX will do) and no sinks is plain causal attention.  Arguments,
+ * workspace, rules and errors as for paged_attn_prefill_window (out 32-byte aligned), k_codes .. v_scale as for
+ * paged_attn_decode_fp8, |q| < 65504.  Products run in f16: a value of the cache enters as the f16 nearest to code *
+ * scale, relative to a power of two taken from the scales that the same 64 tokens' keys have; rows whose scale
+ * is 2^-14 of the largest of them or less lose bits one by one.
+ */
+pa_status paged_attn_prefill_fp8(pa_shape shape, void *out, float *lse, const void *q,
+                                 const void *k_codes, const void *v_codes, const float *k_scale,
+                                 const float *v_scale, const int32_t *block_table,
+                                 int32_t max_blocks_per_seq, int32_t num_blocks,
+                                 const int32_t *cu_q_lens, const int32_t *seq_lens,
+                                 int32_t num_seqs, int32_t total_tokens, int32_t max_q_len,
+                                 int32_t window, int32_t sinks, float scale, void *workspace,
+                                 size_t workspace_bytes, void *stream);
+
+/*
+ * The 4-bit KV cache.  A K or V row (one token, one KV head) is 128 E2M1 codes (magnitudes 0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6 and a sign), one E4M3 scale for every 16 of them and one exponent byte e (1 .. 254; 255 makes the row
+ * NaN); a value is code * scale * 2^(e - 127), which bf16 holds exactly.  73 bytes a row.  Layouts (device
+ * memory, 16-byte aligned):
+ *   k_codes, v_codes  uint8 [num_blocks][256][8][64]   two codes a byte, the even dimension in the low half
+ *   k_scale, v_scale  uint8 [num_blocks][8][256][8]    E4M3, dims 16i .. 16i + 15 under scale i
+ *   k_exp, v_exp      uint8 [num_blocks][8][256]
+ *
+ * kv_append_fp4 quantises every new row x: 2^(e - 127) is the least power of two (from 2^-126) by which the row's
+ * largest magnitude is at most 6 * 448 (e = 127 for a zero row, 255 for one that holds a NaN or an
+ * infinity); with y = x / 2^(e - 127), scale i is E4M3(max|y| / 6) over its 16 dims and a code E2M1(y / scale i),
+ * 0 where that scale is 0, both rounded to nearest, ties to even, and clamped to the largest.  Placement,
+ * arguments and errors are those of kv_append.  paged_rope_append_fp4 is paged_rope_append into this
+ * cache: k rows quantised from their rotated fp32 values.
+ */
+pa_status kv_append_fp4(pa_shape shape, void *k_codes, void *v_codes, void *k_scale, void *v_scale,
+                        void *k_exp, void *v_exp, const void *k_new, const void *v_new,
+                        const int32_t *block_table, int32_t max_blocks_per_seq,
+                        int32_t num_blocks, const int32_t *cu_q_lens, const int32_t *seq_lens,
+                        int32_t num_seqs, int32_t total_tokens, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+pa_status paged_rope_append_fp4(pa_shape shape, float rope_theta, const int32_t *positions, int32_t axes,
+                                const uint8_t *pair_axis, const void *q_norm_weight,
+                                const void *k_norm_weight, float norm_eps, void *q_out,
+                                const void *q, int64_t q_stride, const void *k_new,
+                                int64_t k_stride, const void *v_new, int64_t v_stride,
+                                void *k_codes, void *v_codes, void *k_scale, void *v_scale,
+                                void *k_exp, void *v_exp, const int32_t *block_table,
+                                int32_t max_blocks_per_seq, int32_t num_blocks,
+                                const int32_t *cu_q_lens, const int32_t *seq_lens,
+                                int32_t num_seqs, int32_t total_tokens, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
+ * paged_attn_decode_fp4, paged_attn_prefill_fp4: paged_attn_decode_window and paged_attn_prefill_window over the
+ * 4-bit cache (an INT32_MAX window: all of the context).  Arguments, workspace, rules and errors as for those;
+ * |q| < 65504; split_tokens is a multiple of 256.  In the prefill V rows whose exponent is 14 or more
+ * below the largest of the same 64 tokens' keys lose bits one by one.
+ */
+pa_status paged_attn_decode_fp4(pa_shape shape, void *out, float *lse, const void *q,
+                                const void *k_codes, const void *v_codes, const void *k_scale,
+                                const void *v_scale, const void *k_exp, const void *v_exp,
+                                const int32_t *block_table, int32_t max_blocks_per_seq,
+                                int32_t num_blocks, const int32_t *seq_lens, int32_t batch,
+                                int32_t window, int32_t sinks, float scale, int32_t split_tokens,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+pa_status paged_attn_prefill_fp4(pa_shape shape, void *out, float *lse, const void *q,
+                                 const void *k_codes, const void *v_codes, const void *k_scale,
+                                 const void *v_scale, const void *k_exp, const void *v_exp,
+                                 const int32_t *block_table, int32_t max_blocks_per_seq,
+                                 int32_t num_blocks, const int32_t *cu_q_lens,
+                                 const int32_t *seq_lens, int32_t num_seqs, int32_t total_tokens,
+                                 int32_t max_q_len, int32_t window, int32_t sinks, float scale,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * paged_kv_read_fp8, paged_kv_read_fp4: rows of the cache read back as bf16, for a sequence that moves to another
+ * cache or a consumer of plain rows.  Row cu_rows[s] + i of k_out and v_out ([total_rows][8][128] bf16) is the
+ * token at position first[s] + i of sequence s, i < cu_rows[s + 1] - cu_rows[s]: its value code * scale in
+ * fp32, rounded to bf16 (8 bits), or code * scale * 2^(e - 127), exact down to bf16's smallest (4 bits; codes
+ * may stand for a little more than the row they were taken from: past bf16's largest that is infinity).
+ *   cu_rows int32 [num_seqs + 1], first int32 [num_seqs]; total_rows >= cu_rows[num_seqs]: rows behind the
+ *   last sequence are left as they are.  Table entries of blocks without such a row are not used.
+ *   A row whose block id is outside the pool, whose position is outside the table or whose cu_rows are inconsistent
+ *   comes back as NaN and records PA_ERR_DEVICE.  Outputs must not overlap the cache.
+ */
+pa_status paged_kv_read_fp8(pa_shape shape, void *k_out, void *v_out, const void *k_codes,
+                            const void *v_codes, const float *k_scale, const float *v_scale,
+                            const int32_t *block_table, int32_t max_blocks_per_seq,
+                            int32_t num_blocks, const int32_t *cu_rows, const int32_t *first,
+                            int32_t num_seqs, int32_t total_rows, void *workspace,
+                            size_t workspace_bytes, void *stream);
+
+pa_status paged_kv_read_fp4(pa_shape shape, void *k_out, void *v_out, const void *k_codes,
+                            const void *v_codes, const void *k_scale, const void *v_scale,
+                            const void *k_exp, const void *v_exp, const int32_t *block_table,
+                            int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *cu_rows,
+                            const int32_t *first, int32_t num_seqs, int32_t total_rows,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * paged_attn_decode_append: kv_append of one new token per sequence followed by
  * paged_attn_decode, in one kernel [P1 §4.3.1 append, §4.4.2 decode; P3 §4.2 "append,
  * then attend"].  Row b of k_new / v_new ([batch][8][128] bf16) is written to position

@@ -29,7 +29,7 @@ BINDING_PATH = os.path.join(PKG, "_binding.so")
 BINDING_ABI_PATH = os.path.join(PKG, "_binding.abi")
 BINDING_SOURCE = "binding.cpp"
 SOURCES = ["api.cu", "kv_append.cu", "decode.cu", "decode_fp8.cu", "prefill.cu", "qkv.cu",
-           "rope_append.cu"]
+           "rope_append.cu", "prefill_quant.cu", "decode_fp4.cu", "kv_read.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
 

@@ -10,6 +10,7 @@
 
 #include "pagedattn.h"
 #include "common.cuh"
+#include "fp4.cuh"
 #include "launch.h"
 
 // Handle of pa_decode_graph_create: the captured graph, its executable form and the
@@ -72,6 +73,18 @@ bool encode_code_map(CUtensorMap *map, const void *codes, int num_blocks, int ro
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(codes), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A 4-bit code pool [num_blocks][256][8][64] uint8 likewise: one 64-byte row per token, 64-byte swizzle.
+bool encode_code4_map(CUtensorMap *map, const void *codes, int num_blocks, int rows) {
+    const cuuint64_t row = kFp4RowCodes;
+    const cuuint64_t dims[4] = {row, (cuuint64_t)kHkv, (cuuint64_t)kBlock, (cuuint64_t)num_blocks};
+    const cuuint64_t strides[3] = {row, row * kHkv, row * kHkv * kBlock};
+    const cuuint32_t box[4] = {(cuuint32_t)kFp4RowCodes, 1, (cuuint32_t)rows, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(codes), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -179,6 +192,7 @@ struct SplitCost {
     int most_waved;      // splits tried where even unsplit sequences fill more than one wave
 };
 constexpr SplitCost kSplitCost = {0.42, 1.0, 0.0049, 1.4, 1.9, 0.07, 1.5, 5};          // 64 tokens in bf16
+constexpr SplitCost kSplitCostFp4 = {1.1, 1.5, 0.0058, 1.7, 2.3, 0.15, 1.5, 1};        // 256 tokens in 4 bits
 constexpr SplitCost kSplitCostFp8 = {0.78, 1.8, 0.0053, 1.7, 2.3, 0.15, 1.5, 1};       // 128 tokens in 8 bits
 
 int auto_window_split(int batch, long long tiles, int num_sms, const SplitCost &c) {
@@ -262,6 +276,20 @@ struct CascadeExtras {
 struct Window {
     int32_t window;
     int32_t sinks;
+};
+
+// Scales of an 8-bit cache's rows, or scales and exponents of a 4-bit cache's (k_exp set).
+struct LowBit {
+    const void *k_scale;
+    const void *v_scale;
+    const void *k_exp;
+    const void *v_exp;
+
+    // whether all of them are there, 16-byte aligned (`bits`: the cache's)
+    bool ok(int bits) const {
+        return k_scale && v_scale && aligned16(k_scale) && aligned16(v_scale) &&
+               (bits == 8 || (k_exp && v_exp && aligned16(k_exp) && aligned16(v_exp)));
+    }
 };
 
 bool window_ok(int32_t window, int32_t sinks) { return window >= 1 && sinks >= 0; }
@@ -448,12 +476,12 @@ void rope_frequencies(double theta, float *hi, float *lo) {
     }
 }
 
-// paged_rope_append over the bf16 cache, or over the 8-bit cache when eight_bit.
+// paged_rope_append into the cache of that many bits (16: no scales).
 pa_status rope_append_impl(pa_shape shape, float rope_theta, const int32_t *positions, int32_t axes,
                            const uint8_t *pair_axis, const void *q_norm, const void *k_norm, float norm_eps,
                            void *q_out, const void *q, int64_t q_stride, const void *k_new, int64_t k_stride,
-                           const void *v_new, int64_t v_stride, bool eight_bit, void *k_pool, void *v_pool,
-                           float *k_scale, float *v_scale, const int32_t *block_table, int32_t max_blocks_per_seq,
+                           const void *v_new, int64_t v_stride, int bits, void *k_pool, void *v_pool,
+                           const LowBit &low, const int32_t *block_table, int32_t max_blocks_per_seq,
                            int32_t num_blocks, const int32_t *cu_q_lens, const int32_t *seq_lens, int32_t num_seqs,
                            int32_t total_tokens, void *workspace, size_t workspace_bytes, void *stream) {
     if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
@@ -480,10 +508,10 @@ pa_status rope_append_impl(pa_shape shape, float rope_theta, const int32_t *posi
         return PA_ERR_INVALID_ARG;
     if (total_tokens == 0) return PA_OK;
     if (!q_out || !q || !k_new || !v_new || !k_pool || !v_pool || !block_table || !cu_q_lens || !seq_lens ||
-        (eight_bit && (!k_scale || !v_scale)))
+        (bits != 16 && !low.ok(bits)))
         return PA_ERR_INVALID_ARG;
     if (!aligned16(q_out) || !aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pool) ||
-        !aligned16(v_pool) || !aligned16(k_scale) || !aligned16(v_scale) || !aligned4(block_table) ||
+        !aligned16(v_pool) || !aligned4(block_table) ||
         !aligned4(cu_q_lens) || !aligned4(seq_lens) || !aligned4(positions))
         return PA_ERR_INVALID_ARG;
     if (q_out == q && q_stride != kHq * kD) return PA_ERR_INVALID_ARG;   // in place: the same rows
@@ -499,8 +527,16 @@ pa_status rope_append_impl(pa_shape shape, float rope_theta, const int32_t *posi
     a.v_stride = v_stride;
     a.k_pool = k_pool;
     a.v_pool = v_pool;
-    a.k_scale = k_scale;
-    a.v_scale = v_scale;
+    void *ks = const_cast<void *>(low.k_scale), *vs = const_cast<void *>(low.v_scale);
+    if (bits == 8) {
+        a.k_scale = static_cast<float *>(ks);
+        a.v_scale = static_cast<float *>(vs);
+    } else if (bits == 4) {
+        a.k_scale4 = static_cast<uint8_t *>(ks);
+        a.v_scale4 = static_cast<uint8_t *>(vs);
+        a.k_exp = static_cast<uint8_t *>(const_cast<void *>(low.k_exp));
+        a.v_exp = static_cast<uint8_t *>(const_cast<void *>(low.v_exp));
+    }
     a.block_table = block_table;
     a.max_blocks_per_seq = max_blocks_per_seq;
     a.num_blocks = num_blocks;
@@ -621,29 +657,36 @@ pa_status paged_qkv_append_qknorm(pa_shape shape, int32_t hidden, float rope_the
                     total_tokens, workspace, workspace_bytes, stream);
 }
 
-pa_status kv_append_fp8(pa_shape shape, void *k_codes, void *v_codes, float *k_scale, float *v_scale,
-                        const void *k_new, const void *v_new, const int32_t *block_table,
-                        int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *cu_q_lens,
-                        const int32_t *seq_lens, int32_t num_seqs, int32_t total_tokens, void *workspace,
-                        size_t workspace_bytes, void *stream) {
+// kv_append into the 8-bit or the 4-bit cache.
+static pa_status kv_append_low(int bits, pa_shape shape, void *k_codes, void *v_codes, const LowBit &low,
+                               const void *k_new, const void *v_new, const int32_t *block_table,
+                               int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *cu_q_lens,
+                               const int32_t *seq_lens, int32_t num_seqs, int32_t total_tokens, void *workspace,
+                               size_t workspace_bytes, void *stream) {
     if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
     if (num_seqs < 0 || total_tokens < 0 || max_blocks_per_seq < 1 || num_blocks < 1 ||
         (num_seqs == 0 && total_tokens != 0))
         return PA_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < kHeaderBytes || !aligned16(workspace)) return PA_ERR_INVALID_ARG;
     if (total_tokens == 0) return PA_OK;
-    if (!k_codes || !v_codes || !k_scale || !v_scale || !k_new || !v_new || !block_table || !cu_q_lens ||
-        !seq_lens)
+    if (!k_codes || !v_codes || !low.ok(bits) || !k_new || !v_new || !block_table || !cu_q_lens || !seq_lens)
         return PA_ERR_INVALID_ARG;
-    if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_scale) || !aligned16(v_scale) ||
-        !aligned16(k_new) || !aligned16(v_new) || !aligned4(block_table) || !aligned4(cu_q_lens) ||
-        !aligned4(seq_lens))
+    if (!aligned16(k_codes) || !aligned16(v_codes) || !aligned16(k_new) || !aligned16(v_new) ||
+        !aligned4(block_table) || !aligned4(cu_q_lens) || !aligned4(seq_lens))
         return PA_ERR_INVALID_ARG;
     AppendArgs a = {};
     a.k_pool = k_codes;
     a.v_pool = v_codes;
-    a.k_scale = k_scale;
-    a.v_scale = v_scale;
+    void *ks = const_cast<void *>(low.k_scale), *vs = const_cast<void *>(low.v_scale);
+    if (bits == 8) {
+        a.k_scale = static_cast<float *>(ks);
+        a.v_scale = static_cast<float *>(vs);
+    } else {
+        a.k_scale4 = static_cast<uint8_t *>(ks);
+        a.v_scale4 = static_cast<uint8_t *>(vs);
+        a.k_exp = static_cast<uint8_t *>(const_cast<void *>(low.k_exp));
+        a.v_exp = static_cast<uint8_t *>(const_cast<void *>(low.v_exp));
+    }
     a.k_new = k_new;
     a.v_new = v_new;
     a.block_table = block_table;
@@ -657,6 +700,83 @@ pa_status kv_append_fp8(pa_shape shape, void *k_codes, void *v_codes, float *k_s
     return launch_kv_append(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
+pa_status kv_append_fp8(pa_shape shape, void *k_codes, void *v_codes, float *k_scale, float *v_scale,
+                        const void *k_new, const void *v_new, const int32_t *block_table,
+                        int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *cu_q_lens,
+                        const int32_t *seq_lens, int32_t num_seqs, int32_t total_tokens, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    return kv_append_low(8, shape, k_codes, v_codes, LowBit{k_scale, v_scale, nullptr, nullptr}, k_new, v_new, block_table,
+                         max_blocks_per_seq, num_blocks, cu_q_lens, seq_lens, num_seqs, total_tokens, workspace,
+                         workspace_bytes, stream);
+}
+
+pa_status kv_append_fp4(pa_shape shape, void *k_codes, void *v_codes, void *k_scale, void *v_scale, void *k_exp,
+                        void *v_exp, const void *k_new, const void *v_new, const int32_t *block_table,
+                        int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *cu_q_lens,
+                        const int32_t *seq_lens, int32_t num_seqs, int32_t total_tokens, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    return kv_append_low(4, shape, k_codes, v_codes, LowBit{k_scale, v_scale, k_exp, v_exp}, k_new, v_new, block_table,
+                         max_blocks_per_seq, num_blocks, cu_q_lens, seq_lens, num_seqs, total_tokens, workspace,
+                         workspace_bytes, stream);
+}
+
+// Rows of the 8-bit or the 4-bit cache as bf16.
+static pa_status kv_read_impl(int bits, pa_shape shape, void *k_out, void *v_out, const void *k_codes,
+                              const void *v_codes, const LowBit &low, const int32_t *block_table,
+                              int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *cu_rows,
+                              const int32_t *first, int32_t num_seqs, int32_t total_rows, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+    if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
+    if (num_seqs < 0 || total_rows < 0 || max_blocks_per_seq < 1 || num_blocks < 1 ||
+        (num_seqs == 0 && total_rows != 0) || (long long)max_blocks_per_seq * kBlock > (1ll << 30))
+        return PA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kHeaderBytes || !aligned16(workspace)) return PA_ERR_INVALID_ARG;
+    if (total_rows == 0) return PA_OK;
+    if (!k_out || !v_out || !k_codes || !v_codes || !low.ok(bits) || !block_table || !cu_rows || !first)
+        return PA_ERR_INVALID_ARG;
+    if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_codes) || !aligned16(v_codes) ||
+        !aligned4(block_table) || !aligned4(cu_rows) || !aligned4(first))
+        return PA_ERR_INVALID_ARG;
+    ReadArgs a = {};
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.k_codes = k_codes;
+    a.v_codes = v_codes;
+    a.k_scale = low.k_scale;
+    a.v_scale = low.v_scale;
+    a.k_exp = static_cast<const uint8_t *>(low.k_exp);
+    a.v_exp = static_cast<const uint8_t *>(low.v_exp);
+    a.block_table = block_table;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.cu_rows = cu_rows;
+    a.first = first;
+    a.num_seqs = num_seqs;
+    a.total_rows = total_rows;
+    a.err = static_cast<uint32_t *>(workspace);
+    return launch_kv_read(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
+
+pa_status paged_kv_read_fp8(pa_shape shape, void *k_out, void *v_out, const void *k_codes, const void *v_codes,
+                            const float *k_scale, const float *v_scale, const int32_t *block_table,
+                            int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *cu_rows,
+                            const int32_t *first, int32_t num_seqs, int32_t total_rows, void *workspace,
+                            size_t workspace_bytes, void *stream) {
+    return kv_read_impl(8, shape, k_out, v_out, k_codes, v_codes, LowBit{k_scale, v_scale, nullptr, nullptr}, block_table,
+                        max_blocks_per_seq, num_blocks, cu_rows, first, num_seqs, total_rows, workspace, workspace_bytes,
+                        stream);
+}
+
+pa_status paged_kv_read_fp4(pa_shape shape, void *k_out, void *v_out, const void *k_codes, const void *v_codes,
+                            const void *k_scale, const void *v_scale, const void *k_exp, const void *v_exp,
+                            const int32_t *block_table, int32_t max_blocks_per_seq, int32_t num_blocks,
+                            const int32_t *cu_rows, const int32_t *first, int32_t num_seqs, int32_t total_rows,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+    return kv_read_impl(4, shape, k_out, v_out, k_codes, v_codes, LowBit{k_scale, v_scale, k_exp, v_exp}, block_table,
+                        max_blocks_per_seq, num_blocks, cu_rows, first, num_seqs, total_rows, workspace, workspace_bytes,
+                        stream);
+}
+
 pa_status paged_rope_append(pa_shape shape, float rope_theta, const int32_t *positions, int32_t axes,
                             const uint8_t *pair_axis, const void *q_norm_weight, const void *k_norm_weight,
                             float norm_eps, void *q_out, const void *q, int64_t q_stride, const void *k_new,
@@ -665,8 +785,8 @@ pa_status paged_rope_append(pa_shape shape, float rope_theta, const int32_t *pos
                             const int32_t *cu_q_lens, const int32_t *seq_lens, int32_t num_seqs,
                             int32_t total_tokens, void *workspace, size_t workspace_bytes, void *stream) {
     return rope_append_impl(shape, rope_theta, positions, axes, pair_axis, q_norm_weight, k_norm_weight, norm_eps,
-                            q_out, q, q_stride, k_new, k_stride, v_new, v_stride, false, k_pool, v_pool, nullptr,
-                            nullptr, block_table, max_blocks_per_seq, num_blocks, cu_q_lens, seq_lens, num_seqs,
+                            q_out, q, q_stride, k_new, k_stride, v_new, v_stride, 16, k_pool, v_pool, LowBit{},
+                            block_table, max_blocks_per_seq, num_blocks, cu_q_lens, seq_lens, num_seqs,
                             total_tokens, workspace, workspace_bytes, stream);
 }
 
@@ -679,9 +799,23 @@ pa_status paged_rope_append_fp8(pa_shape shape, float rope_theta, const int32_t 
                                 const int32_t *seq_lens, int32_t num_seqs, int32_t total_tokens, void *workspace,
                                 size_t workspace_bytes, void *stream) {
     return rope_append_impl(shape, rope_theta, positions, axes, pair_axis, q_norm_weight, k_norm_weight, norm_eps,
-                            q_out, q, q_stride, k_new, k_stride, v_new, v_stride, true, k_codes, v_codes, k_scale,
-                            v_scale, block_table, max_blocks_per_seq, num_blocks, cu_q_lens, seq_lens, num_seqs,
+                            q_out, q, q_stride, k_new, k_stride, v_new, v_stride, 8, k_codes, v_codes,
+                            LowBit{k_scale, v_scale, nullptr, nullptr}, block_table, max_blocks_per_seq, num_blocks, cu_q_lens, seq_lens, num_seqs,
                             total_tokens, workspace, workspace_bytes, stream);
+}
+
+pa_status paged_rope_append_fp4(pa_shape shape, float rope_theta, const int32_t *positions, int32_t axes,
+                                const uint8_t *pair_axis, const void *q_norm_weight, const void *k_norm_weight,
+                                float norm_eps, void *q_out, const void *q, int64_t q_stride, const void *k_new,
+                                int64_t k_stride, const void *v_new, int64_t v_stride, void *k_codes, void *v_codes,
+                                void *k_scale, void *v_scale, void *k_exp, void *v_exp, const int32_t *block_table,
+                                int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *cu_q_lens,
+                                const int32_t *seq_lens, int32_t num_seqs, int32_t total_tokens, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    return rope_append_impl(shape, rope_theta, positions, axes, pair_axis, q_norm_weight, k_norm_weight, norm_eps,
+                            q_out, q, q_stride, k_new, k_stride, v_new, v_stride, 4, k_codes, v_codes,
+                            LowBit{k_scale, v_scale, k_exp, v_exp}, block_table, max_blocks_per_seq, num_blocks,
+                            cu_q_lens, seq_lens, num_seqs, total_tokens, workspace, workspace_bytes, stream);
 }
 
 static pa_status decode_fp8_impl(pa_shape shape, void *out, float *lse, const void *q, const void *k_new, const void *v_new,
@@ -796,6 +930,68 @@ pa_status paged_attn_decode_append_fp8(pa_shape shape, void *out, float *lse, co
     return decode_fp8_impl(shape, out, lse, q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, block_table,
                            max_blocks_per_seq, num_blocks, seq_lens, batch, scale, 0, workspace, workspace_bytes,
                            stream);
+}
+
+pa_status paged_attn_decode_fp4(pa_shape shape, void *out, float *lse, const void *q, const void *k_codes,
+                                const void *v_codes, const void *k_scale, const void *v_scale, const void *k_exp,
+                                const void *v_exp, const int32_t *block_table, int32_t max_blocks_per_seq,
+                                int32_t num_blocks, const int32_t *seq_lens, int32_t batch, int32_t window,
+                                int32_t sinks, float scale, int32_t split_tokens, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
+    if (!window_ok(window, sinks) || batch < 0 || batch > kMaxBatch || max_blocks_per_seq < 1 || num_blocks < 1 ||
+        !std::isfinite(scale) || split_tokens < 0 || split_tokens % kDecodeFp4TileTokens != 0)
+        return PA_ERR_INVALID_ARG;
+    if (!workspace || workspace_bytes < kPartialOffset || !aligned16(workspace)) return PA_ERR_INVALID_ARG;
+    if (batch == 0) return PA_OK;
+    const LowBit low = {k_scale, v_scale, k_exp, v_exp};
+    if (!out || !q || !k_codes || !v_codes || !low.ok(4) || !block_table || !seq_lens) return PA_ERR_INVALID_ARG;
+    if (!aligned16(out) || !aligned16(q) || !aligned16(k_codes) || !aligned16(v_codes) || !aligned4(block_table) ||
+        !aligned4(seq_lens) || (lse && !aligned4(lse)))
+        return PA_ERR_INVALID_ARG;
+    if ((long long)max_blocks_per_seq * kBlock > (1ll << 30)) return PA_ERR_INVALID_ARG;
+    const int sms = sm_count();
+    if (sms <= 0) return PA_ERR_CUDA;
+    if (!get_encoder()) return PA_ERR_CUDA;
+    const long long tiles = window_tiles_bound(window, sinks, max_blocks_per_seq, kDecodeFp4TileTokens);
+    const long long per_split = split_tokens ? split_tokens / kDecodeFp4TileTokens
+                                             : auto_window_split(batch, tiles, sms, kSplitCostFp4);
+    const long long nsplit = (tiles + per_split - 1) / per_split;
+    if (nsplit > 65535) return PA_ERR_INVALID_ARG;
+    const size_t entries = (size_t)batch * kHkv * (size_t)nsplit;
+    if (workspace_bytes_for(entries) > workspace_bytes) return PA_ERR_WORKSPACE;
+    CUtensorMap k_map, v_map, k16_map, v16_map;
+    if (!encode_code4_map(&k_map, k_codes, num_blocks, kDecodeFp4TileTokens) ||
+        !encode_code4_map(&v_map, v_codes, num_blocks, kDecodeFp4TileTokens) ||
+        !encode_code4_map(&k16_map, k_codes, num_blocks, 16) || !encode_code4_map(&v16_map, v_codes, num_blocks, 16))
+        return PA_ERR_INVALID_ARG;
+    char *ws = static_cast<char *>(workspace);
+    DecodeArgs a = {};
+    a.out = out;
+    a.lse = lse;
+    a.q = q;
+    a.block_table = block_table;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.num_blocks = num_blocks;
+    a.seq_lens = seq_lens;
+    a.batch = batch;
+    a.split_tokens = (int)(per_split * kDecodeFp4TileTokens);   // (at most the table's 2^30)
+    a.nsplit = (int)nsplit;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.k_scale4 = static_cast<const uint8_t *>(k_scale);
+    a.v_scale4 = static_cast<const uint8_t *>(v_scale);
+    a.k_exp = static_cast<const uint8_t *>(k_exp);
+    a.v_exp = static_cast<const uint8_t *>(v_exp);
+    a.counters = reinterpret_cast<int32_t *>(ws + kCounterOffset);
+    a.part_o = reinterpret_cast<float *>(ws + kPartialOffset);
+    a.part_ml = reinterpret_cast<float *>(ws + kPartialOffset + entries * kPartialOBytes);
+    a.err = reinterpret_cast<uint32_t *>(ws);
+    a.window = window;
+    a.sinks = sinks;
+    a.cluster_merge = nsplit > 1 && nsplit <= 8 && (long long)batch * kHkv * nsplit <= 2LL * sms ? 1 : 0;
+    return launch_decode_fp4(a, k_map, v_map, k16_map, v16_map, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
 }
 
 pa_status paged_attn_decode(pa_shape shape, void *out, float *lse, const void *q, const void *k_pool,
@@ -990,7 +1186,7 @@ static pa_status prefill_impl(pa_shape shape, void *out, float *lse, const void 
                               int32_t max_blocks_per_seq, int32_t num_blocks, const int32_t *cu_q_lens,
                               const int32_t *seq_lens, int32_t num_seqs, int32_t total_tokens, int32_t max_q_len,
                               float scale, void *workspace, size_t workspace_bytes, void *stream,
-                              const Window *win = nullptr) {
+                              const Window *win = nullptr, int bits = 16, const LowBit *low = nullptr) {
     if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
     if (num_seqs < 0 || total_tokens < 0 || max_q_len < 0 || max_blocks_per_seq < 1 || num_blocks < 1 ||
         !std::isfinite(scale) || !(scale > 0.f) || (num_seqs == 0 && total_tokens != 0) || max_q_len > total_tokens ||
@@ -1007,15 +1203,17 @@ static pa_status prefill_impl(pa_shape shape, void *out, float *lse, const void 
         return PA_ERR_INVALID_ARG;
     if ((k_new == nullptr) != (v_new == nullptr) || (k_new && (!aligned16(k_new) || !aligned16(v_new))))
         return PA_ERR_INVALID_ARG;
+    if (low && !low->ok(bits)) return PA_ERR_INVALID_ARG;
     const int sms = sm_count();
     if (sms <= 0) return PA_ERR_CUDA;
     if (!get_encoder()) return PA_ERR_CUDA;
     CUtensorMap q_map, k_map, v_map, kn_map, vn_map;
     const int box = win ? 64 : kPrefillKvTile;
-    if (!encode_q_map(&q_map, q, total_tokens) || !encode_pool_map(&k_map, k_pool, num_blocks, box) ||
-        !encode_pool_map(&v_map, v_pool, num_blocks, box))
+    const auto encode = bits == 16 ? encode_pool_map : bits == 8 ? encode_code_map : encode_code4_map;
+    if (!encode_q_map(&q_map, q, total_tokens) || !encode(&k_map, k_pool, num_blocks, box) ||
+        !encode(&v_map, v_pool, num_blocks, box))
         return PA_ERR_INVALID_ARG;
-    if (win && (!encode_pool_map(&kn_map, k_pool, num_blocks, 16) || !encode_pool_map(&vn_map, v_pool, num_blocks, 16)))
+    if (win && (!encode(&kn_map, k_pool, num_blocks, 16) || !encode(&vn_map, v_pool, num_blocks, 16)))
         return PA_ERR_INVALID_ARG;
     if (k_new && (!encode_new_rows_map(&kn_map, k_new, total_tokens) || !encode_new_rows_map(&vn_map, v_new, total_tokens)))
         return PA_ERR_INVALID_ARG;
@@ -1044,6 +1242,12 @@ static pa_status prefill_impl(pa_shape shape, void *out, float *lse, const void 
     a.order = nullptr;
     a.window = win ? win->window : 0;
     a.sinks = win ? win->sinks : 0;
+    if (low) {
+        a.k_scale = low->k_scale;
+        a.v_scale = low->v_scale;
+        a.k_exp = static_cast<const uint8_t *>(low->k_exp);
+        a.v_exp = static_cast<const uint8_t *>(low->v_exp);
+    }
     const long long plan_units = prefill_plan_units(a);
     if (plan_units > 0 && workspace_bytes >= kPartialOffset + (size_t)plan_units * sizeof(int32_t))
         a.order = reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + kPartialOffset);
@@ -1053,7 +1257,8 @@ static pa_status prefill_impl(pa_shape shape, void *out, float *lse, const void 
                                           (long long)win->sinks + 15 + win->window + 2 * kPrefillQPositions + 15)
                                : 0;
     const long long tiles = (rows + kPrefillKvTile - 1) / kPrefillKvTile;
-    const cudaError_t e = win     ? launch_prefill_window(a, tiles, q_map, k_map, v_map, kn_map, vn_map, sms, st)
+    const cudaError_t e = low     ? launch_prefill_quant(a, tiles, q_map, k_map, v_map, kn_map, vn_map, sms, st)
+                          : win   ? launch_prefill_window(a, tiles, q_map, k_map, v_map, kn_map, vn_map, sms, st)
                           : k_new ? launch_prefill_append(a, q_map, k_map, v_map, kn_map, vn_map, sms, st)
                                   : launch_prefill(a, q_map, k_map, v_map, sms, st);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
@@ -1081,6 +1286,36 @@ pa_status paged_attn_prefill_window(pa_shape shape, void *out, float *lse, const
     return prefill_impl(shape, out, lse, q, nullptr, nullptr, k_pool, v_pool, block_table, max_blocks_per_seq,
                         num_blocks, cu_q_lens, seq_lens, num_seqs, total_tokens, max_q_len, scale, workspace,
                         workspace_bytes, stream, &win);
+}
+
+pa_status paged_attn_prefill_fp8(pa_shape shape, void *out, float *lse, const void *q, const void *k_codes,
+                                 const void *v_codes, const float *k_scale, const float *v_scale,
+                                 const int32_t *block_table, int32_t max_blocks_per_seq, int32_t num_blocks,
+                                 const int32_t *cu_q_lens, const int32_t *seq_lens, int32_t num_seqs,
+                                 int32_t total_tokens, int32_t max_q_len, int32_t window, int32_t sinks, float scale,
+                                 void *workspace, size_t workspace_bytes, void *stream) {
+    if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
+    if (!window_ok(window, sinks)) return PA_ERR_INVALID_ARG;
+    const Window win = {window, sinks};
+    const LowBit low = {k_scale, v_scale, nullptr, nullptr};
+    return prefill_impl(shape, out, lse, q, nullptr, nullptr, k_codes, v_codes, block_table, max_blocks_per_seq,
+                        num_blocks, cu_q_lens, seq_lens, num_seqs, total_tokens, max_q_len, scale, workspace,
+                        workspace_bytes, stream, &win, 8, &low);
+}
+
+pa_status paged_attn_prefill_fp4(pa_shape shape, void *out, float *lse, const void *q, const void *k_codes,
+                                 const void *v_codes, const void *k_scale, const void *v_scale, const void *k_exp,
+                                 const void *v_exp, const int32_t *block_table, int32_t max_blocks_per_seq,
+                                 int32_t num_blocks, const int32_t *cu_q_lens, const int32_t *seq_lens,
+                                 int32_t num_seqs, int32_t total_tokens, int32_t max_q_len, int32_t window,
+                                 int32_t sinks, float scale, void *workspace, size_t workspace_bytes, void *stream) {
+    if (!shape_ok(shape)) return PA_ERR_UNSUPPORTED;
+    if (!window_ok(window, sinks)) return PA_ERR_INVALID_ARG;
+    const Window win = {window, sinks};
+    const LowBit low = {k_scale, v_scale, k_exp, v_exp};
+    return prefill_impl(shape, out, lse, q, nullptr, nullptr, k_codes, v_codes, block_table, max_blocks_per_seq,
+                        num_blocks, cu_q_lens, seq_lens, num_seqs, total_tokens, max_q_len, scale, workspace,
+                        workspace_bytes, stream, &win, 4, &low);
 }
 
 pa_status paged_attn_prefill_append(pa_shape shape, void *out, float *lse, const void *q, const void *k_new,

@@ -1,0 +1,608 @@
+// decode_fp4.cu -- batched single-token GQA attention over the 4-bit KV cache, with an optional
+// sliding window.
+//
+// The attention is that of decode.cu (page "扔掉 vLLM！从零构建 Qwen3-8B 推理引擎，C++/CUDA 实现性能追平
+// 98%" §4.4.2: the four query heads of a group share every KV read; split-K over the context with a
+// log-sum-exp merge); the cache is one step below the 8 bits of page "从零搭建AI工程能力：手写KV Cache与
+// 动态批处理实战" §3.2 (format: fp4.cuh): 146 bytes per token and KV head instead of 512.
+//
+// What bounds it is the work a byte asks for: a byte of codes is two values to convert, scale and multiply,
+// so per 16 tokens a warp issues some 300 instructions for 2.3 KB.  Hence:
+//   * a stage is a whole 256-token block of K and V (16 KiB of codes each, TMA, 64-byte swizzle; 2 KiB of
+//     scales and 256 exponents each, bulk copies), consumed by 8 warps of 32 tokens; three stages, two
+//     CTAs per SM.  Two 16-token tiles a warp give every step of the chain (scores, softmax, output) two
+//     independent halves, and share the votes and the rescaling;
+//   * products in f16 (mma.sync; 4 of 8 columns are heads): code * scale has 6 bits and is exact.
+//     ldmatrix on the codes gives a lane 8 consecutive dims of a token, two k16 steps once Q is loaded in
+//     that order, all 8 in one scale group; the transposed ldmatrix gives it 4 dims of two tokens, paired by
+//     dimension by a byte permute after the conversion.  Accumulator tile 2c + t then holds dims
+//     32c + 4r + 2t (rows r < 8) and 32c + 4(r - 8) + 2t + 1;
+//   * the row's power of two enters S in fp32, and for V through P: each warp accumulates
+//     P * 2^(e - sigma) in f16, sigma the largest exponent it has seen, and rescales its accumulator
+//     when sigma grows, as the online softmax does for its maximum;
+//   * tokens that are not attended to get scale 0 in V (every code is finite) and score -infinity.
+#include <atomic>
+
+#include "cluster.cuh"
+#include "common.cuh"
+#include "fp4.cuh"
+#include "launch.h"
+#include "window.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kTile = kDecodeFp4TileTokens;   // 256 tokens per stage: a cache block
+constexpr int kStages = 3;
+constexpr int kCtasPerSm = 2;
+constexpr int kWarpTokens = 32;
+constexpr int kConsumerWarps = kTile / kWarpTokens;   // 8
+constexpr int kThreads = (kConsumerWarps + 1) * 32;
+constexpr int kCodeBytes = kTile * kFp4RowCodes;      // 16 KiB
+constexpr int kScaleBytes = kTile * kFp4Groups;       // 2 KiB
+constexpr uint32_t kSideTx = 2 * (kScaleBytes + kTile);
+constexpr float kLn2 = 0.693147180559945309f;
+constexpr int kNoSigma = -1000;
+
+struct MergeArrays {                          // the warps' partial results, after the stages
+    float o[kConsumerWarps][kGroup][kD];
+    float m[kConsumerWarps][kGroup];
+    float l[kConsumerWarps][kGroup];
+    int sigma[kConsumerWarps];
+};
+
+struct DecodeFp4Smem {
+    union {
+        uint8_t codes[kStages][2][kCodeBytes];  // [stage][K, V], each 1 KiB aligned
+        MergeArrays mg;                         // reused once every stage is consumed
+    };
+    uint8_t scales[kStages][2][kScaleBytes];
+    uint8_t exps[kStages][2][kTile];
+    uint64_t full[kStages];
+    uint64_t empty[kStages];
+    int last_cta;
+    int poison;
+    float cl_ml[kGroup][2];                    // cluster merge: this split's (m, l) per head
+};
+
+constexpr size_t kSmemBytes = sizeof(DecodeFp4Smem) + 1024;
+static_assert(2 * (kSmemBytes + 1024) <= 233472, "two CTAs per SM");
+
+__device__ __forceinline__ void store_out4(__nv_bfloat16 *dst, const float (&v)[4], float inv) {
+    uint2 w;
+    w.x = pack_bf16x2(v[0] * inv, v[1] * inv);
+    w.y = pack_bf16x2(v[2] * inv, v[3] * inv);
+    *reinterpret_cast<uint2 *>(dst) = w;
+}
+
+// Byte offset of 16-byte piece `piece` (0..3) of row `row` of a tile of 64-byte rows written by TMA with
+// 64-byte swizzling.
+__device__ __forceinline__ uint32_t sw64(int row, int piece) {
+    return (uint32_t)(row * kFp4RowCodes + ((piece ^ ((row >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Two E4M3 bytes -> f16x2 (the lower byte in the low half)
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+    uint32_t d;
+    asm("{\n .reg .b16 a;\n cvt.u16.u32 a, %1;\n cvt.rn.f16x2.e4m3x2 %0, a;\n}" : "=r"(d) : "r"(two));
+    return d;
+}
+
+// 2^n for n <= 127, 0 below the normal range.
+__device__ __forceinline__ float pow2_or_0(int n) { return n < -126 ? 0.f : __uint_as_float((uint32_t)(n + 127) << 23); }
+
+template <bool kCluster>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+decode_fp4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                  const __grid_constant__ CUtensorMap k16_map, const __grid_constant__ CUtensorMap v16_map,
+                  const DecodeArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    DecodeFp4Smem &sm = *reinterpret_cast<DecodeFp4Smem *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+
+    const int pair = blockIdx.x;          // sequence * 8 + kv head
+    const int b = pair / kHkv;
+    const int g = pair % kHkv;
+    // the highest splits start first (longest work first, as in decode.cu)
+    const int split = kCluster ? (int)blockIdx.y : (int)(gridDim.y - 1 - blockIdx.y);
+    // a CTA without work: with a cluster, all of its threads meet the others at both barriers
+    const auto leave = [] {
+        if constexpr (kCluster) {
+            __syncwarp();
+            cluster_sync_all();
+            cluster_sync_all();
+        }
+    };
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+
+    const int32_t *bt = a.block_table + (size_t)b * a.max_blocks_per_seq;
+    if (warp == kConsumerWarps && lane == 0) {
+        tma_prefetch_map(&k_map);
+        tma_prefetch_map(&v_map);
+        tma_prefetch_map(&k16_map);
+        tma_prefetch_map(&v16_map);
+    }
+    const int seq_len = __ldg(a.seq_lens + b);
+    // an empty sequence (a padded row of the batch) has nothing to see: zeros, lse -inf
+    if (seq_len == 0) {
+        if (split == 0 && warp < kGroup) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            const int qh = g * kGroup + warp;
+            const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+            store_out4(static_cast<__nv_bfloat16 *>(a.out) + ((size_t)b * kHq + qh) * kD + lane * 4, zero, 0.f);
+            if (a.lse && lane == 0) a.lse[(size_t)b * kHq + qh] = -INFINITY;
+        }
+        leave();
+        return;
+    }
+    if (seq_len < 1 || seq_len > a.max_blocks_per_seq * kBlock) {
+        if (split == 0 && g == 0 && threadIdx.x == 0) record_error(a.err, kErrDevice | kErrBadSeqLen);
+        // (a kernel whose CTAs all left here must not complete before the one it depends on)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        leave();
+        return;
+    }
+    const WindowTiles<kTile> wt(a.window, a.sinks, seq_len - 1, seq_len - 1);
+    const int per_split = a.split_tokens / kTile;
+    const int nsplit_b = (wt.n + per_split - 1) / per_split;
+    if (split >= nsplit_b) {              // past the context
+        leave();
+        return;
+    }
+    // tiles v_begin .. v_begin + n_tiles - 1 of the list of visible ones
+    const int v_len = (wt.n + nsplit_b - 1) / nsplit_b;
+    const int v_begin = split * v_len;
+    const int n_tiles = min(v_len, wt.n - v_begin);
+
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_u32(&sm.full[s]), 1);
+            mbar_init(smem_u32(&sm.empty[s]), kConsumerWarps);
+        }
+        sm.poison = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+
+    if (warp == kConsumerWarps) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            // the cache may be written by the kernel just before this one on the stream
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            int issued = 0;
+            for (int i = 0; i < n_tiles; ++i) {
+                const int st = i % kStages;
+                if (i >= kStages && !mbar_wait(smem_u32(&sm.empty[st]), ((i / kStages) - 1) & 1)) {
+                    record_error(a.err, kErrTimeout);
+                    break;
+                }
+                const int tok = wt.tile(v_begin + i) * kTile;
+                int blk = __ldg(bt + tok / kBlock);
+                if (blk < 0 || blk >= a.num_blocks) {
+                    record_error(a.err, kErrDevice | kErrBadBlock);
+                    sm.poison = 1;
+                    blk = 0;
+                }
+                const uint32_t bar = smem_u32(&sm.full[st]);
+                const size_t srow = ((size_t)blk * kHkv + g) * kBlock;
+                // the stage's 16-row groups that hold a visible token
+                uint32_t need = 0;
+#pragma unroll
+                for (int r = 0; r < kTile / 16; ++r)
+                    if (tok + 16 * r < seq_len && wt.sees_any(tok + 16 * r, 16)) need |= 1u << r;
+                if (need == (1u << (kTile / 16)) - 1) {
+                    mbar_arrive_expect_tx(bar, 2 * kCodeBytes + kSideTx);
+                    tma_load_4d(smem_u32(sm.codes[st][0]), &k_map, bar, 0, g, 0, blk);
+                    tma_load_4d(smem_u32(sm.codes[st][1]), &v_map, bar, 0, g, 0, blk);
+                } else {
+                    mbar_arrive_expect_tx(bar, __popc(need) * 16 * 2 * kFp4RowCodes + kSideTx);
+                    for (int r = 0; r < kTile / 16; ++r) {
+                        if (!(need >> r & 1u)) continue;
+                        tma_load_4d(smem_u32(sm.codes[st][0] + r * 16 * kFp4RowCodes), &k16_map, bar, 0, g, 16 * r, blk);
+                        tma_load_4d(smem_u32(sm.codes[st][1] + r * 16 * kFp4RowCodes), &v16_map, bar, 0, g, 16 * r, blk);
+                    }
+                }
+                bulk_load(smem_u32(sm.scales[st][0]), a.k_scale4 + srow * kFp4Groups, kScaleBytes, bar);
+                bulk_load(smem_u32(sm.exps[st][0]), a.k_exp + srow, kTile, bar);
+                bulk_load(smem_u32(sm.scales[st][1]), a.v_scale4 + srow * kFp4Groups, kScaleBytes, bar);
+                bulk_load(smem_u32(sm.exps[st][1]), a.v_exp + srow, kTile, bar);
+                issued = i + 1;
+            }
+            for (int i = max(0, issued - kStages); i < issued; ++i)
+                mbar_wait(smem_u32(&sm.full[i % kStages]), (i / kStages) & 1);
+        }
+        leave();
+        return;
+    }
+
+    // ---------------------------------------------------------------- consumers
+    const int w = warp;
+    const int gq = lane >> 2;   // fragment row group
+    const int tq = lane & 3;    // fragment column pair
+    const int mi = lane >> 3;   // ldmatrix: which 8x8 matrix this lane addresses
+    const int ri = lane & 7;    // ldmatrix: row within it
+
+    // q may come from the kernel just before this one on the stream
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // Q^T as the B operand of S^T = K Q^T, f16: of 32-dim piece c, k16 step u holds dims 32c + 8tq + 4u ..
+    // + 3 of head gq (the order the code fragments arrive in); heads 4..7 are zero.
+    uint32_t qb[4][2][2];
+    {
+        const uint4 *qrow = reinterpret_cast<const uint4 *>(
+            static_cast<const __nv_bfloat16 *>(a.q) + ((size_t)b * kHq + g * kGroup + (gq & 3)) * kD);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const uint4 v = gq < kGroup ? __ldg(qrow + c * 4 + tq) : make_uint4(0u, 0u, 0u, 0u);
+            qb[c][0][0] = bf16x2_to_f16x2(v.x);
+            qb[c][0][1] = bf16x2_to_f16x2(v.y);
+            qb[c][1][0] = bf16x2_to_f16x2(v.z);
+            qb[c][1][1] = bf16x2_to_f16x2(v.w);
+        }
+    }
+
+    float m0 = -INFINITY, m1 = -INFINITY;   // running max (log2 units) of heads 2tq, 2tq+1
+    float l0 = 0.f, l1 = 0.f;               // this thread's share of the running sums
+    int sigma = kNoSigma;                   // exponent that the accumulator is in units of
+    float acc[8][4];                        // O^T tiles
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[mt][e] = 0.f;
+
+    const int row = w * kWarpTokens + ri + ((mi & 1) << 3);   // token row addressed by this lane (+ 16 u)
+    const uint32_t pick_k = tq & 2 ? 0x7531u : 0x6420u;       // odd or even bytes of a token's 8 scales
+    const uint32_t pick_v = gq & 4 ? 0x7531u : 0x6420u;
+
+    for (int i = 0; i < n_tiles; ++i) {
+        const int st = i % kStages;
+        if (!mbar_wait(smem_u32(&sm.full[st]), (i / kStages) & 1)) {
+            if (lane == 0) record_error(a.err, kErrTimeout);
+            break;
+        }
+        // this warp's 32 rows hold positions p_w .. p_w + 31
+        const int p_w = wt.tile(v_begin + i) * kTile + w * kWarpTokens;
+        const auto valid = [&](int r) { return p_w + r < seq_len && wt.sees(p_w + r); };
+        if (p_w < seq_len && wt.sees_any(p_w, kWarpTokens)) {
+            const uint32_t kc = smem_u32(sm.codes[st][0]);
+            const uint32_t vc = smem_u32(sm.codes[st][1]);
+            const uint8_t *ksc = sm.scales[st][0] + w * kWarpTokens * kFp4Groups;
+            const uint8_t *vsc = sm.scales[st][1] + w * kWarpTokens * kFp4Groups;
+            const uint8_t *kex = sm.exps[st][0] + w * kWarpTokens;
+            const uint8_t *vex = sm.exps[st][1] + w * kWarpTokens;
+
+            // S^T[2 x 16 tokens x 8 heads] = K . Q^T, 64 dims per ldmatrix
+            float s[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[u][e] = 0.f;
+                // scales of tokens gq and gq + 8, one byte per 32-dim piece (this lane's 16-dim half of it)
+                uint32_t sc[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(ksc + (16 * u + 8 * h + gq) * kFp4Groups);
+                    sc[h] = __byte_perm(x.x, x.y, pick_k);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    uint32_t r[4];
+                    ldsm_x4(r, kc + sw64(row + 16 * u, 2 * j + (mi >> 1)));
+                    uint32_t f[2];   // per token: scales of pieces 2j and 2j + 1
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) f[h] = e4m3x2_to_f16x2(sc[h] >> (16 * j));
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t lo[4], hi[4];
+                        e2m1x8_to_f16x2x4(r[2 * c], lo);        // token gq, dims 32(2j+c) + 8tq ..
+                        e2m1x8_to_f16x2x4(r[2 * c + 1], hi);    // token gq + 8
+                        const uint32_t f_lo = __byte_perm(f[0], 0u, c ? 0x3232 : 0x1010);
+                        const uint32_t f_hi = __byte_perm(f[1], 0u, c ? 0x3232 : 0x1010);
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            const uint32_t af[4] = {mul_f16x2(lo[2 * v], f_lo), mul_f16x2(hi[2 * v], f_hi),
+                                                    mul_f16x2(lo[2 * v + 1], f_lo), mul_f16x2(hi[2 * v + 1], f_hi)};
+                            mma_16816_f16(s[u], af, qb[2 * j + c][v][0], qb[2 * j + c][v][1]);
+                        }
+                    }
+                }
+            }
+            // s[u][0]: (token 16u + gq, head 2tq)   s[u][1]: (.., head 2tq+1)
+            // s[u][2]: (token 16u + gq + 8, head 2tq) ...
+            float x[2][4];
+            int ve[2][2];             // V exponents of tokens 16u + gq (+ 8), unbiased
+            float mx0 = -INFINITY, mx1 = -INFINITY;
+            int vmax = kNoSigma;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int t = 16 * u + 8 * h + gq;
+                    const bool ok = valid(t);
+                    const float k = ok ? fp4_unit(kex[t]) * a.scale_log2 : 0.f;
+                    // (columns of padding heads 4..7: finite dummies, results discarded)
+                    x[u][2 * h] = tq >= 2 ? 0.f : ok ? s[u][2 * h] * k : -INFINITY;
+                    x[u][2 * h + 1] = tq >= 2 ? 0.f : ok ? s[u][2 * h + 1] * k : -INFINITY;
+                    mx0 = fmaxf(mx0, x[u][2 * h]);
+                    mx1 = fmaxf(mx1, x[u][2 * h + 1]);
+                    const int e = vex[t];
+                    ve[u][h] = !ok ? kNoSigma : e == (int)kFp4NanExp ? 128 : e ? e - 127 : kNoSigma;
+                    if (ve[u][h] < 128) vmax = max(vmax, ve[u][h]);
+                }
+            }
+            // lazy rescaling, as in decode_fp8.cu: one vote finds the tiles in which a maximum has grown by
+            // more than 2^8 or a V exponent is the largest so far, and only they reduce over the warp
+            float f0 = 1.f, f1 = 1.f;
+            if (__any_sync(0xffffffffu, mx0 > m0 + 8.f || mx1 > m1 + 8.f || vmax > sigma)) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+                    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+                }
+                const bool up0 = mx0 > m0 + 8.f, up1 = mx1 > m1 + 8.f;   // also when m == -inf
+                const float mn0 = up0 ? mx0 : m0, mn1 = up1 ? mx1 : m1;
+                const float alpha0 = up0 ? fast_exp2(m0 - mn0) : 1.f, alpha1 = up1 ? fast_exp2(m1 - mn1) : 1.f;
+                m0 = mn0;
+                m1 = mn1;
+                l0 *= alpha0;
+                l1 *= alpha1;
+                const int top = __reduce_max_sync(0xffffffffu, vmax);
+                const float grow = top > sigma ? pow2_or_0(sigma - top) : 1.f;
+                sigma = max(sigma, top);
+                f0 = alpha0 * grow;
+                f1 = alpha1 * grow;
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt) {
+                    acc[mt][0] *= f0;
+                    acc[mt][1] *= f1;
+                    acc[mt][2] *= f0;
+                    acc[mt][3] *= f1;
+                }
+            }
+            uint32_t pb[2][2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float p0 = fast_exp2(x[u][2 * h] - m0), p1 = fast_exp2(x[u][2 * h + 1] - m1);
+                    l0 += p0;
+                    l1 += p1;
+                    const float r = ve[u][h] == 128 ? __int_as_float(0x7fc00000) : pow2_or_0(ve[u][h] - sigma);
+                    // P^T as the B operand of O^T += V^T P^T: transpose the 8x8 16-bit blocks
+                    pb[u][h] = movmatrix_trans(pack_f16x2(p0 * r, p1 * r));
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                // scales of tokens 2tq, 2tq + 1 and 2tq + 8, 2tq + 9: one pair per 32-dim piece
+                uint32_t f[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int t = 16 * u + 8 * h + 2 * tq;
+                    const uint4 y = *reinterpret_cast<const uint4 *>(vsc + t * kFp4Groups);
+                    const uint32_t s0 = valid(t) ? __byte_perm(y.x, y.y, pick_v) : 0u;
+                    const uint32_t s1 = valid(t + 1) ? __byte_perm(y.z, y.w, pick_v) : 0u;
+                    const uint32_t lo = __byte_perm(s0, s1, 0x5140), hi = __byte_perm(s0, s1, 0x7362);
+                    f[h][0] = e4m3x2_to_f16x2(lo);
+                    f[h][1] = e4m3x2_to_f16x2(lo >> 16);
+                    f[h][2] = e4m3x2_to_f16x2(hi);
+                    f[h][3] = e4m3x2_to_f16x2(hi >> 16);
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    // matrices: tokens 0-7 / 8-15 of the tile x pieces 2j / 2j + 1
+                    uint32_t r[4];
+                    ldsm_x4_trans(r, vc + sw64(row + 16 * u, 2 * j + (mi >> 1)));
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t lo[4], hi[4];
+                        e2m1x8_to_f16x2x4(r[2 * c], lo);        // {token 2tq: dims 4gq..; token 2tq+1}
+                        e2m1x8_to_f16x2x4(r[2 * c + 1], hi);    // tokens 2tq + 8, 2tq + 9
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            const uint32_t af[4] = {
+                                mul_f16x2(__byte_perm(lo[v], lo[2 + v], 0x5410), f[0][2 * j + c]),
+                                mul_f16x2(__byte_perm(lo[v], lo[2 + v], 0x7632), f[0][2 * j + c]),
+                                mul_f16x2(__byte_perm(hi[v], hi[2 + v], 0x5410), f[1][2 * j + c]),
+                                mul_f16x2(__byte_perm(hi[v], hi[2 + v], 0x7632), f[1][2 * j + c])};
+                            mma_16816_f16(acc[2 * (2 * j + c) + v], af, pb[u][0], pb[u][1]);
+                        }
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.empty[st]));
+    }
+
+    // ------------------------------------------------------------ merge the warps
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, o);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
+    }
+    // the merge arrays overlay the stages: every consumer warp must be done with them
+    named_barrier(1, kConsumerWarps * 32);
+    if (tq < 2) {
+#pragma unroll
+        for (int mt = 0; mt < 8; ++mt) {
+            const int d = (mt >> 1) * 32 + 4 * gq + 2 * (mt & 1);
+            *reinterpret_cast<float2 *>(&sm.mg.o[w][2 * tq][d]) = make_float2(acc[mt][0], acc[mt][2]);
+            *reinterpret_cast<float2 *>(&sm.mg.o[w][2 * tq + 1][d]) = make_float2(acc[mt][1], acc[mt][3]);
+        }
+        if (gq == 0) {
+            sm.mg.m[w][2 * tq] = m0;
+            sm.mg.m[w][2 * tq + 1] = m1;
+            sm.mg.l[w][2 * tq] = l0;
+            sm.mg.l[w][2 * tq + 1] = l1;
+        }
+    }
+    if (lane == 0) sm.mg.sigma[w] = sigma;
+    named_barrier(1, kConsumerWarps * 32);
+    const bool bad = *reinterpret_cast<volatile int *>(&sm.poison) != 0;
+
+    // the first 128 consumer threads merge (4 heads x 32 threads x 4 dims)
+    const int c = threadIdx.x;
+    if (c >= kGroup * 32) {
+        // the others only take part in the partials' barriers below
+        if (kCluster) {
+            leave();
+        } else if (nsplit_b > 1) {
+            named_barrier(2, kConsumerWarps * 32);
+            named_barrier(2, kConsumerWarps * 32);
+        }
+        return;
+    }
+    const int h = c >> 5;               // query head within the group
+    const int d0 = (c & 31) * 4;        // 4 dims per thread
+    float M = -INFINITY;
+#pragma unroll
+    for (int ww = 0; ww < kConsumerWarps; ++ww) M = fmaxf(M, sm.mg.m[ww][h]);
+    float L = 0.f, o4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ww = 0; ww < kConsumerWarps; ++ww) {
+        const float e = fast_exp2(sm.mg.m[ww][h] - M);
+        L += sm.mg.l[ww][h] * e;
+        const float eo = e * pow2_or_0(sm.mg.sigma[ww]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o4[k] += sm.mg.o[ww][h][d0 + k] * eo;
+    }
+    if (bad) {
+        M = L = __int_as_float(0x7fc00000);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o4[k] = __int_as_float(0x7fc00000);
+    }
+    const int qh = g * kGroup + h;      // query head
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + ((size_t)b * kHq + qh) * kD + d0;
+
+    if constexpr (kCluster) {
+        // this split's partial into its own shared memory: thread c alone read entries
+        // [.][h][d0 .. d0+3] of the merge arrays, so it may overwrite warp 0's
+        *reinterpret_cast<float4 *>(&sm.mg.o[0][h][d0]) = make_float4(o4[0], o4[1], o4[2], o4[3]);
+        if ((c & 31) == 0) {
+            sm.cl_ml[h][0] = M;
+            sm.cl_ml[h][1] = L;
+        }
+        cluster_sync_all();   // every split's partial is in place
+        if (split == 0) {
+            float GM = M;
+            for (int k = 1; k < nsplit_b; ++k)
+                GM = fmaxf(GM, ld_cluster_f32(peer_addr(smem_u32(&sm.cl_ml[h][0]), (uint32_t)k)));
+            float GL = 0.f, go[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < nsplit_b; ++k) {
+                const float mk = ld_cluster_f32(peer_addr(smem_u32(&sm.cl_ml[h][0]), (uint32_t)k));
+                const float lk = ld_cluster_f32(peer_addr(smem_u32(&sm.cl_ml[h][1]), (uint32_t)k));
+                const float4 ok = ld_cluster_f4(peer_addr(smem_u32(&sm.mg.o[0][h][d0]), (uint32_t)k));
+                const float e = fast_exp2(mk - GM);
+                GL += lk * e;
+                go[0] += ok.x * e;
+                go[1] += ok.y * e;
+                go[2] += ok.z * e;
+                go[3] += ok.w * e;
+            }
+            if (nsplit_b > 1 && !(GL == GL)) GM = GL;   // a poisoned split (its NaN maximum loses in fmaxf)
+            store_out4(out, go, 1.f / GL);
+            if (a.lse && (c & 31) == 0) a.lse[(size_t)b * kHq + qh] = (GM + __log2f(GL)) * kLn2;
+        }
+        cluster_sync_all();   // the peers' shared memory stays until split 0 has read it
+        return;
+    }
+
+    if (nsplit_b == 1) {
+        store_out4(out, o4, 1.f / L);
+        if (a.lse && (c & 31) == 0) a.lse[(size_t)b * kHq + qh] = (M + __log2f(L)) * kLn2;
+        return;
+    }
+
+    // ------------------------------------------------------------ split-K partials
+    const size_t entry = (size_t)pair * a.nsplit + split;
+    *reinterpret_cast<float4 *>(a.part_o + (entry * kGroup + h) * kD + d0) =
+        make_float4(o4[0], o4[1], o4[2], o4[3]);
+    if ((c & 31) == 0) {
+        a.part_ml[(entry * kGroup + h) * 2 + 0] = M;
+        a.part_ml[(entry * kGroup + h) * 2 + 1] = L;
+    }
+    __threadfence();
+    named_barrier(2, kConsumerWarps * 32);
+    if (c == 0) {
+        const int prev = atomicAdd(a.counters + pair, 1);
+        sm.last_cta = (prev == nsplit_b - 1);
+    }
+    named_barrier(2, kConsumerWarps * 32);
+    if (!sm.last_cta) return;
+
+    // The last CTA of this (sequence, KV head) merges every split by log-sum-exp.
+    __threadfence();
+    if (c == 0) a.counters[pair] = 0;   // ready for the next call
+    const size_t e0 = (size_t)pair * a.nsplit;
+    float GM = -INFINITY;
+    for (int k = 0; k < nsplit_b; ++k) GM = fmaxf(GM, __ldcg(a.part_ml + ((e0 + k) * kGroup + h) * 2));
+    float GL = 0.f, go[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = 0; k < nsplit_b; ++k) {
+        const float mk = __ldcg(a.part_ml + ((e0 + k) * kGroup + h) * 2);
+        const float lk = __ldcg(a.part_ml + ((e0 + k) * kGroup + h) * 2 + 1);
+        const float e = fast_exp2(mk - GM);
+        const float4 ok = __ldcg(reinterpret_cast<const float4 *>(a.part_o + ((e0 + k) * kGroup + h) * kD + d0));
+        GL += lk * e;
+        go[0] += ok.x * e;
+        go[1] += ok.y * e;
+        go[2] += ok.z * e;
+        go[3] += ok.w * e;
+    }
+    if (!(GL == GL)) GM = GL;
+    store_out4(out, go, 1.f / GL);
+    if (a.lse && (c & 31) == 0) a.lse[(size_t)b * kHq + qh] = (GM + __log2f(GL)) * kLn2;
+}
+
+}  // namespace
+
+cudaError_t launch_decode_fp4(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                              const CUtensorMap &k16_map, const CUtensorMap &v16_map, cudaStream_t stream) {
+    if (a.batch == 0) return cudaSuccess;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<bool> configured[64] = {};
+    if (dev < 0 || dev >= 64 || !configured[dev].load()) {
+        for (const auto kernel : {decode_fp4_kernel<false>, decode_fp4_kernel<true>}) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+            if (e != cudaSuccess) return e;
+        }
+        if (dev >= 0 && dev < 64) configured[dev].store(true);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.batch * kHkv, a.nsplit);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (a.cluster_merge) {
+        if (a.nsplit < 1 || a.nsplit > 8) return cudaErrorInvalidValue;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 1;
+        attr[1].val.clusterDim.y = (unsigned)a.nsplit;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+        e = cudaLaunchKernelEx(&cfg, decode_fp4_kernel<true>, k_map, v_map, k16_map, v16_map, a);
+        if (e != cudaErrorLaunchOutOfResources && e != cudaErrorInvalidClusterSize && e != cudaErrorNotSupported &&
+            e != cudaErrorCooperativeLaunchTooLarge)
+            return e;
+        cudaGetLastError();   // the cluster was refused: merge through the workspace instead
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, decode_fp4_kernel<false>, k_map, v_map, k16_map, v16_map, a);
+}
+
+}  // namespace pa

@@ -16,6 +16,10 @@
 // [block][head][slot].  Page "从零搭建AI工程能力：手写KV Cache与动态批处理实战" §3.2: an 8-bit
 // KV cache halves its memory.
 //
+// The 4-bit variant (k_exp set; the format and its rule: fp4.cuh) takes the same half-warp per row: a
+// lane holds 8 values, two lanes a group of 16.  16384 ragged tokens: see rope_append.cu, which reads
+// the same rows.
+//
 // The kernel is a chain of dependent loads (which sequence owns the token, its
 // length, its block id, then the data), so its time is latency: the owner is first
 // guessed in proportion (exact for one token per sequence and for one sequence) and
@@ -23,6 +27,7 @@
 // stream start its own prologue early (programmatic dependent launch); that kernel
 // waits for this one to finish before it reads the pools.
 #include "common.cuh"
+#include "fp4.cuh"
 #include "launch.h"
 #include "tokens.cuh"
 
@@ -31,7 +36,8 @@ namespace {
 
 constexpr int kWarps = 8;  // 4 tokens x {K, V} per CTA
 
-template <bool kFp8>
+// kBits: 16 (copied), 8 or 4
+template <int kBits>
 __global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(AppendArgs a) {
     // The pools are this kernel's only output: a dependent kernel may launch now and
     // run its prologue; it waits for our completion before touching the pools.
@@ -82,11 +88,47 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(AppendArgs a) {
         return;
     }
     const int slot = p % kBlock;
-    if constexpr (!kFp8) {
+    if constexpr (kBits == 16) {
         uint4 *dst = reinterpret_cast<uint4 *>(static_cast<char *>(is_v ? a.v_pool : a.k_pool) +
                                                ((size_t)blk * kBlock + slot) * kTokenBytes);
 #pragma unroll
         for (int k = 0; k < 4; ++k) dst[lane + 32 * k] = v[k];
+    } else if constexpr (kBits == 4) {
+        // vector k of lane l: KV head 2k + l/16, dims 8 (l%16) .. 8 (l%16) + 7
+        uint8_t *codes = static_cast<uint8_t *>(is_v ? a.v_pool : a.k_pool) +
+                         ((size_t)blk * kBlock + slot) * (kHkv * kFp4RowCodes);
+        const size_t row0 = (size_t)blk * kHkv * kBlock + slot;   // + head * 256
+        uint8_t *scales = is_v ? a.v_scale4 : a.k_scale4;
+        uint8_t *exps = is_v ? a.v_exp : a.k_exp;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            float y[8];
+            uint32_t amax = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                y[2 * e] = bf16_lo(w[e]);
+                y[2 * e + 1] = bf16_hi(w[e]);
+                amax = max(amax, max(__float_as_uint(fabsf(y[2 * e])), __float_as_uint(fabsf(y[2 * e + 1]))));
+            }
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) amax = umax_xor(amax, o);
+            const uint32_t exp = fp4_row_exp(amax);
+            const float unit = fp4_unit_inverse(exp);
+            float top = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                y[e] *= unit;
+                top = fmaxf(top, fabsf(y[e]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            const uint32_t scale = fp4_group_scale(top);
+            const int head = 2 * k + (lane >> 4), chunk = lane & 15;
+            *reinterpret_cast<uint32_t *>(codes + head * kFp4RowCodes + chunk * 4) = fp4_codes(y, scale);
+            const size_t row = row0 + (size_t)head * kBlock;
+            if (!(chunk & 1)) scales[row * kFp4Groups + (chunk >> 1)] = (uint8_t)scale;
+            if (chunk == 0) exps[row] = (uint8_t)exp;
+        }
     } else {
         // vector k of lane l: KV head 2k + l/16, dims 8 (l%16) .. 8 (l%16) + 7
         uint8_t *codes = static_cast<uint8_t *>(is_v ? a.v_pool : a.k_pool) +
@@ -125,10 +167,12 @@ cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream) {
     if (a.total_tokens == 0) return cudaSuccess;
     const int tokens_per_cta = kWarps / 2;
     const int grid = (a.total_tokens + tokens_per_cta - 1) / tokens_per_cta;
-    if (a.k_scale)
-        kv_append_kernel<true><<<grid, kWarps * 32, 0, stream>>>(a);
+    if (a.k_exp)
+        kv_append_kernel<4><<<grid, kWarps * 32, 0, stream>>>(a);
+    else if (a.k_scale)
+        kv_append_kernel<8><<<grid, kWarps * 32, 0, stream>>>(a);
     else
-        kv_append_kernel<false><<<grid, kWarps * 32, 0, stream>>>(a);
+        kv_append_kernel<16><<<grid, kWarps * 32, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

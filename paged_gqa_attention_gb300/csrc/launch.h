@@ -23,6 +23,32 @@ struct AppendArgs {
     int32_t num_seqs;
     int32_t total_tokens;
     uint32_t *err;
+    // 4-bit cache only (fp4.cuh; the pools are its codes): E4M3 scales [num_blocks][8][256][8] and
+    // exponents [num_blocks][8][256], else null
+    uint8_t *k_scale4;
+    uint8_t *v_scale4;
+    uint8_t *k_exp;
+    uint8_t *v_exp;
+};
+
+// Rows of the 8-bit or the 4-bit cache read back as bf16 (kv_read.cu).
+struct ReadArgs {
+    void *k_out;            // [total_rows][8][128] bf16
+    void *v_out;
+    const void *k_codes;
+    const void *v_codes;
+    const void *k_scale;    // fp32 [num_blocks][8][256], or E4M3 [num_blocks][8][256][8] when k_exp is set
+    const void *v_scale;
+    const uint8_t *k_exp;
+    const uint8_t *v_exp;
+    const int32_t *block_table;
+    int32_t max_blocks_per_seq;
+    int32_t num_blocks;
+    const int32_t *cu_rows;
+    const int32_t *first;
+    int32_t num_seqs;
+    int32_t total_rows;
+    uint32_t *err;
 };
 
 struct DecodeArgs {
@@ -67,6 +93,11 @@ struct DecodeArgs {
     // bf16 and windowed decode only: 1 = the splits of a (sequence, KV head) form a cluster (nsplit <= 8)
     // and merge through its shared memory; the counters and partials are not used.
     int32_t cluster_merge;
+    // 4-bit cache only (fp4.cuh): k_scale / v_scale above are not used
+    const uint8_t *k_scale4;   // E4M3 [num_blocks][8][256][8]
+    const uint8_t *v_scale4;
+    const uint8_t *k_exp;      // [num_blocks][8][256]
+    const uint8_t *v_exp;
 };
 
 struct PrefillArgs {
@@ -105,6 +136,12 @@ struct PrefillArgs {
     int32_t window;
     int32_t sinks;
     int32_t unit_ctas;   // CTAs that share a work unit (chosen by launch_prefill_window)
+    // Low-bit caches (launch_prefill_quant): scales and, in 4 bits, exponents of the rows, laid out as
+    // in ReadArgs.
+    const void *k_scale;
+    const void *v_scale;
+    const uint8_t *k_exp;
+    const uint8_t *v_exp;
 };
 
 constexpr int kRopePairs = 64;   // rotated pairs of a 128-dim head
@@ -163,10 +200,15 @@ struct RopeAppendArgs {
     const void *q_norm;     // bf16 gains [128] of the q and the k heads, or null: no norm
     const void *k_norm;
     float norm_eps;
+    uint8_t *k_scale4;      // 4-bit cache, as in AppendArgs
+    uint8_t *v_scale4;
+    uint8_t *k_exp;
+    uint8_t *v_exp;
 };
 
 cudaError_t launch_kv_append(const AppendArgs &a, cudaStream_t stream);
 cudaError_t launch_rope_append(const RopeAppendArgs &a, int num_sms, cudaStream_t stream);
+cudaError_t launch_kv_read(const ReadArgs &a, cudaStream_t stream);
 
 // x_map: x [total_tokens][hidden] bf16, box {64, qkv_tile_rows_loaded(total_tokens)}; w_map:
 // w [6144][hidden] bf16, box {64, qkv_weight_box_rows()}; both 128-byte swizzle.
@@ -220,6 +262,11 @@ cudaError_t launch_prefill_window(PrefillArgs a, long long tiles, const CUtensor
 
 // The prefill with the append of the new tokens fused in (a.k_new set): kn_map / vn_map are
 // 3-D maps (dim, head, token) over k_new / v_new with box {64, 1, 128}.
+// The same over the 8-bit cache, or the 4-bit one when a.k_exp is set: maps over the code pools.
+cudaError_t launch_prefill_quant(PrefillArgs a, long long tiles, const CUtensorMap &q_map, const CUtensorMap &k_map,
+                                 const CUtensorMap &v_map, const CUtensorMap &k16_map, const CUtensorMap &v16_map,
+                                 int num_sms, cudaStream_t stream);
+
 cudaError_t launch_prefill_append(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
                                   const CUtensorMap &v_map, const CUtensorMap &kn_map, const CUtensorMap &vn_map,
                                   int num_sms, cudaStream_t stream);
@@ -231,7 +278,12 @@ cudaError_t launch_wait_selftest(uint32_t *err, uint64_t limit_ns, cudaStream_t 
 // failure.
 void *static_scratch_address(cudaError_t *status);
 
+// Decode over the 4-bit cache, window (or all of the context) and sinks as above.
+cudaError_t launch_decode_fp4(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
+                              const CUtensorMap &k16_map, const CUtensorMap &v16_map, cudaStream_t stream);
+
 // Tile sizes the tensor maps must be encoded with.
+constexpr int kDecodeFp4TileTokens = 256;
 constexpr int kDecodeTileTokens = 64;    // decode: rows per TMA box
 constexpr int kPrefillKvTile = 128;      // prefill: K/V rows per TMA box
 constexpr int kPrefillQPositions = 32;   // prefill: query positions per tile (x4 heads)

@@ -1,0 +1,913 @@
+// prefill_quant.cu -- causal (chunked) prefill attention over the 8-bit or the 4-bit KV cache, with an
+// optional sliding window, on the 5th-generation tensor cores.
+//
+// Page "从零搭建AI工程能力：手写KV Cache与动态批处理实战" §3.2 stores the KV cache in 8 bits, §3.3 cuts
+// long prompts into chunks that attend to the cached context before them; here both at once.  The
+// attention, its work units, key lists, tiles and tensor memory are those of the windowed form of
+// prefill.cu (a window as long as the context is plain causal attention); what differs is how a key
+// tile comes into being.
+//
+// Codes are not operands: their row scales run along the keys, and a 4-bit row has a scale for every 16
+// dimensions besides.  So the products run in f16, and four warps turn code tiles into f16 tiles in
+// shared memory while the tensor cores work on the tiles before:
+//   K' = code * s / 2^E,      E the exponent of the tile's largest scale: a magnitude of at most 448 (2688
+//                             in 4 bits); the scores are multiplied by 2^E together with the softmax scale
+//   V' = code * s / sigma,    sigma the power of two above the first tile's largest scale, taken anew only
+//                             when a tile's V' could leave f16; O is then rescaled, as it is for the
+//                             running maximum, and the epilogue multiplies by sigma
+// with one rounding to f16 (8 bits: the scale is split into a sum of two f16, so that code * scale is rounded
+// once, to 2^-12 of the value at most half a step; 4 bits: exact).  Values 2^-14 of the largest and less lose bits one by one.
+// Q is converted to f16 in place (|q| < 65504, as for the decode over these caches), P is f16.
+// A code tile is converted once per 64 positions: 2 x 16384 values, three instructions a pair, against
+// 4 x 128 x 128 x 256 operations of products; what the conversion costs is shared-memory traffic, 48 KiB
+// an operand tile next to the products' reads.
+//
+// CTA = 16 warps, persistent, one per SM:
+//   warps 0-3, 4-7  softmax + epilogue of query tiles A and B (thread = row = TMEM lane), 184 registers
+//   warp 8          TMA producer: Q, and the ring of code tiles in the order K(0) V(0) K(1) V(1) ...
+//   warp 9          TMEM allocator and tcgen05.mma issuer
+//   warps 12-15     converters (warps 8-15: 72 registers)
+// Every wait is bounded; on expiry the CTA records PA_ERR_TIMEOUT, unwinds, waits (bounded) for its own
+// copies and MMAs, frees tensor memory and exits.
+#include <atomic>
+#include <cstddef>
+
+#include <cuda_fp16.h>
+
+#include "cluster.cuh"
+#include "common.cuh"
+#include "fp4.cuh"
+#include "launch.h"
+#include "prefill_common.cuh"
+#include "window.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kProducerWarp = 8;
+constexpr int kMmaWarp = 9;
+constexpr int kConvertWarp = 12;              // 12-15
+constexpr int kConvertWarps = 4;
+constexpr int kThreads = 16 * 32;
+// registers a thread: 2 x 128 x 184 + 2 x 128 x 72 = 512 x 128, what the block is launched with
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+constexpr uint32_t kTileBytes = 2 * kHalf;    // a 128 x 128 f16 tile
+constexpr int kStages = 2;                    // f16 tiles of K and of V
+constexpr int kParams = 4;                    // see TileParams
+
+// f16 operands and fp32 accumulation: formats 0 where idesc_bf16 has 1
+constexpr uint32_t idesc_f16(int m, int n, bool b_mn_major) {
+    return idesc_bf16(m, n, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+constexpr uint32_t kIdescQK = idesc_f16(kRows, kKT, false);
+constexpr uint32_t kIdescPV = idesc_f16(kRows, kD, true);
+
+// Code tiles on their way in, with their scales: a ring of slots, K and V in turn.  A K tile brings along
+// the V scales of the same rows (in 4 bits their exponents), from which sigma is chosen before the softmax
+// needs it; with two slots those of K are all the first one's.
+template <int kBits>
+struct CodeRing;
+template <>
+struct CodeRing<8> {
+    static constexpr int kSlots = 2, kRow = kD;
+    uint8_t codes[kSlots][kKT * kRow];
+    float scale[kSlots][kKT];
+    float v_scale[1][kKT];
+};
+template <>
+struct CodeRing<4> {
+    static constexpr int kSlots = 3, kRow = kFp4RowCodes;
+    uint8_t codes[kSlots][kKT * kRow];
+    uint8_t scale[kSlots][kKT * kFp4Groups];
+    uint8_t exp[kSlots][kKT];
+    uint8_t v_exp[kSlots][kKT];
+};
+
+// What the softmax needs of key tile `it`, in entry it % 4.  Entry it is written when K(it) is converted,
+// which needs the slot of K(it - 2), so S_B(it - 2); that was issued after O_B += P_B(it - 3) V, so both
+// query tiles' softmax have read entry it - 3 by then: 4 entries are enough.
+struct TileParams {
+    float k_unit;             // 2^E
+    float sigma;
+    float grow;               // the factor that brings O to units of sigma (1, or sigma has just grown)
+};
+
+template <int kBits>
+struct QuantSmem {
+    uint8_t q[2][2][kHalf];          // [tile A|B][dims 0-63 | 64-127]
+    uint8_t k[kStages][2][kHalf];
+    uint8_t v[kStages][2][kHalf];
+    union {
+        CodeRing<kBits> ring;
+        float ml[2 * kRows][2];      // kSplit, at the end: running maximum and sum of every row
+    };
+    uint64_t q_full, q_ready, q_empty;
+    uint64_t c_full[CodeRing<kBits>::kSlots], c_empty[CodeRing<kBits>::kSlots];
+    uint64_t k_full[kStages], k_empty[kStages];
+    uint64_t v_full[kStages], v_empty[kStages];
+    uint64_t s_full[2], p_half[2][2], o_done[2];   // per query tile (P in two key halves)
+    uint64_t mma_idle;
+    TileParams params[kParams];
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(offsetof(QuantSmem<8>, k) == sizeof(QuantSmem<8>::q) &&
+                  sizeof(QuantSmem<8>::q) + sizeof(QuantSmem<8>::k) == 2 * kRows * kD * sizeof(float),
+              "split merge area");
+
+template <int kBits>
+constexpr size_t kSmemBytes = sizeof(QuantSmem<kBits>) + 1024;
+static_assert(kSmemBytes<8> <= 232448 && kSmemBytes<4> <= 232448, "shared memory");
+
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs)); }
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs)); }
+
+// c + the f16 in the low / high half of v
+__device__ __forceinline__ float add_f16_lo(uint32_t v, float c) {
+    float d;
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n add.rn.f32.f16 %0, lo, %2;\n}" : "=f"(d) : "r"(v), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float add_f16_hi(uint32_t v, float c) {
+    float d;
+    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n add.rn.f32.f16 %0, hi, %2;\n}" : "=f"(d) : "r"(v), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+
+// The work unit dealt as the r-th of this CTA.
+template <bool kPlanned, bool kSplit>
+__device__ __forceinline__ Unit unit_for(const PrefillArgs &a, int idx, int qblocks) {
+    if constexpr (kSplit) {
+        // this CTA's run of the unit's key tiles (none: it only takes part in the merge)
+        Unit t = unit_at<false, true>(a, idx, qblocks);
+        if (!t.run) return t;
+        const int len = (t.n_kt + a.unit_ctas - 1) / a.unit_ctas;
+        t.kt0 = (int)(blockIdx.x % a.unit_ctas) * len;
+        t.n_kt = min(len, t.n_kt - t.kt0);
+        if (t.n_kt <= 0) t.run = false;
+        return t;
+    }
+    return unit_at<false, true>(a, kPlanned ? __ldg(a.order + idx) : idx, qblocks);
+}
+
+// Fetch rows c0 .. c0 + 127 of the unit's key list (load_list_tile's rule in prefill.cu): codes in
+// boxes of 64 and 16 rows, their scales beside them a run at a time.  Block ids are reported by K.
+template <int kBits>
+__device__ __forceinline__ void load_codes(const PrefillArgs &a, const Unit &t, const int32_t *bt, int c0, bool is_k,
+                                           CodeRing<kBits> &ring, int st, uint32_t bar, const CUtensorMap *map64,
+                                           const CUtensorMap *map16) {
+    constexpr int kRow = CodeRing<kBits>::kRow;
+    constexpr int kScales = kBits == 8 ? 4 : kFp4Groups + 1;
+    const int rows = min(kKT, ((t.win.rows + 15) & ~15) - c0);
+    mbar_arrive_expect_tx(bar, (uint32_t)rows * (kRow + kScales + (is_k ? (kBits == 8 ? 4 : 1) : 0)));
+    for (int r = 0; r < rows;) {
+        const int p = t.win.position(c0 + r);
+        int run = min(rows - r, kBlock - p % kBlock);
+        if (c0 + r < t.win.s16) run = min(run, t.win.s16 - c0 - r);
+        int blk = __ldg(bt + p / kBlock);
+        if (blk < 0 || blk >= a.num_blocks) {
+            if (is_k) record_error(a.err, kErrDevice | kErrBadBlock);
+            blk = 0;   // stay inside the pool; the result is flagged as invalid
+        }
+        int off = p % kBlock;
+        const size_t row = ((size_t)blk * kHkv + t.g) * kBlock + off;   // (off and run are multiples of 16)
+        if constexpr (kBits == 8) {
+            bulk_load(smem_u32(ring.scale[st] + r), static_cast<const float *>(is_k ? a.k_scale : a.v_scale) + row, run * 4, bar);
+            if (is_k) bulk_load(smem_u32(ring.v_scale[0] + r), static_cast<const float *>(a.v_scale) + row, run * 4, bar);
+        } else {
+            bulk_load(smem_u32(ring.scale[st] + r * kFp4Groups),
+                      static_cast<const uint8_t *>(is_k ? a.k_scale : a.v_scale) + row * kFp4Groups, run * kFp4Groups, bar);
+            bulk_load(smem_u32(ring.exp[st] + r), (is_k ? a.k_exp : a.v_exp) + row, run, bar);
+            if (is_k) bulk_load(smem_u32(ring.v_exp[st] + r), a.v_exp + row, run, bar);
+        }
+        while (run > 0) {
+            const int n = run >= 64 ? 64 : 16;
+            tma_load_4d(smem_u32(ring.codes[st] + r * kRow), run >= 64 ? map64 : map16, bar, 0, t.g, off, blk);
+            r += n;
+            off += n;
+            run -= n;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- conversion (one warp's share)
+
+// Largest scale of the tile's live rows, as exponent: the least n with scale < 2^n (8 bits; scales that are
+// zero, infinite or NaN leave it out), or the largest exponent byte - 127 (4 bits).  kNone: no such row.
+constexpr int kNone = -1000;
+
+__device__ __forceinline__ int top_exponent(const CodeRing<8> &s, int st, bool of_v, const DeadRows &dead, int lane) {
+    const float4 x = *reinterpret_cast<const float4 *>((of_v ? s.v_scale[0] : s.scale[st]) + 4 * lane);
+    const float v[4] = {x.x, x.y, x.z, x.w};
+    int top = 0;   // biased exponent + 1 of the largest
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * lane + i;
+        const uint32_t bits = __float_as_uint(v[i]) & 0x7fffffffu;
+        const bool live = !(r >= dead.lo && r < dead.hi) && r < dead.tail;
+        if (live && bits < 0x7f800000u && bits) top = max(top, (int)(bits >> 23) + 1);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    return top ? top - 127 : kNone;
+}
+
+__device__ __forceinline__ int top_exponent(const CodeRing<4> &s, int st, bool of_v, const DeadRows &dead, int lane) {
+    const uint32_t x = *reinterpret_cast<const uint32_t *>((of_v ? s.v_exp[st] : s.exp[st]) + 4 * lane);
+    int top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * lane + i, e = (int)(x >> (8 * i) & 0xffu);
+        const bool live = !(r >= dead.lo && r < dead.hi) && r < dead.tail;
+        if (live && e < (int)kFp4NanExp) top = max(top, e);
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    return top ? top - 127 : kNone;
+}
+
+// 2^n as a float for n in -126 .. 127 (clamped).
+__device__ __forceinline__ float exp2_int(int n) { return __uint_as_float((uint32_t)(min(max(n, -126), 127) + 127) << 23); }
+
+// 16 values of row r, dims 16 chunk .. 16 chunk + 15, from the slot into an f16 tile: code * scale * unit,
+// `unit` a power of two.
+__device__ __forceinline__ void convert16(const CodeRing<8> &s, int st, int r, int chunk, float unit, uint32_t (&h)[8]) {
+    const uint4 c = *reinterpret_cast<const uint4 *>(s.codes[st] + sw128(r, chunk));
+    const float x = s.scale[st][r] * unit;
+    // the scale as hi + lo, so that code * scale is rounded once (code * lo is far below the last place)
+    const __half hi = __float2half_rn(x);
+    const __half lo = __float2half_rn(x - __half2float(hi));
+    const uint32_t hi2 = (uint32_t)__half_as_ushort(hi) * 0x10001u, lo2 = (uint32_t)__half_as_ushort(lo) * 0x10001u;
+    e4m3x4_to_f16x2x2(c.x, h[0], h[1]);
+    e4m3x4_to_f16x2x2(c.y, h[2], h[3]);
+    e4m3x4_to_f16x2x2(c.z, h[4], h[5]);
+    e4m3x4_to_f16x2x2(c.w, h[6], h[7]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = fma_f16x2(h[i], hi2, mul_f16x2(h[i], lo2));
+}
+
+__device__ __forceinline__ void convert16(const CodeRing<4> &s, int st, int r, int chunk, float unit, uint32_t (&h)[8]) {
+    // 64-byte rows, 64-byte swizzle: 16-byte piece p of row r is at p ^ (r / 2 % 4)
+    const uint2 c = *reinterpret_cast<const uint2 *>(s.codes[st] + r * kFp4RowCodes +
+                                                     ((((chunk >> 1) ^ (r >> 1)) & 3) << 4) + ((chunk & 1) << 3));
+    const float x = e4m3_value(s.scale[st][r * kFp4Groups + chunk]) * (fp4_unit(s.exp[st][r]) * unit);
+    const uint32_t x2 = (uint32_t)__half_as_ushort(__float2half_rn(x)) * 0x10001u;
+    uint32_t lo[4], hi[4];
+    e2m1x8_to_f16x2x4(c.x, lo);
+    e2m1x8_to_f16x2x4(c.y, hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i] = mul_f16x2(lo[i], x2);
+        h[4 + i] = mul_f16x2(hi[i], x2);
+    }
+}
+
+// This warp's 32 rows of a tile: a lane 16 values at a time, four rows a warp instruction.  Dead rows are
+// zeros: their codes and scales may be anything, and 0 * NaN is not 0.
+template <int kBits>
+__device__ __forceinline__ void convert_tile(const CodeRing<kBits> &s, int st, uint8_t (*dst)[kHalf], float unit,
+                                             const DeadRows &dead, int w, int lane) {
+    const int chunk = lane & 7, half = chunk >> 2;
+    // lanes of the upper half of the dims store their two pieces in the other order: the halves of the tile
+    // are 16 KiB apart, and each store then meets every bank once
+    const int first = 2 * (chunk & 3) + half, second = 2 * (chunk & 3) + 1 - half;
+#pragma unroll 4
+    for (int i = 0; i < 8; ++i) {
+        const int r = w * 32 + i * 4 + (lane >> 3);
+        uint32_t h[8];
+        convert16(s, st, r, chunk, unit, h);
+        const bool live = !(r >= dead.lo && r < dead.hi) && r < dead.tail;
+        const uint4 p0 = live ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 p1 = live ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4 *>(dst[half] + sw128(r, first)) = half ? p1 : p0;
+        *reinterpret_cast<uint4 *>(dst[half] + sw128(r, second)) = half ? p0 : p1;
+    }
+}
+
+// Q in place, bf16 -> f16: this warp's quarter.
+__device__ __forceinline__ void convert_q(uint8_t *q, int w, int lane) {
+    uint4 *p = reinterpret_cast<uint4 *>(q) + w * (4 * kHalf / 16 / kConvertWarps) + lane;
+#pragma unroll 4
+    for (int i = 0; i < 4 * kHalf / 16 / kConvertWarps / 32; ++i) {
+        uint4 x = p[i * 32];
+        x.x = bf16x2_to_f16x2(x.x);
+        x.y = bf16x2_to_f16x2(x.y);
+        x.z = bf16x2_to_f16x2(x.z);
+        x.w = bf16x2_to_f16x2(x.w);
+        p[i * 32] = x;
+    }
+}
+
+template <int kBits, bool kPlanned, bool kSplit>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                     const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap k16_map,
+                     const __grid_constant__ CUtensorMap v16_map, const PrefillArgs a) {
+    using Smem = QuantSmem<kBits>;
+    constexpr int kRing = CodeRing<kBits>::kSlots;
+    extern __shared__ uint8_t smem_raw[];
+    Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    volatile int *abort_flag = &sm.abort;
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int qblocks = (a.max_q_len + kUnitPos - 1) / kUnitPos;
+    const int total = a.num_seqs * kHkv * qblocks;
+
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(&sm.q_full), 1);
+        mbar_init(smem_u32(&sm.q_ready), kConvertWarps);
+        mbar_init(smem_u32(&sm.q_empty), 1);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(smem_u32(&sm.c_full[i]), 1);
+            mbar_init(smem_u32(&sm.c_empty[i]), kConvertWarps);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&sm.k_full[i]), kConvertWarps);
+            mbar_init(smem_u32(&sm.k_empty[i]), 1);
+            mbar_init(smem_u32(&sm.v_full[i]), kConvertWarps);
+            mbar_init(smem_u32(&sm.v_empty[i]), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(smem_u32(&sm.s_full[x]), 1);
+            mbar_init(smem_u32(&sm.p_half[x][0]), 4);   // the 4 warps of the tile's softmax
+            mbar_init(smem_u32(&sm.p_half[x][1]), 4);
+            mbar_init(smem_u32(&sm.o_done[x]), 1);
+        }
+        mbar_init(smem_u32(&sm.mma_idle), 1);
+        sm.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(&sm.tmem_base), kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    const auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, wait_or_abort(smem_u32(bar), parity, abort_flag, a.err));
+    };
+
+    if (warp >= kSoftmaxWarps) {
+        regs_dec();
+    if (warp == kProducerWarp) {
+        // ---------------------------------------------------------------- TMA producer
+        const bool leader = elect_one();
+        if (leader) {
+            tma_prefetch_map(&q_map);
+            tma_prefetch_map(&k_map);
+            tma_prefetch_map(&v_map);
+            tma_prefetch_map(&k16_map);
+            tma_prefetch_map(&v16_map);
+        }
+        // the cache and q may be written by the kernel just before this one on the stream
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        int units = 0, it = 0;               // units, code tiles (K and V) issued
+        bool ok = true;
+        for (int r = 0; ok; ++r) {
+            const int idx = snake<kSplit>(a, r, total);
+            if (idx < 0) break;
+            const Unit t = unit_for<kPlanned, kSplit>(a, idx, qblocks);
+            if (leader && t.error) record_error(a.err, kErrDevice | kErrQLen);
+            if (!t.run) continue;
+            const int32_t *bt = a.block_table + (size_t)t.s * a.max_blocks_per_seq;
+            for (int i = 0; i < 2 * t.n_kt; ++i, ++it) {
+                const int st = it % kRing;
+                if (it >= kRing && !(ok = wait_all(&sm.c_empty[st], ((it / kRing) - 1) & 1))) break;
+                const bool is_k = !(i & 1);
+                if (leader)
+                    load_codes<kBits>(a, t, bt, (t.kt0 + (i >> 1)) * kKT, is_k, sm.ring, st, smem_u32(&sm.c_full[st]),
+                                      is_k ? &k_map : &v_map, is_k ? &k16_map : &v16_map);
+                __syncwarp();
+                if (i == 0) {   // Q behind the first K tile, which does not wait for the unit before
+                    if (units >= 1 && !(ok = wait_all(&sm.q_empty, (units - 1) & 1))) {
+                        ++it;
+                        break;
+                    }
+                    if (leader) {
+                        const uint32_t qbar = smem_u32(&sm.q_full);
+                        mbar_arrive_expect_tx(qbar, 2 * kTileBytes);
+                        for (int x = 0; x < 2; ++x) {
+                            tma_load_3d(smem_u32(sm.q[x][0]), &q_map, qbar, 0, t.g * kGroup, t.tok0 + x * kTilePos);
+                            tma_load_3d(smem_u32(sm.q[x][1]), &q_map, qbar, 64, t.g * kGroup, t.tok0 + x * kTilePos);
+                        }
+                    }
+                    __syncwarp();
+                    ++units;
+                }
+            }
+        }
+        // Drain: no TMA copy may still be landing when the CTA exits.  In the normal path every load has
+        // been consumed and these waits return at once.
+        if (units > 0) mbar_wait(smem_u32(&sm.q_full), (units - 1) & 1);
+        for (int i = max(0, it - kRing); i < it; ++i) mbar_wait(smem_u32(&sm.c_full[i % kRing]), (i / kRing) & 1);
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------------- MMA issuer (as in prefill.cu)
+        const bool leader = elect_one();
+        if constexpr (kPlanned) asm volatile("griddepcontrol.wait;" ::: "memory");
+        const uint64_t qd0 = sdesc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
+        const uint64_t kd0 = sdesc_sw128(smem_u32(sm.k[0][0]), 16, 1024);
+        const uint64_t vd0 = sdesc_sw128(smem_u32(sm.v[0][0]), (uint32_t)kHalf, 1024);
+        int units = 0, it = 0;
+        int pend_it = -1, pend_j = 0;   // O_B += P_B V still to issue for key tile pend_it
+        bool ok = true;
+        auto issue_s = [&](int x, int ks) {
+            const uint64_t qa = qd0 + (uint64_t)(x * 2048);
+            const uint64_t kb = kd0 + (uint64_t)(ks * 2048);
+            const uint32_t sd = tmem + col_s(x);
+            if (leader) {
+                umma_ss_c<false>(sd, qa, kb, kIdescQK);
+#pragma unroll
+                for (int kk = 1; kk < kD / 16; ++kk) {
+                    const uint64_t off = (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);
+                    umma_ss_c<true>(sd, qa + off, kb + off, kIdescQK);
+                }
+                umma_commit(smem_u32(&sm.s_full[x]));
+            }
+            __syncwarp();
+        };
+        auto issue_pv = [&](int x, int pit, int pj) -> bool {
+            const int vs = pit % kStages;
+            if (x == 0 && !wait_all(&sm.v_full[vs], (pit / kStages) & 1)) return false;
+            const uint64_t vb = vd0 + (uint64_t)(vs * 2048);
+            const uint32_t pa = tmem + col_s(x);
+            if (!wait_all(&sm.p_half[x][x], pit & 1)) return false;
+            tc_fence_after();
+            if (leader) {
+                umma_ts(tmem + col_o(x), pa, vb, kIdescPV, pj > 0 ? 1u : 0u);
+#pragma unroll
+                for (int kk = 1; kk < kKT / 32; ++kk)
+                    umma_ts_c<true>(tmem + col_o(x), pa + kk * 8, vb + (uint64_t)(kk * 128), kIdescPV);
+            }
+            __syncwarp();
+            if (x == 0) {
+                if (!wait_all(&sm.p_half[x][1], pit & 1)) return false;
+                tc_fence_after();
+            }
+            if (leader) {
+#pragma unroll
+                for (int kk = kKT / 32; kk < kKT / 16; ++kk)
+                    umma_ts_c<true>(tmem + col_o(x), pa + kk * 8, vb + (uint64_t)(kk * 128), kIdescPV);
+                umma_commit(smem_u32(&sm.o_done[x]));
+                if (x == 1) umma_commit(smem_u32(&sm.v_empty[vs]));   // B is the V tile's last reader
+            }
+            __syncwarp();
+            return true;
+        };
+        for (int r = 0; ok; ++r) {
+            const int idx = snake<kSplit>(a, r, total);
+            if (idx < 0) break;
+            const Unit t = unit_for<kPlanned, kSplit>(a, idx, qblocks);
+            if (!t.run) continue;
+            if (!(ok = wait_all(&sm.q_ready, units & 1))) break;
+            for (int j = 0; j < t.n_kt; ++j, ++it) {
+                const int ks = it % kStages;
+                if (!(ok = wait_all(&sm.k_full[ks], (it / kStages) & 1))) break;
+                tc_fence_after();
+                issue_s(0, ks);                                        // S_A(j)
+                if (pend_it >= 0 && !(ok = issue_pv(1, pend_it, pend_j))) break;   // O_B, tile j-1
+                issue_s(1, ks);                                        // S_B(j)
+                if (leader) {
+                    umma_commit(smem_u32(&sm.k_empty[ks]));
+                    if (j == t.n_kt - 1) umma_commit(smem_u32(&sm.q_empty));
+                }
+                __syncwarp();
+                if (!(ok = issue_pv(0, it, j))) break;                 // O_A, tile j
+                pend_it = it;
+                pend_j = j;
+            }
+            // the unit's last O_B += P_B V now, not behind the next unit's Q and first S_A
+            if (ok && pend_it >= 0) ok = issue_pv(1, pend_it, pend_j);
+            pend_it = -1;
+            ++units;
+        }
+        // Every MMA issued must have finished before tensor memory is released.
+        if (leader) umma_commit(smem_u32(&sm.mma_idle));
+        __syncwarp();
+        mbar_wait(smem_u32(&sm.mma_idle), 0);
+    } else if (warp >= kConvertWarp) {
+        // ---------------------------------------------------------------- converters
+        if constexpr (kPlanned) asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int w = warp - kConvertWarp;
+        // V' stays below 65504: codes reach 448 (2688 with their group's scale), so the tile's largest scale
+        // may be this many powers of two above sigma
+        constexpr int kHeadroom = kBits == 8 ? 7 : 4;
+        int units = 0, it = 0, kt = 0;       // units, code tiles, key tiles
+        bool ok = true;
+        for (int r = 0; ok; ++r) {
+            const int idx = snake<kSplit>(a, r, total);
+            if (idx < 0) break;
+            const Unit t = unit_for<kPlanned, kSplit>(a, idx, qblocks);
+            if (!t.run) continue;
+            int sigma = kNone;               // exponent of sigma
+            for (int j = 0; j < t.n_kt; ++j, ++kt) {
+                const DeadRows dead(t.win, (t.kt0 + j) * kKT);
+                const int ks = kt % kStages;
+                // K(j)
+                int st = it % kRing;
+                if (!(ok = wait_all(&sm.c_full[st], (it / kRing) & 1))) break;
+                const int top = top_exponent(sm.ring, st, false, dead, lane);
+                const int v_top = top_exponent(sm.ring, st, true, dead, lane);
+                float grow = 1.f;
+                if (v_top != kNone && (sigma == kNone || v_top > sigma + kHeadroom)) {
+                    const int up = min(max(v_top, -126), 126);
+                    if (sigma != kNone) grow = exp2_int(sigma - up);
+                    sigma = up;
+                }
+                if (kt >= kStages && !(ok = wait_all(&sm.k_empty[ks], ((kt / kStages) - 1) & 1))) break;
+                const int unit = top == kNone ? 0 : min(max(top, -126), 126);
+                convert_tile<kBits>(sm.ring, st, sm.k[ks], exp2_int(-unit), dead, w, lane);
+                const float sig = exp2_int(sigma == kNone ? 0 : sigma);
+                if (w == 0 && lane == 0) sm.params[kt % kParams] = TileParams{exp2_int(unit), sig, grow};
+                fence_proxy_async_smem();    // generic writes -> visible to the MMA's reads
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sm.k_full[ks]));
+                    mbar_arrive(smem_u32(&sm.c_empty[st]));
+                }
+                ++it;
+                if (j == 0) {                // Q, which has been on its way meanwhile
+                    if (!(ok = wait_all(&sm.q_full, units & 1))) break;
+                    convert_q(sm.q[0][0], w, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.q_ready));
+                    ++units;
+                }
+                // V(j)
+                st = it % kRing;
+                if (!(ok = wait_all(&sm.c_full[st], (it / kRing) & 1))) break;
+                if (kt >= kStages && !(ok = wait_all(&sm.v_empty[ks], ((kt / kStages) - 1) & 1))) break;
+                convert_tile<kBits>(sm.ring, st, sm.v[ks], exp2_int(sigma == kNone ? 0 : -sigma), dead, w, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&sm.v_full[ks]));
+                    mbar_arrive(smem_u32(&sm.c_empty[st]));
+                }
+                ++it;
+            }
+        }
+    }
+    } else {
+        // ---------------------------------------------------------------- softmax warps
+        // Warpgroup x (= warp / 4) owns query tile x; thread = one row = one TMEM lane.
+        regs_inc();
+        if constexpr (kPlanned) asm volatile("griddepcontrol.wait;" ::: "memory");
+        const int x = warp >> 2;
+        const int row = (warp & 3) * 32 + lane;    // MMA row == TMEM lane
+        const int pl = row >> 2;                   // query position within the tile
+        const int hl = row & 3;                    // query head within the group
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t s_col = col_s(x), o_col = col_o(x);
+        int it = 0;
+        bool ok = true;
+        float split_m = -INFINITY, split_l = 0.f, split_sigma = 1.f;   // kSplit: no key seen so far
+        bool split_done = false;
+        // (a unit's lengths are looked up before the epilogue of the one before it, whose stores they would
+        // otherwise queue behind)
+        [[maybe_unused]] Unit next;
+        [[maybe_unused]] bool fetched = false;
+        next.run = false;
+        for (int r = 0; ok; ++r) {
+            const int idx = snake<kSplit>(a, r, total);
+            if (idx < 0) break;
+            const Unit t = [&]() -> Unit {
+                if constexpr (!kSplit) {
+                    const bool have = fetched;
+                    fetched = false;
+                    return have ? next : unit_for<kPlanned, kSplit>(a, idx, qblocks);
+                } else {
+                    return unit_for<kPlanned, kSplit>(a, idx, qblocks);
+                }
+            }();
+            if (!t.run) continue;
+            const int pos_first = t.pos0 + x * kTilePos;
+            const int pos = pos_first + pl;
+            float m = -INFINITY;                   // running max, log2 units (scaled)
+            float l = 0.f;                         // running sum of the f16 weights
+            float sigma = 1.f;                     // what O is in units of
+            for (int j = 0; j < t.n_kt; ++j, ++it) {
+                ok = wait_or_abort(smem_u32(&sm.s_full[x]), it & 1, abort_flag, a.err);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(lane_base + s_col + c * 32, s[c]);
+                const TileParams par = sm.params[it % kParams];
+                const float sl2 = a.scale_log2 * par.k_unit;
+                const float grow = par.grow;
+                sigma = par.sigma;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_wait_ld(s[c]);
+
+                // the tile's rows that some query of this MMA tile may not see lie past its first position, or
+                // before its last one's window and behind the sinks: a bit per column, 32 columns at a time
+                const int base = (t.kt0 + j) * kKT;
+                const int shift = t.win.shift;     // list row r beyond the sinks holds position r + shift
+                if (base + kKT - 1 > pos_first - shift ||
+                    (base + shift <= pos_first + kTilePos - 1 - a.window && base + kKT > a.sinks)) {
+                    const int hi = pos - shift - base + 1;       // columns below hi
+                    const int lo = hi - min(a.window, hi + kKT);   // columns from lo on
+                    const int sk = a.sinks - base;               // or below sk
+                    const auto below = [](int n) {               // bits 0 .. n-1
+                        return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+                    };
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const uint32_t see = below(hi - c * 32) & (~below(lo - c * 32) | below(sk - c * 32));
+                        // (a warp's 8 positions differ in few columns: most chunks are all seen)
+                        if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(see >> e & 1u)) s[c][e] = __float_as_uint(-INFINITY);
+                    }
+                }
+                float cmax[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float r0 = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+                    float r1 = fmaxf(__uint_as_float(s[c][16]), __uint_as_float(s[c][17]));
+#pragma unroll
+                    for (int e = 2; e < 16; e += 2) {
+                        r0 = fmax3(r0, __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+                        r1 = fmax3(r1, __uint_as_float(s[c][e + 16]), __uint_as_float(s[c][e + 17]));
+                    }
+                    cmax[c] = fmaxf(r0, r1);
+                }
+                const float rmax = fmaxf(fmaxf(cmax[0], cmax[1]), fmaxf(cmax[2], cmax[3]));
+                const float m_new = fmaxf(m, rmax * sl2);
+                const bool rescale = m_new > m + kRescaleThreshold;   // also when m == -inf
+                const float m_use = rescale ? m_new : m;
+                const float alpha = rescale ? fast_exp2(m - m_new) : 1.f;
+                // a row with every key so far masked keeps m = -inf; its weights are 0
+                const float m_sub = m_use == -INFINITY ? 0.f : m_use;
+                if (j > 0 && __any_sync(0xffffffffu, rescale || grow != 1.f)) {
+                    // O must hold O += P V of the previous tile before it is rescaled (that product was
+                    // issued before this tile's S, so it has completed).
+                    ok = wait_or_abort(smem_u32(&sm.o_done[x]), (it - 1) & 1, abort_flag, a.err);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    tc_fence_after();
+                    const float f = alpha * grow;
+                    // 8 columns at a time: the scores of this tile are still live in registers
+#pragma unroll 1
+                    for (int c = 0; c < 16; ++c) {
+                        uint32_t o[8];
+                        tmem_ld8(lane_base + o_col + c * 8, o);
+                        tmem_wait_ld8(o);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_st8(lane_base + o_col + c * 8, o);
+                    }
+                }
+                float part[4] = {0.f, 0.f, 0.f, 0.f};   // 4 partial row sums
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int c = 2 * h; c < 2 * h + 2; ++c) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            float x0, x1;
+                            ffma2(x0, x1, __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]), sl2, sl2,
+                                  -m_sub, -m_sub);
+                            // weights are at most 2^8 (the lazy maximum), those under 2^-14 lose bits one by one
+                            const uint32_t pp = pack_f16x2(fast_exp2(x0), fast_exp2(x1));
+                            // the row sum uses the same f16-rounded weights the PV product uses
+                            const int k = (e >> 1) & 1;
+                            part[2 * k] = add_f16_lo(pp, part[2 * k]);
+                            part[2 * k + 1] = add_f16_hi(pp, part[2 * k + 1]);
+                            pk[e / 2] = pp;
+                        }
+                        // P columns 16c..16c+15 go over S columns already read into registers
+                        tmem_st16(lane_base + s_col + 16 * c, pk);
+                    }
+                    // P of keys 64h..64h+63 is in tensor memory: release that half of O += P V
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.p_half[x][h]));
+                }
+                const float rsum = (part[0] + part[1]) + (part[2] + part[3]);
+                l = l * alpha + rsum;
+                m = m_use;
+            }
+            if (!ok) break;
+
+            // ------------------------------------------------------------ epilogue
+            if constexpr (!kSplit) {
+                const int idx_next = snake<kSplit>(a, r + 1, total);
+                if (idx_next >= 0) {
+                    next = unit_for<kPlanned, kSplit>(a, idx_next, qblocks);
+                    fetched = true;
+                }
+            }
+            ok = wait_or_abort(smem_u32(&sm.o_done[x]), (it - 1) & 1, abort_flag, a.err);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            tc_fence_after();
+            if constexpr (kSplit) {
+                split_m = m;
+                split_l = l;
+                split_sigma = sigma;
+                split_done = true;
+                continue;
+            }
+            const float inv_l = sigma / l;
+            const bool row_ok = x * kTilePos + pl < t.positions;
+            const size_t orow = (size_t)(t.tok0 + x * kTilePos + pl) * kHq + t.g * kGroup + hl;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tmem_ld32(lane_base + o_col + c * 32, o);
+                tmem_wait_ld(o);
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2)
+                    w[e / 2] = pack_bf16x2(__uint_as_float(o[e]) * inv_l, __uint_as_float(o[e + 1]) * inv_l);
+                // 32-byte stores: each writes whole sectors (out is 32-byte aligned, rows are 256 bytes)
+                if (row_ok) {
+                    __nv_bfloat16 *d = static_cast<__nv_bfloat16 *>(a.out) + orow * kD + c * 32;
+                    st_global_32b(d, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+                    st_global_32b(d + 16, w[8], w[9], w[10], w[11], w[12], w[13], w[14], w[15]);
+                }
+            }
+            if (row_ok && a.lse) a.lse[orow] = (m + __log2f(l)) * kLn2;
+            tc_fence_before();
+        }
+        if constexpr (kSplit) {
+            // Once both tiles' products are done, their reads of Q and K are too, and this CTA's O goes
+            // over them, row by row, the 16-byte pieces of a row permuted by its low bits so that neither
+            // these stores nor the merge's loads meet on a bank.  (All softmax warps come to this barrier,
+            // also those that gave up.)
+            named_barrier(1, kSoftmaxWarps * 32);
+            const int rr = x * kRows + row;
+            if (split_done) {
+                uint8_t *dst = sm.q[0][0] + rr * (kD * 4);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(lane_base + o_col + c * 32, o);
+                    tmem_wait_ld(o);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * split_sigma);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        *reinterpret_cast<uint4 *>(dst + (((c * 8 + v) ^ (rr & 7)) << 4)) =
+                            make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+                }
+                tc_fence_before();
+            }
+            sm.ml[rr][0] = split_m;
+            sm.ml[rr][1] = split_l;
+        }
+    }
+
+    if constexpr (kSplit) {
+        // every CTA's part is in its shared memory, merged by all, and stays until all have read it
+        // (after an abort too: every wait above is bounded, so every CTA comes here)
+        __syncwarp();
+        cluster_sync_all();
+        if (warp < kSoftmaxWarps) {
+            const Unit t = unit_at<false, true>(a, (int)(blockIdx.x / a.unit_ctas), qblocks);
+            if (t.run) merge_rows(a, t, smem_u32(sm.q), smem_u32(sm.ml), warp, lane);
+        }
+        __syncwarp();
+        cluster_sync_all();
+    }
+
+    // ---------------------------------------------------------------- teardown
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int kBits, bool kPlanned, bool kSplit>
+cudaError_t launch_mode(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
+                        const CUtensorMap &v_map, const CUtensorMap &k16_map, const CUtensorMap &v16_map, int num_sms,
+                        cudaStream_t stream) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const auto kernel = prefill_quant_kernel<kBits, kPlanned, kSplit>;
+    static std::atomic<bool> configured[64] = {};
+    if (dev < 0 || dev >= 64 || !configured[dev].load()) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<kBits>);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev].store(true);
+    }
+    const long long qblocks = (a.max_q_len + kUnitPos - 1) / kUnitPos;
+    const long long units = (long long)a.num_seqs * kHkv * qblocks;
+    // Programmatic dependent launch: the producer waits (griddepcontrol.wait) before its first load, so the
+    // launch and prologue may overlap the previous kernel on the stream.
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;   // kSplit only
+    attr[1].val.clusterDim.x = kSplit ? (unsigned)a.unit_ctas : 1u;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = kSplit ? 2 : 1;
+    if constexpr (kPlanned) {
+        cfg.gridDim = dim3(1);
+        cfg.blockDim = dim3(kPlanThreads);
+        cfg.dynamicSmemBytes = 0;
+        e = cudaLaunchKernelEx(&cfg, prefill_plan_kernel<false, true>, a, (int)qblocks, (int)units, plan_keys(a));
+        if (e != cudaSuccess) return e;
+    }
+    cfg.gridDim = dim3(kSplit ? (unsigned)(units * a.unit_ctas) : (unsigned)std::min<long long>(units, num_sms));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes<kBits>;
+    return cudaLaunchKernelEx(&cfg, kernel, q_map, k_map, v_map, k16_map, v16_map, a);
+}
+
+// How many clusters of c CTAs of the split kernel fit on the current device at once, c = 2 .. 8
+// (looked up once per device; a lookup that failed counts as none and is made again next time).
+template <int kBits>
+cudaError_t split_clusters(int (&out)[9]) {
+    static std::atomic<int> known[64][9];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const auto kernel = prefill_quant_kernel<kBits, false, true>;
+    for (int c = 2; c <= 8; ++c) {
+        int n = known[dev][c].load();
+        if (n == 0) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<kBits>);
+            if (e != cudaSuccess) return e;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = (unsigned)c;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)c);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = kSmemBytes<kBits>;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                out[c] = 0;
+                continue;
+            }
+            n = n > 0 ? n : -1;
+            known[dev][c].store(n);
+        }
+        out[c] = n;
+    }
+    return cudaSuccess;
+}
+
+template <int kBits>
+cudaError_t launch_bits(PrefillArgs a, long long tiles, const CUtensorMap &q_map, const CUtensorMap &k_map,
+                        const CUtensorMap &v_map, const CUtensorMap &k16_map, const CUtensorMap &v16_map, int num_sms,
+                        cudaStream_t stream) {
+    const long long units = (long long)a.num_seqs * kHkv * ((a.max_q_len + kUnitPos - 1) / kUnitPos);
+    a.unit_ctas = 1;
+    if (units * 2 <= num_sms) {
+        int clusters[9] = {};
+        const cudaError_t e = split_clusters<kBits>(clusters);
+        if (e != cudaSuccess) return e;
+        a.unit_ctas = unit_ctas_for(units, tiles, std::min(a.max_q_len, kUnitPos), num_sms, clusters);
+    }
+    if (a.unit_ctas > 1) {
+        const cudaError_t e =
+            launch_mode<kBits, false, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
+        if (e != cudaErrorLaunchOutOfResources && e != cudaErrorInvalidClusterSize && e != cudaErrorNotSupported &&
+            e != cudaErrorCooperativeLaunchTooLarge)
+            return e;
+        cudaGetLastError();   // the clusters were refused: one CTA a unit instead
+        a.unit_ctas = 1;
+    }
+    if (a.order && units > num_sms)   // (units that all start at once need no order)
+        return launch_mode<kBits, true, false>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
+    return launch_mode<kBits, false, false>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill_quant(PrefillArgs a, long long tiles, const CUtensorMap &q_map, const CUtensorMap &k_map,
+                                 const CUtensorMap &v_map, const CUtensorMap &k16_map, const CUtensorMap &v16_map,
+                                 int num_sms, cudaStream_t stream) {
+    if (a.num_seqs == 0 || a.max_q_len == 0 || a.total_tokens == 0) return cudaSuccess;
+    return a.k_exp ? launch_bits<4>(a, tiles, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream)
+                   : launch_bits<8>(a, tiles, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
+}
+
+}  // namespace pa

@@ -1,6 +1,6 @@
 // rope_append.cu -- the new tokens' q, k and v on their way into attention: per-head norm and
-// rotary position embedding of q and k, k and v into their cache slots (bf16 or 8 bits), in
-// one pass.
+// rotary position embedding of q and k, k and v into their cache slots (bf16, 8 or 4
+// bits), in one pass.
 //
 // Page "扔掉 vLLM！从零构建 Qwen3-8B 推理引擎，C++/CUDA 实现性能追平 98%" §4.3.1 appends a new
 // token's K and V to its cache block; the pages name no position encoding or norm.  Those are
@@ -32,6 +32,7 @@
 // meanwhile and 16 warps an SM at 124 registers to cover it; that is where this form stands, not
 // shown to be a limit (the one form tried with more warps spilled its prefetched rows).
 #include "common.cuh"
+#include "fp4.cuh"
 #include "launch.h"
 #include "tokens.cuh"
 
@@ -105,6 +106,37 @@ __device__ __forceinline__ void store_row8(uint8_t *codes, float *scale_slot, in
     if (j == 0) *scale_slot = scale;
 }
 
+// The same into the 4-bit cache: this lane's two runs of 8 values are halves of groups j / 2 and 4 + j / 2,
+// whose other halves its neighbour holds.
+__device__ __forceinline__ void store_row4(uint8_t *codes, uint8_t *scales, uint8_t *exp_slot, int j, float (&lo)[8],
+                                           float (&hi)[8]) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) amax = max(amax, max(__float_as_uint(fabsf(lo[e])), __float_as_uint(fabsf(hi[e]))));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) amax = umax_xor(amax, o);
+    const uint32_t exp = fp4_row_exp(amax);
+    const float unit = fp4_unit_inverse(exp);
+    float top_lo = 0.f, top_hi = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        lo[e] *= unit;
+        hi[e] *= unit;
+        top_lo = fmaxf(top_lo, fabsf(lo[e]));
+        top_hi = fmaxf(top_hi, fabsf(hi[e]));
+    }
+    top_lo = fmaxf(top_lo, __shfl_xor_sync(0xffffffffu, top_lo, 1));
+    top_hi = fmaxf(top_hi, __shfl_xor_sync(0xffffffffu, top_hi, 1));
+    const uint32_t s_lo = fp4_group_scale(top_lo), s_hi = fp4_group_scale(top_hi);
+    *reinterpret_cast<uint32_t *>(codes + 4 * j) = fp4_codes(lo, s_lo);
+    *reinterpret_cast<uint32_t *>(codes + kFp4RowCodes / 2 + 4 * j) = fp4_codes(hi, s_hi);
+    if (!(j & 1)) {
+        scales[j >> 1] = (uint8_t)s_lo;
+        scales[kFp4Groups / 2 + (j >> 1)] = (uint8_t)s_hi;
+    }
+    if (j == 0) *exp_slot = (uint8_t)exp;
+}
+
 // Where token t of the batch goes.
 struct Place {
     bool live;        // a sequence's token (false: behind the last sequence, left alone)
@@ -149,7 +181,8 @@ __device__ __forceinline__ Place place_of(const RopeAppendArgs &a, int t, int la
     return pl;
 }
 
-template <bool kFp8, bool kNorm>
+// kBits: the cache's, 16, 8 or 4
+template <int kBits, bool kNorm>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
 rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
     // The next kernel on the stream may start its prologue; it waits for this one to complete
@@ -248,13 +281,26 @@ rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
             __nv_bfloat16 *dst =
                 is_q ? static_cast<__nv_bfloat16 *>(a.q_out) + ((size_t)tok * kHq + g * 8) * kD
                      : static_cast<__nv_bfloat16 *>(is_v ? a.v_pool : a.k_pool) + pl.row * (kHkv * kD);
-            uint8_t *codes = nullptr;
+            uint8_t *codes = nullptr, *scales4 = nullptr, *exps = nullptr;
             float *scales = nullptr;
-            if (kFp8 && !is_q) {
+            if (kBits == 8 && !is_q) {
                 codes = static_cast<uint8_t *>(is_v ? a.v_pool : a.k_pool) + pl.row * (kHkv * kD);
                 scales = (is_v ? a.v_scale : a.k_scale) +
                          ((pl.row / kBlock) * kHkv * kBlock + pl.row % kBlock);   // + head * 256
             }
+            if (kBits == 4 && !is_q) {
+                const long long row0 = (pl.row / kBlock) * kHkv * kBlock + pl.row % kBlock;
+                codes = static_cast<uint8_t *>(is_v ? a.v_pool : a.k_pool) + pl.row * (kHkv * kFp4RowCodes);
+                scales4 = (is_v ? a.v_scale4 : a.k_scale4) + row0 * kFp4Groups;   // + head * 256 * 8
+                exps = (is_v ? a.v_exp : a.k_exp) + row0;                         // + head * 256
+            }
+            const auto store_low = [&](int h, float (&lo)[8], float (&hi)[8]) {
+                if constexpr (kBits == 8)
+                    store_row8(codes + h * kD, scales + h * kBlock, j, lo, hi);
+                else
+                    store_row4(codes + h * kFp4RowCodes, scales4 + h * (kBlock * kFp4Groups), exps + h * kBlock, j, lo,
+                               hi);
+            };
             uint4 gain_lo = {}, gain_hi = {};
             if (kNorm && !is_v) {
                 const uint4 *gw = static_cast<const uint4 *>(is_q ? a.q_norm : a.k_norm) + j;
@@ -264,7 +310,7 @@ rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int h = 4 * u + hs;
-                if (!kFp8 && is_v) {      // v: the row as it is
+                if (kBits == 16 && is_v) {      // v: the row as it is
                     uint4 *d = reinterpret_cast<uint4 *>(dst + h * kD) + j;
                     d[0] = w_lo[u];
                     d[kD / 16] = w_hi[u];
@@ -273,8 +319,8 @@ rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
                 float lo[8], hi[8];
                 unpack8(w_lo[u], lo);
                 unpack8(w_hi[u], hi);
-                if (kFp8 && is_v) {
-                    store_row8(codes + h * kD, scales + h * kBlock, j, lo, hi);
+                if (kBits != 16 && is_v) {
+                    store_low(h, lo, hi);
                     continue;
                 }
                 if constexpr (kNorm) {
@@ -316,8 +362,8 @@ rope_append_kernel(const __grid_constant__ RopeAppendArgs a) {
                         zh[e] = hi[e];
                     }
                 }
-                if (kFp8 && !is_q) {
-                    store_row8(codes + h * kD, scales + h * kBlock, j, zl, zh);
+                if (kBits != 16 && !is_q) {
+                    store_low(h, zl, zh);
                 } else {
                     uint4 *d = reinterpret_cast<uint4 *>(dst + h * kD) + j;
                     d[0] = pack8(zl);
@@ -343,11 +389,14 @@ cudaError_t launch_rope_append(const RopeAppendArgs &a, int num_sms, cudaStream_
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (a.k_exp)
+        return a.q_norm ? cudaLaunchKernelEx(&cfg, rope_append_kernel<4, true>, a)
+                        : cudaLaunchKernelEx(&cfg, rope_append_kernel<4, false>, a);
     if (a.k_scale)
-        return a.q_norm ? cudaLaunchKernelEx(&cfg, rope_append_kernel<true, true>, a)
-                        : cudaLaunchKernelEx(&cfg, rope_append_kernel<true, false>, a);
-    return a.q_norm ? cudaLaunchKernelEx(&cfg, rope_append_kernel<false, true>, a)
-                    : cudaLaunchKernelEx(&cfg, rope_append_kernel<false, false>, a);
+        return a.q_norm ? cudaLaunchKernelEx(&cfg, rope_append_kernel<8, true>, a)
+                        : cudaLaunchKernelEx(&cfg, rope_append_kernel<8, false>, a);
+    return a.q_norm ? cudaLaunchKernelEx(&cfg, rope_append_kernel<16, true>, a)
+                    : cudaLaunchKernelEx(&cfg, rope_append_kernel<16, false>, a);
 }
 
 }  // namespace pa

@@ -102,6 +102,22 @@ def load() -> ctypes.CDLL:
     lib.paged_attn_prefill_window.argtypes = [pa_shape, vp, vp, vp, vp, vp, vp, i32, i32, vp, vp, i32, i32, i32, i32,
                                               i32, f32, vp, sz, vp]
     lib.paged_attn_prefill_window.restype = ctypes.c_int
+    lib.kv_append_fp4.argtypes = [pa_shape] + [vp] * 9 + [i32, i32, vp, vp, i32, i32, vp, sz, vp]
+    lib.kv_append_fp4.restype = ctypes.c_int
+    lib.paged_rope_append_fp4.argtypes = rope + [vp] * 7 + [i32, i32, vp, vp, i32, i32, vp, sz, vp]
+    lib.paged_rope_append_fp4.restype = ctypes.c_int
+    lib.paged_kv_read_fp8.argtypes = [pa_shape] + [vp] * 7 + [i32, i32, vp, vp, i32, i32, vp, sz, vp]
+    lib.paged_kv_read_fp8.restype = ctypes.c_int
+    lib.paged_kv_read_fp4.argtypes = [pa_shape] + [vp] * 9 + [i32, i32, vp, vp, i32, i32, vp, sz, vp]
+    lib.paged_kv_read_fp4.restype = ctypes.c_int
+    lib.paged_attn_decode_fp4.argtypes = [pa_shape] + [vp] * 10 + [i32, i32, vp, i32, i32, i32, f32, i32, vp, sz, vp]
+    lib.paged_attn_decode_fp4.restype = ctypes.c_int
+    lib.paged_attn_prefill_fp8.argtypes = [pa_shape] + [vp] * 8 + [i32, i32, vp, vp, i32, i32, i32, i32, i32, f32, vp,
+                                                                  sz, vp]
+    lib.paged_attn_prefill_fp8.restype = ctypes.c_int
+    lib.paged_attn_prefill_fp4.argtypes = [pa_shape] + [vp] * 10 + [i32, i32, vp, vp, i32, i32, i32, i32, i32, f32, vp,
+                                                                   sz, vp]
+    lib.paged_attn_prefill_fp4.restype = ctypes.c_int
     lib.paged_attn_decode_append.argtypes = [pa_shape, vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp,
                                              i32, f32, vp, sz, vp]
     lib.paged_attn_decode_append.restype = ctypes.c_int
@@ -896,6 +912,178 @@ def paged_attn_prefill_window(q, k_pool, v_pool, block_table, cu_q_lens, seq_len
                    cu_q_lens.data_ptr(), seq_lens.data_ptr(), num_seqs, q.shape[0], max_q_len, window, sinks, scale,
                    workspace.data_ptr(), workspace.numel()))
     return out
+
+
+# ------------------------------------------------------------------ low-bit caches
+
+FULL_WINDOW = 2 ** 31 - 1       # a window that every context fits into
+FP4_GROUP = 16                  # values under one scale of the 4-bit cache
+
+
+def fp4_cache(num_blocks: int, device=None):
+    """An empty 4-bit KV cache: (k_codes, v_codes) uint8 [N, 256, 8, 64], (k_scale, v_scale) uint8
+    [N, 8, 256, 8] (E4M3) and (k_exp, v_exp) uint8 [N, 8, 256] holding 255, so a slot that was never
+    written shows up as NaN wherever it is read."""
+    dev = device or "cuda"
+    codes = torch.zeros(num_blocks, BLOCK_SIZE, NUM_KV_HEADS, HEAD_DIM // 2, dtype=torch.uint8, device=dev)
+    scales = torch.zeros(num_blocks, NUM_KV_HEADS, BLOCK_SIZE, HEAD_DIM // FP4_GROUP, dtype=torch.uint8, device=dev)
+    exps = torch.full((num_blocks, NUM_KV_HEADS, BLOCK_SIZE), 255, dtype=torch.uint8, device=dev)
+    return codes, codes.clone(), scales, scales.clone(), exps, exps.clone()
+
+
+def _need_fp4_cache(cache, dev):
+    k_codes, v_codes, k_scale, v_scale, k_exp, v_exp = cache
+    _need(k_codes, "k_codes", torch.uint8, (None, BLOCK_SIZE, NUM_KV_HEADS, HEAD_DIM // 2), dev)
+    n = k_codes.shape[0]
+    _need(v_codes, "v_codes", torch.uint8, (n, BLOCK_SIZE, NUM_KV_HEADS, HEAD_DIM // 2), dev)
+    scales, exps = (n, NUM_KV_HEADS, BLOCK_SIZE, HEAD_DIM // FP4_GROUP), (n, NUM_KV_HEADS, BLOCK_SIZE)
+    _need(k_scale, "k_scale", torch.uint8, scales, dev)
+    _need(v_scale, "v_scale", torch.uint8, scales, dev)
+    _need(k_exp, "k_exp", torch.uint8, exps, dev)
+    _need(v_exp, "v_exp", torch.uint8, exps, dev)
+
+
+def kv_append_fp4(k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, k_new, v_new, block_table, cu_q_lens, seq_lens,
+                  workspace, stream=None) -> None:
+    """Quantise the new tokens' K/V rows into the 4-bit cache (fp4_cache, in place)."""
+    cache = (k_codes, v_codes, k_scale, v_scale, k_exp, v_exp)
+    _need(k_new, "k_new", torch.bfloat16, (None, NUM_KV_HEADS, HEAD_DIM))
+    dev = k_new.device
+    _need_fp4_cache(cache, dev)
+    _need(v_new, "v_new", torch.bfloat16, k_new.shape, dev)
+    num_seqs, width = _need_table(block_table, dev)
+    _need(cu_q_lens, "cu_q_lens", torch.int32, (num_seqs + 1,), dev)
+    _need(seq_lens, "seq_lens", torch.int32, (num_seqs,), dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    _check("kv_append_fp4", _launch(load().kv_append_fp4, dev, stream, SHAPE, *[t.data_ptr() for t in cache],
+                                    k_new.data_ptr(), v_new.data_ptr(), block_table.data_ptr(), width,
+                                    k_codes.shape[0], cu_q_lens.data_ptr(), seq_lens.data_ptr(), num_seqs,
+                                    k_new.shape[0], workspace.data_ptr(), workspace.numel()))
+
+
+def paged_rope_append_fp4(q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, block_table, cu_q_lens,
+                          seq_lens, workspace, *, rope_theta: float, positions=None, pair_axis=None,
+                          q_norm_weight=None, k_norm_weight=None, norm_eps: float = QWEN3_NORM_EPS, q_out=None,
+                          stream=None) -> torch.Tensor:
+    """paged_rope_append into the 4-bit cache (fp4_cache): k rows quantised from their rotated fp32 values,
+    v rows as kv_append_fp4 does."""
+    cache = (k_codes, v_codes, k_scale, v_scale, k_exp, v_exp)
+    pair_axis = _pair_axes(pair_axis)
+    _need(k_codes, "k_codes", torch.uint8)
+    _need_fp4_cache(cache, k_codes.device)
+    return _rope_append("paged_rope_append_fp4", load().paged_rope_append_fp4, q, k_new, v_new, cache, block_table,
+                        cu_q_lens, seq_lens, workspace, rope_theta, positions, pair_axis, q_norm_weight, k_norm_weight,
+                        norm_eps, q_out, stream)
+
+
+def _kv_read(name, fn, cache, block_table, cu_rows, first, total_rows, workspace, k_out, v_out, stream):
+    """paged_kv_read_* of a cache whose tensors have been checked."""
+    dev = cache[0].device
+    num_seqs, width = _need_table(block_table, dev)
+    _need(cu_rows, "cu_rows", torch.int32, (num_seqs + 1,), dev)
+    _need(first, "first", torch.int32, (num_seqs,), dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    _int32(total_rows=total_rows)
+    if total_rows < 0:
+        raise ValueError(f"total_rows must not be negative, got {total_rows}")
+    shape = (total_rows, NUM_KV_HEADS, HEAD_DIM)
+    outs = []
+    for out, what in ((k_out, "k_out"), (v_out, "v_out")):
+        if out is None:
+            out = _empty(shape, dev, stream)
+        else:
+            _need(out, what, torch.bfloat16, shape, dev)
+        outs.append(out)
+    _check(name, _launch(fn, dev, stream, SHAPE, outs[0].data_ptr(), outs[1].data_ptr(), *[t.data_ptr() for t in cache],
+                         block_table.data_ptr(), width, cache[0].shape[0], cu_rows.data_ptr(), first.data_ptr(),
+                         num_seqs, total_rows, workspace.data_ptr(), workspace.numel()))
+    return outs[0], outs[1]
+
+
+def paged_kv_read_fp8(k_codes, v_codes, k_scale, v_scale, block_table, cu_rows, first, total_rows: int, workspace, *,
+                      k_out=None, v_out=None, stream=None):
+    """Rows of the 8-bit cache read back as bf16: (k, v), [total_rows, 8, 128] each.  Rows cu_rows[s] ..
+    cu_rows[s + 1] - 1 (int32 [S + 1]) are the tokens of sequence s from position first[s] (int32 [S]) on;
+    rows behind the last sequence are left as they are."""
+    _need(k_codes, "k_codes", torch.uint8)
+    _need_fp8_cache(k_codes, v_codes, k_scale, v_scale, k_codes.device)
+    return _kv_read("paged_kv_read_fp8", load().paged_kv_read_fp8, (k_codes, v_codes, k_scale, v_scale), block_table,
+                    cu_rows, first, total_rows, workspace, k_out, v_out, stream)
+
+
+def paged_kv_read_fp4(k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, block_table, cu_rows, first, total_rows: int,
+                      workspace, *, k_out=None, v_out=None, stream=None):
+    """paged_kv_read_fp8 of the 4-bit cache."""
+    cache = (k_codes, v_codes, k_scale, v_scale, k_exp, v_exp)
+    _need(k_codes, "k_codes", torch.uint8)
+    _need_fp4_cache(cache, k_codes.device)
+    return _kv_read("paged_kv_read_fp4", load().paged_kv_read_fp4, cache, block_table, cu_rows, first, total_rows,
+                    workspace, k_out, v_out, stream)
+
+
+def paged_attn_decode_fp4(q, k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, block_table, seq_lens, workspace, *,
+                          window: int = FULL_WINDOW, sinks: int = 0, scale: float = DEFAULT_SCALE, out=None, lse=None,
+                          split_tokens: int = 0, stream=None) -> torch.Tensor:
+    """One query token per sequence over the 4-bit cache: the whole context, or its first `sinks` and last
+    `window` tokens; q [B, 32, 128] -> out [B, 32, 128] (bf16).  A row with seq_lens 0 gives zeros.
+    split_tokens: visible tokens per CTA (a multiple of 256), 0 = the library's choice."""
+    cache = (k_codes, v_codes, k_scale, v_scale, k_exp, v_exp)
+    _need(k_codes, "k_codes", torch.uint8)
+    dev = k_codes.device
+    _need_fp4_cache(cache, dev)
+    _int32(window=window, sinks=sinks, split_tokens=split_tokens)
+    out = _need_decode(q, block_table, seq_lens, workspace, out, lse, dev, stream)
+    _check("paged_attn_decode_fp4",
+           _launch(load().paged_attn_decode_fp4, dev, stream, SHAPE, out.data_ptr(), _ptr(lse), q.data_ptr(),
+                   *[t.data_ptr() for t in cache], block_table.data_ptr(), block_table.shape[1], k_codes.shape[0],
+                   seq_lens.data_ptr(), q.shape[0], window, sinks, scale, split_tokens, workspace.data_ptr(),
+                   workspace.numel()))
+    return out
+
+
+def _prefill_low(name, fn, q, cache, block_table, cu_q_lens, seq_lens, max_q_len, workspace, window, sinks, scale, out,
+                 lse, stream):
+    """paged_attn_prefill_* over a low-bit cache whose tensors have been checked."""
+    _int32(max_q_len=max_q_len, window=window, sinks=sinks)
+    dev = cache[0].device
+    _need(q, "q", torch.bfloat16, (None, NUM_Q_HEADS, HEAD_DIM), dev)
+    num_seqs, width = _need_table(block_table, dev)
+    _need(cu_q_lens, "cu_q_lens", torch.int32, (num_seqs + 1,), dev)
+    _need(seq_lens, "seq_lens", torch.int32, (num_seqs,), dev)
+    _need(workspace, "workspace", torch.uint8, None, dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (q.shape[0], NUM_Q_HEADS), dev)
+    if out is None:
+        out = _empty(q.shape, dev, stream)
+    else:
+        _need(out, "out", torch.bfloat16, q.shape, dev)
+    _check(name, _launch(fn, dev, stream, SHAPE, out.data_ptr(), _ptr(lse), q.data_ptr(),
+                         *[t.data_ptr() for t in cache], block_table.data_ptr(), width, cache[0].shape[0],
+                         cu_q_lens.data_ptr(), seq_lens.data_ptr(), num_seqs, q.shape[0], max_q_len, window, sinks,
+                         scale, workspace.data_ptr(), workspace.numel()))
+    return out
+
+
+def paged_attn_prefill_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, cu_q_lens, seq_lens, max_q_len: int,
+                           workspace, *, window: int = FULL_WINDOW, sinks: int = 0, scale: float = DEFAULT_SCALE,
+                           out=None, lse=None, stream=None) -> torch.Tensor:
+    """Causal attention of each sequence's new tokens (q [T, 32, 128], appended before) over its context in the
+    8-bit cache, all of it or the first `sinks` tokens and the last `window` up to each new one."""
+    _need(k_codes, "k_codes", torch.uint8)
+    _need_fp8_cache(k_codes, v_codes, k_scale, v_scale, k_codes.device)
+    return _prefill_low("paged_attn_prefill_fp8", load().paged_attn_prefill_fp8, q, (k_codes, v_codes, k_scale, v_scale),
+                        block_table, cu_q_lens, seq_lens, max_q_len, workspace, window, sinks, scale, out, lse, stream)
+
+
+def paged_attn_prefill_fp4(q, k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, block_table, cu_q_lens, seq_lens,
+                           max_q_len: int, workspace, *, window: int = FULL_WINDOW, sinks: int = 0,
+                           scale: float = DEFAULT_SCALE, out=None, lse=None, stream=None) -> torch.Tensor:
+    """paged_attn_prefill_fp8 over the 4-bit cache."""
+    cache = (k_codes, v_codes, k_scale, v_scale, k_exp, v_exp)
+    _need(k_codes, "k_codes", torch.uint8)
+    _need_fp4_cache(cache, k_codes.device)
+    return _prefill_low("paged_attn_prefill_fp4", load().paged_attn_prefill_fp4, q, cache, block_table, cu_q_lens,
+                        seq_lens, max_q_len, workspace, window, sinks, scale, out, lse, stream)
 
 
 def decode_step_host_staging(max_batch: int, max_blocks_per_seq: int, device=None) -> torch.Tensor:

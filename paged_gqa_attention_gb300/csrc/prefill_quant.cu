@@ -23,10 +23,10 @@
 // an operand tile next to the products' reads.
 //
 // CTA = 16 warps, persistent, one per SM:
-//   warps 0-3, 4-7  softmax + epilogue of query tiles A and B (thread = row = TMEM lane), 184 registers
-//   warp 8          TMA producer: Q, and the ring of code tiles in the order K(0) V(0) K(1) V(1) ...
-//   warp 9          TMEM allocator and tcgen05.mma issuer
-//   warps 12-15     converters (warps 8-15: 72 registers)
+//   warps 0-3, 4-7  softmax + epilogue of query tiles A and B (thread = row = TMEM lane)
+//   warps 8-11      converters
+//   warp 12         TMA producer: Q, and the ring of code tiles in the order K(0) V(0) K(1) V(1) ...
+//   warp 13         TMEM allocator and tcgen05.mma issuer
 // Every wait is bounded; on expiry the CTA records PA_ERR_TIMEOUT, unwinds, waits (bounded) for its own
 // copies and MMAs, frees tensor memory and exits.
 #include <atomic>
@@ -44,13 +44,14 @@
 namespace pa {
 namespace {
 
-constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
-constexpr int kConvertWarp = 12;              // 12-15
+constexpr int kConvertWarp = 8;               // 8-11
 constexpr int kConvertWarps = 4;
+constexpr int kProducerWarp = 12;
+constexpr int kMmaWarp = 13;                  // (14 and 15 complete the warpgroup that gives up its registers)
 constexpr int kThreads = 16 * 32;
-// registers a thread: 2 x 128 x 184 + 2 x 128 x 72 = 512 x 128, what the block is launched with
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+// registers a thread, warpgroup by warpgroup: together the 512 x 128 that the block is launched with
+constexpr int kSoftmaxRegs = 176, kConvertRegs = 80, kControlRegs = 80;
+static_assert(2 * kSoftmaxRegs + kConvertRegs + kControlRegs == 4 * 128, "register split");
 constexpr uint32_t kTileBytes = 2 * kHalf;    // a 128 x 128 f16 tile
 constexpr int kStages = 2;                    // f16 tiles of K and of V
 constexpr int kParams = 4;                    // see TileParams
@@ -120,18 +121,15 @@ constexpr size_t kSmemBytes = sizeof(QuantSmem<kBits>) + 1024;
 static_assert(kSmemBytes<8> <= 232448 && kSmemBytes<4> <= 232448, "shared memory");
 
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs)); }
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs)); }
+template <int kRegs>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
-// c + the f16 in the low / high half of v
-__device__ __forceinline__ float add_f16_lo(uint32_t v, float c) {
-    float d;
-    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n add.rn.f32.f16 %0, lo, %2;\n}" : "=f"(d) : "r"(v), "f"(c));
-    return d;
-}
-__device__ __forceinline__ float add_f16_hi(uint32_t v, float c) {
-    float d;
-    asm("{\n .reg .b16 lo, hi;\n mov.b32 {lo, hi}, %1;\n add.rn.f32.f16 %0, hi, %2;\n}" : "=f"(d) : "r"(v), "f"(c));
-    return d;
+// Two fp32 sums in one packed instruction: (d0, d1) += (a0, a1)
+__device__ __forceinline__ void fadd2(float &d0, float &d1, float a0, float a1) {
+    asm("{\n .reg .b64 ra, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rd, {%0, %1};\n add.rn.f32x2 rd, rd, ra;\n"
+        " mov.b64 {%0, %1}, rd;\n}"
+        : "+f"(d0), "+f"(d1)
+        : "f"(a0), "f"(a1));
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -142,6 +140,20 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
     uint32_t d;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
+}
+
+__device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint2 ld_shared_8(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 // The work unit dealt as the r-th of this CTA.
@@ -202,100 +214,170 @@ __device__ __forceinline__ void load_codes(const PrefillArgs &a, const Unit &t, 
 
 // ---------------------------------------------------------------- conversion (one warp's share)
 
-// Largest scale of the tile's live rows, as exponent: the least n with scale < 2^n (8 bits; scales that are
-// zero, infinite or NaN leave it out), or the largest exponent byte - 127 (4 bits).  kNone: no such row.
-constexpr int kNone = -1000;
+// What a lane converts at a time: 2 x 16 codes of one row, dims 16c .. 16c + 15 and 64 + 16c .., with what scales
+// them; then their f16 values code * scale * unit, `unit` a power of two.
+template <int kBits>
+struct Piece;
+template <>
+struct Piece<8> {
+    uint4 c[2];
+    float s;
 
-__device__ __forceinline__ int top_exponent(const CodeRing<8> &s, int st, bool of_v, const DeadRows &dead, int lane) {
-    const float4 x = *reinterpret_cast<const float4 *>((of_v ? s.v_scale[0] : s.scale[st]) + 4 * lane);
-    const float v[4] = {x.x, x.y, x.z, x.w};
-    int top = 0;   // biased exponent + 1 of the largest
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = 4 * lane + i;
-        const uint32_t bits = __float_as_uint(v[i]) & 0x7fffffffu;
-        const bool live = !(r >= dead.lo && r < dead.hi) && r < dead.tail;
-        if (live && bits < 0x7f800000u && bits) top = max(top, (int)(bits >> 23) + 1);
+    // lo, hi: addresses of the codes in the ring; row: of the tile
+    __device__ __forceinline__ void read(const CodeRing<8> &ring, int st, uint32_t lo, uint32_t hi, int row, int) {
+        c[0] = ld_shared_16(lo);
+        c[1] = ld_shared_16(hi);
+        s = ring.scale[st][row];
     }
-    top = __reduce_max_sync(0xffffffffu, top);
-    return top ? top - 127 : kNone;
-}
+    __device__ __forceinline__ void convert(float unit, uint32_t (&h)[2][8]) const {
+        // the scale as hi + lo, so that code * scale is rounded once (code * lo is far below the last place)
+        const float x = s * unit;
+        const uint32_t hi = pack_f16x2(x, x);
+        const float rest = x - __half2float(__ushort_as_half((unsigned short)hi));
+        const uint32_t lo = pack_f16x2(rest, rest);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            e4m3x4_to_f16x2x2(c[u].x, h[u][0], h[u][1]);
+            e4m3x4_to_f16x2x2(c[u].y, h[u][2], h[u][3]);
+            e4m3x4_to_f16x2x2(c[u].z, h[u][4], h[u][5]);
+            e4m3x4_to_f16x2x2(c[u].w, h[u][6], h[u][7]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[u][e] = fma_f16x2(h[u][e], hi, mul_f16x2(h[u][e], lo));
+        }
+    }
+};
+template <>
+struct Piece<4> {
+    uint2 c[2];
+    uint32_t s[2], exp;
 
-__device__ __forceinline__ int top_exponent(const CodeRing<4> &s, int st, bool of_v, const DeadRows &dead, int lane) {
-    const uint32_t x = *reinterpret_cast<const uint32_t *>((of_v ? s.v_exp[st] : s.exp[st]) + 4 * lane);
+    __device__ __forceinline__ void read(const CodeRing<4> &ring, int st, uint32_t lo, uint32_t hi, int row, int chunk) {
+        c[0] = ld_shared_8(lo);
+        c[1] = ld_shared_8(hi);
+        const uint8_t *scale = ring.scale[st] + row * kFp4Groups + chunk;
+        s[0] = scale[0];
+        s[1] = scale[4];
+        exp = ring.exp[st][row];
+    }
+    __device__ __forceinline__ void convert(float unit, uint32_t (&h)[2][8]) const {
+        const float power = fp4_unit(exp) * unit;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const float x = e4m3_value(s[u]) * power;
+            const uint32_t x2 = pack_f16x2(x, x);
+            uint32_t lo[4], hi[4];
+            e2m1x8_to_f16x2x4(c[u].x, lo);
+            e2m1x8_to_f16x2x4(c[u].y, hi);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                h[u][e] = mul_f16x2(lo[e], x2);
+                h[u][4 + e] = mul_f16x2(hi[e], x2);
+            }
+        }
+    }
+};
+
+// The scales (8 bits) or exponents (4 bits) of rows 4 lane .. 4 lane + 3, K's and the V ones beside them, from which
+// the tile's powers of two are taken.
+template <int kBits>
+struct Tops;
+template <>
+struct Tops<8> {
+    float4 k, v;
+    __device__ __forceinline__ void read(const CodeRing<8> &ring, int st, int lane) {
+        k = *reinterpret_cast<const float4 *>(ring.scale[st] + 4 * lane);
+        v = *reinterpret_cast<const float4 *>(ring.v_scale[0] + 4 * lane);
+    }
+    // of row 4 lane + i: biased exponent + 1, 0 for a zero, an infinity and a NaN
+    __device__ __forceinline__ static int of(float x) {
+        const uint32_t bits = __float_as_uint(x) & 0x7fffffffu;
+        return bits < 0x7f800000u && bits ? (int)(bits >> 23) + 1 : 0;
+    }
+    __device__ __forceinline__ int at(bool of_v, int i) const {
+        const float4 &x = of_v ? v : k;
+        return of(i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w);
+    }
+};
+template <>
+struct Tops<4> {
+    uint32_t k, v;
+    __device__ __forceinline__ void read(const CodeRing<4> &ring, int st, int lane) {
+        k = *reinterpret_cast<const uint32_t *>(ring.exp[st] + 4 * lane);
+        v = *reinterpret_cast<const uint32_t *>(ring.v_exp[st] + 4 * lane);
+    }
+    __device__ __forceinline__ int at(bool of_v, int i) const {
+        const int e = (int)((of_v ? v : k) >> (8 * i) & 0xffu);
+        return e < (int)kFp4NanExp ? e : 0;
+    }
+};
+
+// Exponent n of the power of two that the live rows' largest scale is below (8 bits) or at (4 bits); kNone:
+// every one is zero or no number.
+constexpr int kNone = -1000;
+template <int kBits>
+__device__ __forceinline__ int top_exponent(const Tops<kBits> &x, bool of_v, const DeadRows &dead, int lane) {
     int top = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int r = 4 * lane + i, e = (int)(x >> (8 * i) & 0xffu);
-        const bool live = !(r >= dead.lo && r < dead.hi) && r < dead.tail;
-        if (live && e < (int)kFp4NanExp) top = max(top, e);
+        const int r = 4 * lane + i;
+        if (!(r >= dead.lo && r < dead.hi) && r < dead.tail) top = max(top, x.at(of_v, i));
     }
     top = __reduce_max_sync(0xffffffffu, top);
-    return top ? top - 127 : kNone;
+    return top ? min(max(top - 127, -126), 126) : kNone;
 }
 
 // 2^n as a float for n in -126 .. 127 (clamped).
 __device__ __forceinline__ float exp2_int(int n) { return __uint_as_float((uint32_t)(min(max(n, -126), 127) + 127) << 23); }
 
-// 16 values of row r, dims 16 chunk .. 16 chunk + 15, from the slot into an f16 tile: code * scale * unit,
-// `unit` a power of two.
-__device__ __forceinline__ void convert16(const CodeRing<8> &s, int st, int r, int chunk, float unit, uint32_t (&h)[8]) {
-    const uint4 c = *reinterpret_cast<const uint4 *>(s.codes[st] + sw128(r, chunk));
-    const float x = s.scale[st][r] * unit;
-    // the scale as hi + lo, so that code * scale is rounded once (code * lo is far below the last place)
-    const __half hi = __float2half_rn(x);
-    const __half lo = __float2half_rn(x - __half2float(hi));
-    const uint32_t hi2 = (uint32_t)__half_as_ushort(hi) * 0x10001u, lo2 = (uint32_t)__half_as_ushort(lo) * 0x10001u;
-    e4m3x4_to_f16x2x2(c.x, h[0], h[1]);
-    e4m3x4_to_f16x2x2(c.y, h[2], h[3]);
-    e4m3x4_to_f16x2x2(c.z, h[4], h[5]);
-    e4m3x4_to_f16x2x2(c.w, h[6], h[7]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = fma_f16x2(h[i], hi2, mul_f16x2(h[i], lo2));
-}
-
-__device__ __forceinline__ void convert16(const CodeRing<4> &s, int st, int r, int chunk, float unit, uint32_t (&h)[8]) {
-    // 64-byte rows, 64-byte swizzle: 16-byte piece p of row r is at p ^ (r / 2 % 4)
-    const uint2 c = *reinterpret_cast<const uint2 *>(s.codes[st] + r * kFp4RowCodes +
-                                                     ((((chunk >> 1) ^ (r >> 1)) & 3) << 4) + ((chunk & 1) << 3));
-    const float x = e4m3_value(s.scale[st][r * kFp4Groups + chunk]) * (fp4_unit(s.exp[st][r]) * unit);
-    const uint32_t x2 = (uint32_t)__half_as_ushort(__float2half_rn(x)) * 0x10001u;
-    uint32_t lo[4], hi[4];
-    e2m1x8_to_f16x2x4(c.x, lo);
-    e2m1x8_to_f16x2x4(c.y, hi);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i] = mul_f16x2(lo[i], x2);
-        h[4 + i] = mul_f16x2(hi[i], x2);
-    }
-}
-
-// This warp's 32 rows of a tile: a lane 16 values at a time, four rows a warp instruction.  Dead rows are
-// zeros: their codes and scales may be anything, and 0 * NaN is not 0.
+// This warp's 32 rows of a code tile into an f16 tile, 8 rows a round, the next round's read ahead.  Dead rows
+// are zeros: their codes and scales may be anything, and 0 * NaN is not 0.
+// Lanes 8q .. 8q + 3 have row q of the 8, lanes 8q + 4 .. 8q + 7 row q ^ 5, so that with the swizzles below neither
+// a load (whose rows must differ in bit 2) nor a store (in bit 0) meets a bank twice, and no lane has to exchange its
+// pieces first.
+// The loop stays rolled, and K and V share it: the roles of this kernel run different code at the same time, and
+// with eight rounds of half the size unrolled, once for K and once for V, warps waited for instructions more than for
+// anything else (2.3 of 10 warp-cycles an instruction; 2500 us for 8192 tokens after 8192).
 template <int kBits>
-__device__ __forceinline__ void convert_tile(const CodeRing<kBits> &s, int st, uint8_t (*dst)[kHalf], float unit,
+__device__ __forceinline__ void convert_tile(const CodeRing<kBits> &ring, int st, uint32_t dst, float unit,
                                              const DeadRows &dead, int w, int lane) {
-    const int chunk = lane & 7, half = chunk >> 2;
-    // lanes of the upper half of the dims store their two pieces in the other order: the halves of the tile
-    // are 16 KiB apart, and each store then meets every bank once
-    const int first = 2 * (chunk & 3) + half, second = 2 * (chunk & 3) + 1 - half;
-#pragma unroll 4
-    for (int i = 0; i < 8; ++i) {
-        const int r = w * 32 + i * 4 + (lane >> 3);
-        uint32_t h[8];
-        convert16(s, st, r, chunk, unit, h);
-        const bool live = !(r >= dead.lo && r < dead.hi) && r < dead.tail;
-        const uint4 p0 = live ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(0u, 0u, 0u, 0u);
-        const uint4 p1 = live ? make_uint4(h[4], h[5], h[6], h[7]) : make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4 *>(dst[half] + sw128(r, first)) = half ? p1 : p0;
-        *reinterpret_cast<uint4 *>(dst[half] + sw128(r, second)) = half ? p0 : p1;
+    constexpr int kRow = CodeRing<kBits>::kRow;
+    const int c = lane & 3;
+    int row = w * 32 + ((lane >> 3) ^ ((lane & 4) ? 5 : 0));
+    // 8 bits: 128-byte rows, 128-byte swizzle (sw128); 4 bits: 64-byte rows, 64-byte swizzle, in which 16-byte
+    // piece p of row r is at p ^ (r / 2 % 4).  Either repeats every 8 rows; 64 dims on flip one bit of the address.
+    uint32_t src = smem_u32(ring.codes[st]) + (kBits == 8 ? sw128(row, c)
+                                                          : row * kRow + (((c >> 1) ^ ((row >> 1) & 3)) << 4) + ((c & 1) << 3));
+    constexpr uint32_t kFlip = kBits == 8 ? 64 : 32;
+    uint32_t at = dst + sw128(row, 2 * c);
+    const bool any_dead = dead.any();
+    Piece<kBits> x;
+    x.read(ring, st, src, src ^ kFlip, row, c);
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+        Piece<kBits> next = x;
+        src += 8 * kRow;
+        if (b < 3) next.read(ring, st, src, src ^ kFlip, row + 8, c);
+        uint32_t h[2][8];
+        x.convert(unit, h);
+        if (any_dead && ((row >= dead.lo && row < dead.hi) || row >= dead.tail)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) h[e >> 3][e & 7] = 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            st_shared_16(at + u * kHalf, h[u][0], h[u][1], h[u][2], h[u][3]);
+            st_shared_16((at ^ 16u) + u * kHalf, h[u][4], h[u][5], h[u][6], h[u][7]);
+        }
+        x = next;
+        at += 1024;
+        row += 8;
     }
 }
 
 // Q in place, bf16 -> f16: this warp's quarter.
 __device__ __forceinline__ void convert_q(uint8_t *q, int w, int lane) {
     uint4 *p = reinterpret_cast<uint4 *>(q) + w * (4 * kHalf / 16 / kConvertWarps) + lane;
-#pragma unroll 4
+#pragma unroll 2
     for (int i = 0; i < 4 * kHalf / 16 / kConvertWarps / 32; ++i) {
         uint4 x = p[i * 32];
         x.x = bf16x2_to_f16x2(x.x);
@@ -357,151 +439,153 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         return __all_sync(0xffffffffu, wait_or_abort(smem_u32(bar), parity, abort_flag, a.err));
     };
 
-    if (warp >= kSoftmaxWarps) {
-        regs_dec();
-    if (warp == kProducerWarp) {
-        // ---------------------------------------------------------------- TMA producer
-        const bool leader = elect_one();
-        if (leader) {
-            tma_prefetch_map(&q_map);
-            tma_prefetch_map(&k_map);
-            tma_prefetch_map(&v_map);
-            tma_prefetch_map(&k16_map);
-            tma_prefetch_map(&v16_map);
-        }
-        // the cache and q may be written by the kernel just before this one on the stream
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        int units = 0, it = 0;               // units, code tiles (K and V) issued
-        bool ok = true;
-        for (int r = 0; ok; ++r) {
-            const int idx = snake<kSplit>(a, r, total);
-            if (idx < 0) break;
-            const Unit t = unit_for<kPlanned, kSplit>(a, idx, qblocks);
-            if (leader && t.error) record_error(a.err, kErrDevice | kErrQLen);
-            if (!t.run) continue;
-            const int32_t *bt = a.block_table + (size_t)t.s * a.max_blocks_per_seq;
-            for (int i = 0; i < 2 * t.n_kt; ++i, ++it) {
-                const int st = it % kRing;
-                if (it >= kRing && !(ok = wait_all(&sm.c_empty[st], ((it / kRing) - 1) & 1))) break;
-                const bool is_k = !(i & 1);
-                if (leader)
-                    load_codes<kBits>(a, t, bt, (t.kt0 + (i >> 1)) * kKT, is_k, sm.ring, st, smem_u32(&sm.c_full[st]),
-                                      is_k ? &k_map : &v_map, is_k ? &k16_map : &v16_map);
-                __syncwarp();
-                if (i == 0) {   // Q behind the first K tile, which does not wait for the unit before
-                    if (units >= 1 && !(ok = wait_all(&sm.q_empty, (units - 1) & 1))) {
-                        ++it;
-                        break;
-                    }
-                    if (leader) {
-                        const uint32_t qbar = smem_u32(&sm.q_full);
-                        mbar_arrive_expect_tx(qbar, 2 * kTileBytes);
-                        for (int x = 0; x < 2; ++x) {
-                            tma_load_3d(smem_u32(sm.q[x][0]), &q_map, qbar, 0, t.g * kGroup, t.tok0 + x * kTilePos);
-                            tma_load_3d(smem_u32(sm.q[x][1]), &q_map, qbar, 64, t.g * kGroup, t.tok0 + x * kTilePos);
+    if (warp >= kProducerWarp) {
+        regs_dec<kControlRegs>();
+        if (warp == kProducerWarp) {
+            // ---------------------------------------------------------------- TMA producer
+            const bool leader = elect_one();
+            if (leader) {
+                tma_prefetch_map(&q_map);
+                tma_prefetch_map(&k_map);
+                tma_prefetch_map(&v_map);
+                tma_prefetch_map(&k16_map);
+                tma_prefetch_map(&v16_map);
+            }
+            // the cache and q may be written by the kernel just before this one on the stream
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            int units = 0, it = 0;               // units, code tiles (K and V) issued
+            bool ok = true;
+            for (int r = 0; ok; ++r) {
+                const int idx = snake<kSplit>(a, r, total);
+                if (idx < 0) break;
+                const Unit t = unit_for<kPlanned, kSplit>(a, idx, qblocks);
+                if (leader && t.error) record_error(a.err, kErrDevice | kErrQLen);
+                if (!t.run) continue;
+                const int32_t *bt = a.block_table + (size_t)t.s * a.max_blocks_per_seq;
+                for (int i = 0; i < 2 * t.n_kt; ++i, ++it) {
+                    const int st = it % kRing;
+                    if (it >= kRing && !(ok = wait_all(&sm.c_empty[st], ((it / kRing) - 1) & 1))) break;
+                    const bool is_k = !(i & 1);
+                    if (leader)
+                        load_codes<kBits>(a, t, bt, (t.kt0 + (i >> 1)) * kKT, is_k, sm.ring, st, smem_u32(&sm.c_full[st]),
+                                          is_k ? &k_map : &v_map, is_k ? &k16_map : &v16_map);
+                    __syncwarp();
+                    if (i == 0) {   // Q behind the first K tile, which does not wait for the unit before
+                        if (units >= 1 && !(ok = wait_all(&sm.q_empty, (units - 1) & 1))) {
+                            ++it;
+                            break;
                         }
+                        if (leader) {
+                            const uint32_t qbar = smem_u32(&sm.q_full);
+                            mbar_arrive_expect_tx(qbar, 2 * kTileBytes);
+                            for (int x = 0; x < 2; ++x) {
+                                tma_load_3d(smem_u32(sm.q[x][0]), &q_map, qbar, 0, t.g * kGroup, t.tok0 + x * kTilePos);
+                                tma_load_3d(smem_u32(sm.q[x][1]), &q_map, qbar, 64, t.g * kGroup, t.tok0 + x * kTilePos);
+                            }
+                        }
+                        __syncwarp();
+                        ++units;
+                    }
+                }
+            }
+            // Drain: no TMA copy may still be landing when the CTA exits.  In the normal path every load has
+            // been consumed and these waits return at once.
+            if (units > 0) mbar_wait(smem_u32(&sm.q_full), (units - 1) & 1);
+            for (int i = max(0, it - kRing); i < it; ++i) mbar_wait(smem_u32(&sm.c_full[i % kRing]), (i / kRing) & 1);
+        } else if (warp == kMmaWarp) {
+            // ---------------------------------------------------------------- MMA issuer (as in prefill.cu)
+            const bool leader = elect_one();
+            if constexpr (kPlanned) asm volatile("griddepcontrol.wait;" ::: "memory");
+            const uint64_t qd0 = sdesc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
+            const uint64_t kd0 = sdesc_sw128(smem_u32(sm.k[0][0]), 16, 1024);
+            const uint64_t vd0 = sdesc_sw128(smem_u32(sm.v[0][0]), (uint32_t)kHalf, 1024);
+            int units = 0, it = 0;
+            int pend_it = -1, pend_j = 0;   // O_B += P_B V still to issue for key tile pend_it
+            bool ok = true;
+            auto issue_s = [&](int x, int ks) {
+                const uint64_t qa = qd0 + (uint64_t)(x * 2048);
+                const uint64_t kb = kd0 + (uint64_t)(ks * 2048);
+                const uint32_t sd = tmem + col_s(x);
+                if (leader) {
+                    umma_ss_c<false>(sd, qa, kb, kIdescQK);
+    #pragma unroll
+                    for (int kk = 1; kk < kD / 16; ++kk) {
+                        const uint64_t off = (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);
+                        umma_ss_c<true>(sd, qa + off, kb + off, kIdescQK);
+                    }
+                    umma_commit(smem_u32(&sm.s_full[x]));
+                }
+                __syncwarp();
+            };
+            auto issue_pv = [&](int x, int pit, int pj) -> bool {
+                const int vs = pit % kStages;
+                if (x == 0 && !wait_all(&sm.v_full[vs], (pit / kStages) & 1)) return false;
+                const uint64_t vb = vd0 + (uint64_t)(vs * 2048);
+                const uint32_t pa = tmem + col_s(x);
+                if (!wait_all(&sm.p_half[x][x], pit & 1)) return false;
+                tc_fence_after();
+                if (leader) {
+                    umma_ts(tmem + col_o(x), pa, vb, kIdescPV, pj > 0 ? 1u : 0u);
+    #pragma unroll
+                    for (int kk = 1; kk < kKT / 32; ++kk)
+                        umma_ts_c<true>(tmem + col_o(x), pa + kk * 8, vb + (uint64_t)(kk * 128), kIdescPV);
+                }
+                __syncwarp();
+                if (x == 0) {
+                    if (!wait_all(&sm.p_half[x][1], pit & 1)) return false;
+                    tc_fence_after();
+                }
+                if (leader) {
+    #pragma unroll
+                    for (int kk = kKT / 32; kk < kKT / 16; ++kk)
+                        umma_ts_c<true>(tmem + col_o(x), pa + kk * 8, vb + (uint64_t)(kk * 128), kIdescPV);
+                    umma_commit(smem_u32(&sm.o_done[x]));
+                    if (x == 1) umma_commit(smem_u32(&sm.v_empty[vs]));   // B is the V tile's last reader
+                }
+                __syncwarp();
+                return true;
+            };
+            for (int r = 0; ok; ++r) {
+                const int idx = snake<kSplit>(a, r, total);
+                if (idx < 0) break;
+                const Unit t = unit_for<kPlanned, kSplit>(a, idx, qblocks);
+                if (!t.run) continue;
+                if (!(ok = wait_all(&sm.q_ready, units & 1))) break;
+                for (int j = 0; j < t.n_kt; ++j, ++it) {
+                    const int ks = it % kStages;
+                    if (!(ok = wait_all(&sm.k_full[ks], (it / kStages) & 1))) break;
+                    tc_fence_after();
+                    issue_s(0, ks);                                        // S_A(j)
+                    if (pend_it >= 0 && !(ok = issue_pv(1, pend_it, pend_j))) break;   // O_B, tile j-1
+                    issue_s(1, ks);                                        // S_B(j)
+                    if (leader) {
+                        umma_commit(smem_u32(&sm.k_empty[ks]));
+                        if (j == t.n_kt - 1) umma_commit(smem_u32(&sm.q_empty));
                     }
                     __syncwarp();
-                    ++units;
+                    if (!(ok = issue_pv(0, it, j))) break;                 // O_A, tile j
+                    pend_it = it;
+                    pend_j = j;
                 }
+                // the unit's last O_B += P_B V now, not behind the next unit's Q and first S_A
+                if (ok && pend_it >= 0) ok = issue_pv(1, pend_it, pend_j);
+                pend_it = -1;
+                ++units;
             }
+            // Every MMA issued must have finished before tensor memory is released.
+            if (leader) umma_commit(smem_u32(&sm.mma_idle));
+            __syncwarp();
+            mbar_wait(smem_u32(&sm.mma_idle), 0);
         }
-        // Drain: no TMA copy may still be landing when the CTA exits.  In the normal path every load has
-        // been consumed and these waits return at once.
-        if (units > 0) mbar_wait(smem_u32(&sm.q_full), (units - 1) & 1);
-        for (int i = max(0, it - kRing); i < it; ++i) mbar_wait(smem_u32(&sm.c_full[i % kRing]), (i / kRing) & 1);
-    } else if (warp == kMmaWarp) {
-        // ---------------------------------------------------------------- MMA issuer (as in prefill.cu)
-        const bool leader = elect_one();
-        if constexpr (kPlanned) asm volatile("griddepcontrol.wait;" ::: "memory");
-        const uint64_t qd0 = sdesc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
-        const uint64_t kd0 = sdesc_sw128(smem_u32(sm.k[0][0]), 16, 1024);
-        const uint64_t vd0 = sdesc_sw128(smem_u32(sm.v[0][0]), (uint32_t)kHalf, 1024);
-        int units = 0, it = 0;
-        int pend_it = -1, pend_j = 0;   // O_B += P_B V still to issue for key tile pend_it
-        bool ok = true;
-        auto issue_s = [&](int x, int ks) {
-            const uint64_t qa = qd0 + (uint64_t)(x * 2048);
-            const uint64_t kb = kd0 + (uint64_t)(ks * 2048);
-            const uint32_t sd = tmem + col_s(x);
-            if (leader) {
-                umma_ss_c<false>(sd, qa, kb, kIdescQK);
-#pragma unroll
-                for (int kk = 1; kk < kD / 16; ++kk) {
-                    const uint64_t off = (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);
-                    umma_ss_c<true>(sd, qa + off, kb + off, kIdescQK);
-                }
-                umma_commit(smem_u32(&sm.s_full[x]));
-            }
-            __syncwarp();
-        };
-        auto issue_pv = [&](int x, int pit, int pj) -> bool {
-            const int vs = pit % kStages;
-            if (x == 0 && !wait_all(&sm.v_full[vs], (pit / kStages) & 1)) return false;
-            const uint64_t vb = vd0 + (uint64_t)(vs * 2048);
-            const uint32_t pa = tmem + col_s(x);
-            if (!wait_all(&sm.p_half[x][x], pit & 1)) return false;
-            tc_fence_after();
-            if (leader) {
-                umma_ts(tmem + col_o(x), pa, vb, kIdescPV, pj > 0 ? 1u : 0u);
-#pragma unroll
-                for (int kk = 1; kk < kKT / 32; ++kk)
-                    umma_ts_c<true>(tmem + col_o(x), pa + kk * 8, vb + (uint64_t)(kk * 128), kIdescPV);
-            }
-            __syncwarp();
-            if (x == 0) {
-                if (!wait_all(&sm.p_half[x][1], pit & 1)) return false;
-                tc_fence_after();
-            }
-            if (leader) {
-#pragma unroll
-                for (int kk = kKT / 32; kk < kKT / 16; ++kk)
-                    umma_ts_c<true>(tmem + col_o(x), pa + kk * 8, vb + (uint64_t)(kk * 128), kIdescPV);
-                umma_commit(smem_u32(&sm.o_done[x]));
-                if (x == 1) umma_commit(smem_u32(&sm.v_empty[vs]));   // B is the V tile's last reader
-            }
-            __syncwarp();
-            return true;
-        };
-        for (int r = 0; ok; ++r) {
-            const int idx = snake<kSplit>(a, r, total);
-            if (idx < 0) break;
-            const Unit t = unit_for<kPlanned, kSplit>(a, idx, qblocks);
-            if (!t.run) continue;
-            if (!(ok = wait_all(&sm.q_ready, units & 1))) break;
-            for (int j = 0; j < t.n_kt; ++j, ++it) {
-                const int ks = it % kStages;
-                if (!(ok = wait_all(&sm.k_full[ks], (it / kStages) & 1))) break;
-                tc_fence_after();
-                issue_s(0, ks);                                        // S_A(j)
-                if (pend_it >= 0 && !(ok = issue_pv(1, pend_it, pend_j))) break;   // O_B, tile j-1
-                issue_s(1, ks);                                        // S_B(j)
-                if (leader) {
-                    umma_commit(smem_u32(&sm.k_empty[ks]));
-                    if (j == t.n_kt - 1) umma_commit(smem_u32(&sm.q_empty));
-                }
-                __syncwarp();
-                if (!(ok = issue_pv(0, it, j))) break;                 // O_A, tile j
-                pend_it = it;
-                pend_j = j;
-            }
-            // the unit's last O_B += P_B V now, not behind the next unit's Q and first S_A
-            if (ok && pend_it >= 0) ok = issue_pv(1, pend_it, pend_j);
-            pend_it = -1;
-            ++units;
-        }
-        // Every MMA issued must have finished before tensor memory is released.
-        if (leader) umma_commit(smem_u32(&sm.mma_idle));
-        __syncwarp();
-        mbar_wait(smem_u32(&sm.mma_idle), 0);
     } else if (warp >= kConvertWarp) {
+        regs_dec<kConvertRegs>();
         // ---------------------------------------------------------------- converters
         if constexpr (kPlanned) asm volatile("griddepcontrol.wait;" ::: "memory");
         const int w = warp - kConvertWarp;
         // V' stays below 65504: codes reach 448 (2688 with their group's scale), so the tile's largest scale
         // may be this many powers of two above sigma
         constexpr int kHeadroom = kBits == 8 ? 7 : 4;
-        int units = 0, it = 0, kt = 0;       // units, code tiles, key tiles
+        int units = 0, it = 0;               // units, code tiles (K and V)
         bool ok = true;
         for (int r = 0; ok; ++r) {
             const int idx = snake<kSplit>(a, r, total);
@@ -509,55 +593,49 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             const Unit t = unit_for<kPlanned, kSplit>(a, idx, qblocks);
             if (!t.run) continue;
             int sigma = kNone;               // exponent of sigma
-            for (int j = 0; j < t.n_kt; ++j, ++kt) {
-                const DeadRows dead(t.win, (t.kt0 + j) * kKT);
-                const int ks = kt % kStages;
-                // K(j)
-                int st = it % kRing;
+            DeadRows dead(t.win, t.kt0 * kKT);
+            for (int i = 0; i < 2 * t.n_kt; ++i, ++it) {     // K(0), V(0), K(1), ...
+                const bool is_k = !(i & 1);
+                const int st = it % kRing, kt = it >> 1, ks = kt % kStages;
                 if (!(ok = wait_all(&sm.c_full[st], (it / kRing) & 1))) break;
-                const int top = top_exponent(sm.ring, st, false, dead, lane);
-                const int v_top = top_exponent(sm.ring, st, true, dead, lane);
+                int unit;                    // exponent of what the tile is divided by
                 float grow = 1.f;
-                if (v_top != kNone && (sigma == kNone || v_top > sigma + kHeadroom)) {
-                    const int up = min(max(v_top, -126), 126);
-                    if (sigma != kNone) grow = exp2_int(sigma - up);
-                    sigma = up;
+                if (is_k) {
+                    dead = DeadRows(t.win, (t.kt0 + (i >> 1)) * kKT);
+                    Tops<kBits> tops;
+                    tops.read(sm.ring, st, lane);
+                    const int top = top_exponent(tops, false, dead, lane);
+                    const int v_top = top_exponent(tops, true, dead, lane);
+                    if (v_top != kNone && (sigma == kNone || v_top > sigma + kHeadroom)) {
+                        if (sigma != kNone) grow = exp2_int(sigma - v_top);
+                        sigma = v_top;
+                    }
+                    unit = top == kNone ? 0 : top;
+                } else {
+                    unit = sigma == kNone ? 0 : sigma;
                 }
-                if (kt >= kStages && !(ok = wait_all(&sm.k_empty[ks], ((kt / kStages) - 1) & 1))) break;
-                const int unit = top == kNone ? 0 : min(max(top, -126), 126);
-                convert_tile<kBits>(sm.ring, st, sm.k[ks], exp2_int(-unit), dead, w, lane);
-                const float sig = exp2_int(sigma == kNone ? 0 : sigma);
-                if (w == 0 && lane == 0) sm.params[kt % kParams] = TileParams{exp2_int(unit), sig, grow};
+                if (kt >= kStages &&
+                    !(ok = wait_all(is_k ? &sm.k_empty[ks] : &sm.v_empty[ks], ((kt / kStages) - 1) & 1)))
+                    break;
+                if (is_k && w == 0 && lane == 0)
+                    sm.params[kt % kParams] = TileParams{exp2_int(unit), exp2_int(sigma == kNone ? 0 : sigma), grow};
+                convert_tile<kBits>(sm.ring, st, smem_u32(is_k ? sm.k[ks] : sm.v[ks]), exp2_int(-unit), dead, w, lane);
                 fence_proxy_async_smem();    // generic writes -> visible to the MMA's reads
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(smem_u32(&sm.k_full[ks]));
+                    mbar_arrive(smem_u32(is_k ? &sm.k_full[ks] : &sm.v_full[ks]));
                     mbar_arrive(smem_u32(&sm.c_empty[st]));
                 }
-                ++it;
-                if (j == 0) {                // Q, which has been on its way meanwhile
-                    if (!(ok = wait_all(&sm.q_full, units & 1))) break;
+                if (i == 0) {                // Q, which has been on its way meanwhile
+                    if (!(ok = wait_all(&sm.q_full, units & 1))) { ++it; break; }
                     convert_q(sm.q[0][0], w, lane);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(smem_u32(&sm.q_ready));
                     ++units;
                 }
-                // V(j)
-                st = it % kRing;
-                if (!(ok = wait_all(&sm.c_full[st], (it / kRing) & 1))) break;
-                if (kt >= kStages && !(ok = wait_all(&sm.v_empty[ks], ((kt / kStages) - 1) & 1))) break;
-                convert_tile<kBits>(sm.ring, st, sm.v[ks], exp2_int(sigma == kNone ? 0 : -sigma), dead, w, lane);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_u32(&sm.v_full[ks]));
-                    mbar_arrive(smem_u32(&sm.c_empty[st]));
-                }
-                ++it;
             }
         }
-    }
     } else {
         // ---------------------------------------------------------------- softmax warps
         // Warpgroup x (= warp / 4) owns query tile x; thread = one row = one TMEM lane.
@@ -594,7 +672,7 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             const int pos_first = t.pos0 + x * kTilePos;
             const int pos = pos_first + pl;
             float m = -INFINITY;                   // running max, log2 units (scaled)
-            float l = 0.f;                         // running sum of the f16 weights
+            float l = 0.f;                         // running sum of the weights
             float sigma = 1.f;                     // what O is in units of
             for (int j = 0; j < t.n_kt; ++j, ++it) {
                 ok = wait_or_abort(smem_u32(&sm.s_full[x]), it & 1, abort_flag, a.err);
@@ -680,13 +758,13 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                             float x0, x1;
                             ffma2(x0, x1, __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]), sl2, sl2,
                                   -m_sub, -m_sub);
-                            // weights are at most 2^8 (the lazy maximum), those under 2^-14 lose bits one by one
-                            const uint32_t pp = pack_f16x2(fast_exp2(x0), fast_exp2(x1));
-                            // the row sum uses the same f16-rounded weights the PV product uses
+                            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                            // weights are at most 2^8 (the lazy maximum); in f16 those under 2^-14 lose bits one by
+                            // one.  The row sum takes them before that rounding (2^-12 of a weight at most): the sum of
+                            // the rounded ones costs three instructions a pair more, 2000 of 10000 a tile.
+                            pk[e / 2] = pack_f16x2(p0, p1);
                             const int k = (e >> 1) & 1;
-                            part[2 * k] = add_f16_lo(pp, part[2 * k]);
-                            part[2 * k + 1] = add_f16_hi(pp, part[2 * k + 1]);
-                            pk[e / 2] = pp;
+                            fadd2(part[2 * k], part[2 * k + 1], p0, p1);
                         }
                         // P columns 16c..16c+15 go over S columns already read into registers
                         tmem_st16(lane_base + s_col + 16 * c, pk);

@@ -946,6 +946,11 @@ def _need_fp4_cache(cache, dev):
 def kv_append_fp4(k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, k_new, v_new, block_table, cu_q_lens, seq_lens,
                   workspace, stream=None) -> None:
     """Quantise the new tokens' K/V rows into the 4-bit cache (fp4_cache, in place)."""
+    if stream is None:
+        got = (_binding or _usual()).append_fp4(k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, k_new, v_new, block_table,
+                                                cu_q_lens, seq_lens, workspace)
+        if got is not None:
+            return _check("kv_append_fp4", got)
     cache = (k_codes, v_codes, k_scale, v_scale, k_exp, v_exp)
     _need(k_new, "k_new", torch.bfloat16, (None, NUM_KV_HEADS, HEAD_DIM))
     dev = k_new.device
@@ -967,8 +972,14 @@ def paged_rope_append_fp4(q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, k
                           stream=None) -> torch.Tensor:
     """paged_rope_append into the 4-bit cache (fp4_cache): k rows quantised from their rotated fp32 values,
     v rows as kv_append_fp4 does."""
-    cache = (k_codes, v_codes, k_scale, v_scale, k_exp, v_exp)
     pair_axis = _pair_axes(pair_axis)
+    if stream is None:
+        got = (_binding or _usual()).rope_append(None, q, k_new, v_new, k_codes, v_codes, k_scale, v_scale, k_exp, v_exp,
+                                                 block_table, cu_q_lens, seq_lens, workspace, rope_theta, positions,
+                                                 pair_axis, q_norm_weight, k_norm_weight, norm_eps, q_out)
+        if got is not None:
+            return got if type(got) is not int else _check("paged_rope_append_fp4", got)
+    cache = (k_codes, v_codes, k_scale, v_scale, k_exp, v_exp)
     _need(k_codes, "k_codes", torch.uint8)
     _need_fp4_cache(cache, k_codes.device)
     return _rope_append("paged_rope_append_fp4", load().paged_rope_append_fp4, q, k_new, v_new, cache, block_table,
@@ -1005,6 +1016,11 @@ def paged_kv_read_fp8(k_codes, v_codes, k_scale, v_scale, block_table, cu_rows, 
     """Rows of the 8-bit cache read back as bf16: (k, v), [total_rows, 8, 128] each.  Rows cu_rows[s] ..
     cu_rows[s + 1] - 1 (int32 [S + 1]) are the tokens of sequence s from position first[s] (int32 [S]) on;
     rows behind the last sequence are left as they are."""
+    if stream is None:
+        got = (_binding or _usual()).kv_read(k_codes, v_codes, k_scale, v_scale, None, None, block_table, cu_rows, first,
+                                             total_rows, workspace, k_out, v_out)
+        if got is not None:
+            return got if type(got) is not int else _check("paged_kv_read_fp8", got)
     _need(k_codes, "k_codes", torch.uint8)
     _need_fp8_cache(k_codes, v_codes, k_scale, v_scale, k_codes.device)
     return _kv_read("paged_kv_read_fp8", load().paged_kv_read_fp8, (k_codes, v_codes, k_scale, v_scale), block_table,
@@ -1014,6 +1030,11 @@ def paged_kv_read_fp8(k_codes, v_codes, k_scale, v_scale, block_table, cu_rows, 
 def paged_kv_read_fp4(k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, block_table, cu_rows, first, total_rows: int,
                       workspace, *, k_out=None, v_out=None, stream=None):
     """paged_kv_read_fp8 of the 4-bit cache."""
+    if stream is None:
+        got = (_binding or _usual()).kv_read(k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, block_table, cu_rows, first,
+                                             total_rows, workspace, k_out, v_out)
+        if got is not None:
+            return got if type(got) is not int else _check("paged_kv_read_fp4", got)
     cache = (k_codes, v_codes, k_scale, v_scale, k_exp, v_exp)
     _need(k_codes, "k_codes", torch.uint8)
     _need_fp4_cache(cache, k_codes.device)
@@ -1027,6 +1048,11 @@ def paged_attn_decode_fp4(q, k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, b
     """One query token per sequence over the 4-bit cache: the whole context, or its first `sinks` and last
     `window` tokens; q [B, 32, 128] -> out [B, 32, 128] (bf16).  A row with seq_lens 0 gives zeros.
     split_tokens: visible tokens per CTA (a multiple of 256), 0 = the library's choice."""
+    if stream is None:
+        got = (_binding or _usual()).decode_fp4(q, k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, block_table, seq_lens,
+                                                workspace, window, sinks, scale, split_tokens, out, lse)
+        if got is not None:
+            return got if type(got) is not int else _check("paged_attn_decode_fp4", got)
     cache = (k_codes, v_codes, k_scale, v_scale, k_exp, v_exp)
     _need(k_codes, "k_codes", torch.uint8)
     dev = k_codes.device
@@ -1069,6 +1095,11 @@ def paged_attn_prefill_fp8(q, k_codes, v_codes, k_scale, v_scale, block_table, c
                            out=None, lse=None, stream=None) -> torch.Tensor:
     """Causal attention of each sequence's new tokens (q [T, 32, 128], appended before) over its context in the
     8-bit cache, all of it or the first `sinks` tokens and the last `window` up to each new one."""
+    if stream is None:
+        got = (_binding or _usual()).prefill_low(q, k_codes, v_codes, k_scale, v_scale, None, None, block_table, cu_q_lens,
+                                                 seq_lens, max_q_len, workspace, window, sinks, scale, out, lse)
+        if got is not None:
+            return got if type(got) is not int else _check("paged_attn_prefill_fp8", got)
     _need(k_codes, "k_codes", torch.uint8)
     _need_fp8_cache(k_codes, v_codes, k_scale, v_scale, k_codes.device)
     return _prefill_low("paged_attn_prefill_fp8", load().paged_attn_prefill_fp8, q, (k_codes, v_codes, k_scale, v_scale),
@@ -1079,6 +1110,11 @@ def paged_attn_prefill_fp4(q, k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, 
                            max_q_len: int, workspace, *, window: int = FULL_WINDOW, sinks: int = 0,
                            scale: float = DEFAULT_SCALE, out=None, lse=None, stream=None) -> torch.Tensor:
     """paged_attn_prefill_fp8 over the 4-bit cache."""
+    if stream is None:
+        got = (_binding or _usual()).prefill_low(q, k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, block_table, cu_q_lens,
+                                                 seq_lens, max_q_len, workspace, window, sinks, scale, out, lse)
+        if got is not None:
+            return got if type(got) is not int else _check("paged_attn_prefill_fp4", got)
     cache = (k_codes, v_codes, k_scale, v_scale, k_exp, v_exp)
     _need(k_codes, "k_codes", torch.uint8)
     _need_fp4_cache(cache, k_codes.device)

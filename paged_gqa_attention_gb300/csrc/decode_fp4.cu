@@ -21,6 +21,8 @@
 //     P * 2^(e - sigma) in f16, sigma the largest exponent it has seen, and rescales its accumulator
 //     when sigma grows, as the online softmax does for its maximum;
 //   * tokens that are not attended to get scale 0 in V (every code is finite) and score -infinity.
+#include <cuda_fp16.h>
+
 #include <atomic>
 
 #include "cluster.cuh"
@@ -91,6 +93,22 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
     uint32_t d;
     asm("{\n .reg .b16 a;\n cvt.u16.u32 a, %1;\n cvt.rn.f16x2.e4m3x2 %0, a;\n}" : "=r"(d) : "r"(two));
+    return d;
+}
+
+__device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t a) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&a));
+}
+
+// One half of an f16x2, twice
+__device__ __forceinline__ uint32_t low_f16x2(uint32_t a) {
+    uint32_t d;
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n mov.b32 %0, {l, l};\n}" : "=r"(d) : "r"(a));
+    return d;
+}
+__device__ __forceinline__ uint32_t high_f16x2(uint32_t a) {
+    uint32_t d;
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n mov.b32 %0, {h, h};\n}" : "=r"(d) : "r"(a));
     return d;
 }
 
@@ -234,14 +252,15 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // Q^T as the B operand of S^T = K Q^T, f16: of 32-dim piece c, k16 step u holds dims 32c + 8tq + 4u ..
-    // + 3 of head gq (the order the code fragments arrive in); heads 4..7 are zero.
+    // + 3 of head gq & 3 (the order the code fragments arrive in); columns 0..3 have the piece's first 16
+    // dims (tq < 2) and zeros, columns 4..7 the other 16.
     uint32_t qb[4][2][2];
     {
         const uint4 *qrow = reinterpret_cast<const uint4 *>(
             static_cast<const __nv_bfloat16 *>(a.q) + ((size_t)b * kHq + g * kGroup + (gq & 3)) * kD);
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const uint4 v = gq < kGroup ? __ldg(qrow + c * 4 + tq) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 v = (gq >> 2) == (tq >> 1) ? __ldg(qrow + c * 4 + tq) : make_uint4(0u, 0u, 0u, 0u);
             qb[c][0][0] = bf16x2_to_f16x2(v.x);
             qb[c][0][1] = bf16x2_to_f16x2(v.y);
             qb[c][1][0] = bf16x2_to_f16x2(v.z);
@@ -249,18 +268,20 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
         }
     }
 
-    float m0 = -INFINITY, m1 = -INFINITY;   // running max (log2 units) of heads 2tq, 2tq+1
+    float m0 = -INFINITY, m1 = -INFINITY;   // running max (log2 units) of heads 2tq, 2tq+1 (mod 4)
     float l0 = 0.f, l1 = 0.f;               // this thread's share of the running sums
     int sigma = kNoSigma;                   // exponent that the accumulator is in units of
-    float acc[8][4];                        // O^T tiles
+    float acc[4][4];                        // O^T tiles
 #pragma unroll
-    for (int mt = 0; mt < 8; ++mt)
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[mt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) acc[c][e] = 0.f;
 
     const int row = w * kWarpTokens + ri + ((mi & 1) << 3);   // token row addressed by this lane (+ 16 u)
     const uint32_t pick_k = tq & 2 ? 0x7531u : 0x6420u;       // odd or even bytes of a token's 8 scales
     const uint32_t pick_v = gq & 4 ? 0x7531u : 0x6420u;
+    // P of a token beside a zero: even dims (columns 0..3) take it in the lower half, odd ones in the upper
+    const uint32_t pick_p0 = gq & 4 ? 0x1044u : 0x4410u, pick_p1 = gq & 4 ? 0x3244u : 0x4432u;
 
     for (int i = 0; i < n_tiles; ++i) {
         const int st = i % kStages;
@@ -270,78 +291,76 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
         }
         // this warp's 32 rows hold positions p_w .. p_w + 31
         const int p_w = wt.tile(v_begin + i) * kTile + w * kWarpTokens;
-        const auto valid = [&](int r) { return p_w + r < seq_len && wt.sees(p_w + r); };
         if (p_w < seq_len && wt.sees_any(p_w, kWarpTokens)) {
             const uint32_t kc = smem_u32(sm.codes[st][0]);
             const uint32_t vc = smem_u32(sm.codes[st][1]);
             const uint8_t *ksc = sm.scales[st][0] + w * kWarpTokens * kFp4Groups;
             const uint8_t *vsc = sm.scales[st][1] + w * kWarpTokens * kFp4Groups;
-            const uint8_t *kex = sm.exps[st][0] + w * kWarpTokens;
-            const uint8_t *vex = sm.exps[st][1] + w * kWarpTokens;
 
-            // S^T[2 x 16 tokens x 8 heads] = K . Q^T, 64 dims per ldmatrix
-            float s[2][4];
+            // lane l's token is p_w + l: whether it is attended to, K's factor, V's exponent
+            const bool ok = p_w + lane < seq_len && wt.sees(p_w + lane);
+            const uint32_t seen = __ballot_sync(0xffffffffu, ok);
+            const float kf = fp4_unit(sm.exps[st][0][w * kWarpTokens + lane]) * a.scale_log2;
+            const uint32_t ev = sm.exps[st][1][w * kWarpTokens + lane];
+            const int ve = !ok || ev == 0 ? kNoSigma : (int)ev - 127;   // 128: NaN
+
+            // S^T[2 x 16 tokens x 8 columns] = K . Q^T, 64 dims per ldmatrix
+            float x[2][4];
+            float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[u][e] = 0.f;
-                // scales of tokens gq and gq + 8, one byte per 32-dim piece (this lane's 16-dim half of it)
+                // scales of tokens gq and gq + 8, one byte per 32-dim piece (this column's 16-dim half of it)
                 uint32_t sc[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint2 x = *reinterpret_cast<const uint2 *>(ksc + (16 * u + 8 * h + gq) * kFp4Groups);
-                    sc[h] = __byte_perm(x.x, x.y, pick_k);
+                    const uint2 y = *reinterpret_cast<const uint2 *>(ksc + (16 * u + 8 * h + gq) * kFp4Groups);
+                    sc[h] = __byte_perm(y.x, y.y, pick_k);
                 }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[u][e] = 0.f;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     uint32_t r[4];
                     ldsm_x4(r, kc + sw64(row + 16 * u, 2 * j + (mi >> 1)));
-                    uint32_t f[2];   // per token: scales of pieces 2j and 2j + 1
+                    float2 f[2];   // per token: scales of pieces 2j and 2j + 1
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) f[h] = e4m3x2_to_f16x2(sc[h] >> (16 * j));
+                    for (int h = 0; h < 2; ++h) f[h] = f16x2_to_f32x2(e4m3x2_to_f16x2(sc[h] >> (16 * j)));
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t lo[4], hi[4];
                         e2m1x8_to_f16x2x4(r[2 * c], lo);        // token gq, dims 32(2j+c) + 8tq ..
                         e2m1x8_to_f16x2x4(r[2 * c + 1], hi);    // token gq + 8
-                        const uint32_t f_lo = __byte_perm(f[0], 0u, c ? 0x3232 : 0x1010);
-                        const uint32_t f_hi = __byte_perm(f[1], 0u, c ? 0x3232 : 0x1010);
+                        float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                         for (int v = 0; v < 2; ++v) {
-                            const uint32_t af[4] = {mul_f16x2(lo[2 * v], f_lo), mul_f16x2(hi[2 * v], f_hi),
-                                                    mul_f16x2(lo[2 * v + 1], f_lo), mul_f16x2(hi[2 * v + 1], f_hi)};
-                            mma_16816_f16(s[u], af, qb[2 * j + c][v][0], qb[2 * j + c][v][1]);
+                            const uint32_t af[4] = {lo[2 * v], hi[2 * v], lo[2 * v + 1], hi[2 * v + 1]};
+                            mma_16816_f16(s, af, qb[2 * j + c][v][0], qb[2 * j + c][v][1]);
                         }
+                        const float f_lo = c ? f[0].y : f[0].x, f_hi = c ? f[1].y : f[1].x;
+                        x[u][0] = fmaf(s[0], f_lo, x[u][0]);
+                        x[u][1] = fmaf(s[1], f_lo, x[u][1]);
+                        x[u][2] = fmaf(s[2], f_hi, x[u][2]);
+                        x[u][3] = fmaf(s[3], f_hi, x[u][3]);
                     }
                 }
-            }
-            // s[u][0]: (token 16u + gq, head 2tq)   s[u][1]: (.., head 2tq+1)
-            // s[u][2]: (token 16u + gq + 8, head 2tq) ...
-            float x[2][4];
-            int ve[2][2];             // V exponents of tokens 16u + gq (+ 8), unbiased
-            float mx0 = -INFINITY, mx1 = -INFINITY;
-            int vmax = kNoSigma;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
+                // the other half of every piece; then x[u][2h + e]: (token 16u + 8h + gq, head 2tq + e mod 4)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int t = 16 * u + 8 * h + gq;
-                    const bool ok = valid(t);
-                    const float k = ok ? fp4_unit(kex[t]) * a.scale_log2 : 0.f;
-                    // (columns of padding heads 4..7: finite dummies, results discarded)
-                    x[u][2 * h] = tq >= 2 ? 0.f : ok ? s[u][2 * h] * k : -INFINITY;
-                    x[u][2 * h + 1] = tq >= 2 ? 0.f : ok ? s[u][2 * h + 1] * k : -INFINITY;
+                    const float k = __shfl_sync(0xffffffffu, kf, t);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float &y = x[u][2 * h + e];
+                        y = (y + __shfl_xor_sync(0xffffffffu, y, 2)) * k;
+                        if (seen != 0xffffffffu && !(seen >> t & 1u)) y = -INFINITY;
+                    }
                     mx0 = fmaxf(mx0, x[u][2 * h]);
                     mx1 = fmaxf(mx1, x[u][2 * h + 1]);
-                    const int e = vex[t];
-                    ve[u][h] = !ok ? kNoSigma : e == (int)kFp4NanExp ? 128 : e ? e - 127 : kNoSigma;
-                    if (ve[u][h] < 128) vmax = max(vmax, ve[u][h]);
                 }
             }
             // lazy rescaling, as in decode_fp8.cu: one vote finds the tiles in which a maximum has grown by
             // more than 2^8 or a V exponent is the largest so far, and only they reduce over the warp
-            float f0 = 1.f, f1 = 1.f;
-            if (__any_sync(0xffffffffu, mx0 > m0 + 8.f || mx1 > m1 + 8.f || vmax > sigma)) {
+            if (__any_sync(0xffffffffu, mx0 > m0 + 8.f || mx1 > m1 + 8.f || (ve > sigma && ve < 128))) {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) {
                     mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
@@ -354,19 +373,19 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
                 m1 = mn1;
                 l0 *= alpha0;
                 l1 *= alpha1;
-                const int top = __reduce_max_sync(0xffffffffu, vmax);
+                const int top = __reduce_max_sync(0xffffffffu, ve < 128 ? ve : kNoSigma);
                 const float grow = top > sigma ? pow2_or_0(sigma - top) : 1.f;
                 sigma = max(sigma, top);
-                f0 = alpha0 * grow;
-                f1 = alpha1 * grow;
+                const float f0 = alpha0 * grow, f1 = alpha1 * grow;
 #pragma unroll
-                for (int mt = 0; mt < 8; ++mt) {
-                    acc[mt][0] *= f0;
-                    acc[mt][1] *= f1;
-                    acc[mt][2] *= f0;
-                    acc[mt][3] *= f1;
+                for (int c = 0; c < 4; ++c) {
+                    acc[c][0] *= f0;
+                    acc[c][1] *= f1;
+                    acc[c][2] *= f0;
+                    acc[c][3] *= f1;
                 }
             }
+            const float vf = ve == 128 ? __int_as_float(0x7fc00000) : pow2_or_0(ve - sigma);
             uint32_t pb[2][2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -375,26 +394,25 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
                     const float p0 = fast_exp2(x[u][2 * h] - m0), p1 = fast_exp2(x[u][2 * h + 1] - m1);
                     l0 += p0;
                     l1 += p1;
-                    const float r = ve[u][h] == 128 ? __int_as_float(0x7fc00000) : pow2_or_0(ve[u][h] - sigma);
+                    const float r = __shfl_sync(0xffffffffu, vf, 16 * u + 8 * h + gq);
                     // P^T as the B operand of O^T += V^T P^T: transpose the 8x8 16-bit blocks
                     pb[u][h] = movmatrix_trans(pack_f16x2(p0 * r, p1 * r));
                 }
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                // scales of tokens 2tq, 2tq + 1 and 2tq + 8, 2tq + 9: one pair per 32-dim piece
-                uint32_t f[2][4];
+                // scales of tokens 2tq, 2tq + 1 of both halves, one byte per 32-dim piece
+                uint32_t sc[2][2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int t = 16 * u + 8 * h + 2 * tq;
                     const uint4 y = *reinterpret_cast<const uint4 *>(vsc + t * kFp4Groups);
-                    const uint32_t s0 = valid(t) ? __byte_perm(y.x, y.y, pick_v) : 0u;
-                    const uint32_t s1 = valid(t + 1) ? __byte_perm(y.z, y.w, pick_v) : 0u;
-                    const uint32_t lo = __byte_perm(s0, s1, 0x5140), hi = __byte_perm(s0, s1, 0x7362);
-                    f[h][0] = e4m3x2_to_f16x2(lo);
-                    f[h][1] = e4m3x2_to_f16x2(lo >> 16);
-                    f[h][2] = e4m3x2_to_f16x2(hi);
-                    f[h][3] = e4m3x2_to_f16x2(hi >> 16);
+                    sc[h][0] = __byte_perm(y.x, y.y, pick_v);
+                    sc[h][1] = __byte_perm(y.z, y.w, pick_v);
+                    if (seen != 0xffffffffu) {
+                        if (!(seen >> t & 1u)) sc[h][0] = 0u;
+                        if (!(seen >> t & 2u)) sc[h][1] = 0u;
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -402,18 +420,17 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
                     uint32_t r[4];
                     ldsm_x4_trans(r, vc + sw64(row + 16 * u, 2 * j + (mi >> 1)));
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t lo[4], hi[4];
-                        e2m1x8_to_f16x2x4(r[2 * c], lo);        // {token 2tq: dims 4gq..; token 2tq+1}
-                        e2m1x8_to_f16x2x4(r[2 * c + 1], hi);    // tokens 2tq + 8, 2tq + 9
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t b0 = __byte_perm(pb[u][h], 0u, pick_p0), b1 = __byte_perm(pb[u][h], 0u, pick_p1);
+                        const uint32_t f0 = e4m3x2_to_f16x2(sc[h][0] >> (16 * j)), f1 = e4m3x2_to_f16x2(sc[h][1] >> (16 * j));
 #pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            const uint32_t af[4] = {
-                                mul_f16x2(__byte_perm(lo[v], lo[2 + v], 0x5410), f[0][2 * j + c]),
-                                mul_f16x2(__byte_perm(lo[v], lo[2 + v], 0x7632), f[0][2 * j + c]),
-                                mul_f16x2(__byte_perm(hi[v], hi[2 + v], 0x5410), f[1][2 * j + c]),
-                                mul_f16x2(__byte_perm(hi[v], hi[2 + v], 0x7632), f[1][2 * j + c])};
-                            mma_16816_f16(acc[2 * (2 * j + c) + v], af, pb[u][0], pb[u][1]);
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t d[4];   // {token 2tq: dims 4gq, +1; +2, +3; token 2tq + 1: ..}
+                            e2m1x8_to_f16x2x4(r[2 * c + h], d);
+                            const uint32_t s0 = c ? high_f16x2(f0) : low_f16x2(f0), s1 = c ? high_f16x2(f1) : low_f16x2(f1);
+                            const uint32_t af[4] = {mul_f16x2(d[0], s0), mul_f16x2(d[1], s0), mul_f16x2(d[2], s1),
+                                                    mul_f16x2(d[3], s1)};
+                            mma_16816_f16(acc[2 * j + c], af, b0, b1);
                         }
                     }
                 }
@@ -431,19 +448,19 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
     }
     // the merge arrays overlay the stages: every consumer warp must be done with them
     named_barrier(1, kConsumerWarps * 32);
-    if (tq < 2) {
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
-            const int d = (mt >> 1) * 32 + 4 * gq + 2 * (mt & 1);
-            *reinterpret_cast<float2 *>(&sm.mg.o[w][2 * tq][d]) = make_float2(acc[mt][0], acc[mt][2]);
-            *reinterpret_cast<float2 *>(&sm.mg.o[w][2 * tq + 1][d]) = make_float2(acc[mt][1], acc[mt][3]);
-        }
-        if (gq == 0) {
-            sm.mg.m[w][2 * tq] = m0;
-            sm.mg.m[w][2 * tq + 1] = m1;
-            sm.mg.l[w][2 * tq] = l0;
-            sm.mg.l[w][2 * tq + 1] = l1;
-        }
+    for (int c = 0; c < 4; ++c) {
+        const int d = c * 32 + 4 * gq + (tq >> 1), hd = 2 * (tq & 1);
+        sm.mg.o[w][hd][d] = acc[c][0];
+        sm.mg.o[w][hd + 1][d] = acc[c][1];
+        sm.mg.o[w][hd][d + 2] = acc[c][2];
+        sm.mg.o[w][hd + 1][d + 2] = acc[c][3];
+    }
+    if (tq < 2 && gq == 0) {
+        sm.mg.m[w][2 * tq] = m0;
+        sm.mg.m[w][2 * tq + 1] = m1;
+        sm.mg.l[w][2 * tq] = l0;
+        sm.mg.l[w][2 * tq + 1] = l1;
     }
     if (lane == 0) sm.mg.sigma[w] = sigma;
     named_barrier(1, kConsumerWarps * 32);

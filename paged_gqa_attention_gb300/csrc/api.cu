@@ -186,13 +186,16 @@ long long window_tiles_bound(int window, int sinks, int max_blocks_per_seq, int 
 // as long as a walk, every one wave_us to start.  So many sequences are split only where few CTAs
 // would be left for a last wave of long walks: 39 sequences and 4096 tokens 103.9 us in 4 (unsplit,
 // 304 CTAs and 8 more, 116.4), but 56 sequences 134.4 unsplit (in 2 137.5) and 40 with 512 tokens
-// 21.5 (in 2 23.8).  Over the 8-bit cache splits saved at most 5 % there and are not tried.
+// 21.5 (in 2 23.8).  Over the 8-bit cache splits saved at most 5 % there and are not tried.  Over the
+// 4-bit cache two are: 64 sequences and 8192 to 16384 tokens 183 us (unsplit 204, in 3 176), 16384 tokens
+// 227 (unsplit 251), but 48 and 4096 53.7 unsplit (in 2 58.9); one sequence and 4096 tokens takes 7.4 us in 8
+// (unsplit 21.3), 9001 10.1 in 12 (44.2).
 struct SplitCost {
     double tile_us, crowded, stream_us, cluster_us, merge_us, merge_each_us, wave_us;
     int most_waved;      // splits tried where even unsplit sequences fill more than one wave
 };
 constexpr SplitCost kSplitCost = {0.42, 1.0, 0.0049, 1.4, 1.9, 0.07, 1.5, 5};          // 64 tokens in bf16
-constexpr SplitCost kSplitCostFp4 = {1.1, 1.5, 0.0058, 1.7, 2.3, 0.15, 1.5, 1};        // 256 tokens in 4 bits
+constexpr SplitCost kSplitCostFp4 = {1.1, 1.57, 0.005, 2.3, 1.8, 0.22, 1.7, 2};        // 256 tokens in 4 bits
 constexpr SplitCost kSplitCostFp8 = {0.78, 1.8, 0.0053, 1.7, 2.3, 0.15, 1.5, 1};       // 128 tokens in 8 bits
 
 int auto_window_split(int batch, long long tiles, int num_sms, const SplitCost &c) {
@@ -206,7 +209,8 @@ int auto_window_split(int batch, long long tiles, int num_sms, const SplitCost &
         const long long splits = (tiles + per - 1) / per;
         const long long ctas = pairs * splits;
         if (splits > 1 && ctas > kDecodeCtaCap) break;   // what a workspace provides for
-        const double walk = c.tile_us * (ctas > num_sms ? c.crowded : 1.0) * (double)per;
+        const long long beside = waves ? ctas % places : ctas;   // CTAs that run while the longest walk ends
+        const double walk = c.tile_us * (beside > num_sms ? c.crowded : 1.0) * (double)per;
         double us;
         if (waves) {
             const double last = stream * (double)(ctas % places) / (double)ctas;

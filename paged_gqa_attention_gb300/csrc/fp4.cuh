@@ -87,11 +87,16 @@ __device__ __forceinline__ void e2m1x8_to_f16x2x4(uint32_t codes, uint32_t (&h)[
 // The codes of eight values y of a group with E4M3 scale byte `scale`.
 __device__ __forceinline__ uint32_t fp4_codes(const float (&y)[8], uint32_t scale) {
     const float m = e4m3_value(scale);
-    const float r = m > 0.f ? __frcp_rn(m) : 0.f;
+    const float r = __frcp_rn(m);
     float q[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = m > 0.f ? fp4_quotient(y[e], m, r) : 0.f;
-    return f32x8_to_e2m1x8(q);
+    for (int e = 0; e < 8; e += 2) {   // fp4_quotient, two at a time
+        float p0, p1, d0, d1;
+        ffma2(p0, p1, y[e], y[e + 1], r, r, -0.f, -0.f);
+        ffma2(d0, d1, p0, p1, m, m, -y[e], -y[e + 1]);
+        ffma2(q[e], q[e + 1], d0, d1, -r, -r, p0, p1);
+    }
+    return m > 0.f ? f32x8_to_e2m1x8(q) : 0u;
 }
 
 __device__ __forceinline__ uint32_t umax_xor(uint32_t x, int o) {

@@ -16,9 +16,8 @@
 // [block][head][slot].  Page "从零搭建AI工程能力：手写KV Cache与动态批处理实战" §3.2: an 8-bit
 // KV cache halves its memory.
 //
-// The 4-bit variant (k_exp set; the format and its rule: fp4.cuh) takes the same half-warp per row: a
-// lane holds 8 values, two lanes a group of 16.  16384 ragged tokens: see rope_append.cu, which reads
-// the same rows.
+// The 4-bit variant (k_exp set; the format and its rule: fp4.cuh) gives a lane the 16 values of a group:
+// the group's maximum, found among the packed bf16 bits, needs no other lane, the row's three shuffles.
 //
 // The kernel is a chain of dependent loads (which sequence owns the token, its
 // length, its block id, then the data), so its time is latency: the owner is first
@@ -35,6 +34,13 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 8;  // 4 tokens x {K, V} per CTA
+
+// The larger 16-bit halves, unsigned
+__device__ __forceinline__ uint32_t umax_u16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 
 // kBits: 16 (copied), 8 or 4
 template <int kBits>
@@ -54,7 +60,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(AppendArgs a) {
         static_cast<const char *>(is_v ? a.v_new : a.k_new) + (size_t)t * kTokenBytes);
     uint4 v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = __ldg(src + lane + 32 * k);
+    for (int k = 0; k < 4; ++k) v[k] = __ldg(src + (kBits == 4 ? 2 * lane + 64 * (k >> 1) + (k & 1) : lane + 32 * k));
 
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         // cu_q_lens must start at 0 and end at total_tokens
@@ -94,40 +100,40 @@ __global__ void __launch_bounds__(kWarps * 32) kv_append_kernel(AppendArgs a) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) dst[lane + 32 * k] = v[k];
     } else if constexpr (kBits == 4) {
-        // vector k of lane l: KV head 2k + l/16, dims 8 (l%16) .. 8 (l%16) + 7
+        // vectors 2k, 2k + 1 of lane l: KV head 4k + l/8, group l%8
         uint8_t *codes = static_cast<uint8_t *>(is_v ? a.v_pool : a.k_pool) +
                          ((size_t)blk * kBlock + slot) * (kHkv * kFp4RowCodes);
         const size_t row0 = (size_t)blk * kHkv * kBlock + slot;   // + head * 256
         uint8_t *scales = is_v ? a.v_scale4 : a.k_scale4;
         uint8_t *exps = is_v ? a.v_exp : a.k_exp;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-            float y[8];
-            uint32_t amax = 0;
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t w[8] = {v[2 * k].x,     v[2 * k].y,     v[2 * k].z,     v[2 * k].w,
+                                   v[2 * k + 1].x, v[2 * k + 1].y, v[2 * k + 1].z, v[2 * k + 1].w};
+            uint32_t pair = 0;   // magnitudes as bits, of the even and of the odd values
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                y[2 * e] = bf16_lo(w[e]);
-                y[2 * e + 1] = bf16_hi(w[e]);
-                amax = max(amax, max(__float_as_uint(fabsf(y[2 * e])), __float_as_uint(fabsf(y[2 * e + 1]))));
-            }
+            for (int e = 0; e < 8; ++e) pair = umax_u16x2(pair, w[e] & 0x7fff7fffu);
+            const uint32_t top = max(pair & 0xffffu, pair >> 16);
+            uint32_t amax = top;
 #pragma unroll
-            for (int o = 1; o < 16; o <<= 1) amax = umax_xor(amax, o);
-            const uint32_t exp = fp4_row_exp(amax);
+            for (int o = 1; o < 8; o <<= 1) amax = umax_xor(amax, o);
+            const uint32_t exp = fp4_row_exp(amax << 16);
             const float unit = fp4_unit_inverse(exp);
-            float top = 0.f;
+            const uint32_t scale = fp4_group_scale(__uint_as_float(top << 16) * unit);
+            uint2 c;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                y[e] *= unit;
-                top = fmaxf(top, fabsf(y[e]));
+            for (int h = 0; h < 2; ++h) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    ffma2(y[2 * e], y[2 * e + 1], bf16_lo(w[4 * h + e]), bf16_hi(w[4 * h + e]), unit, unit, -0.f, -0.f);
+                (h ? c.y : c.x) = fp4_codes(y, scale);
             }
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            const uint32_t scale = fp4_group_scale(top);
-            const int head = 2 * k + (lane >> 4), chunk = lane & 15;
-            *reinterpret_cast<uint32_t *>(codes + head * kFp4RowCodes + chunk * 4) = fp4_codes(y, scale);
+            const int head = 4 * k + (lane >> 3), group = lane & 7;
+            *reinterpret_cast<uint2 *>(codes + head * kFp4RowCodes + group * 8) = c;
             const size_t row = row0 + (size_t)head * kBlock;
-            if (!(chunk & 1)) scales[row * kFp4Groups + (chunk >> 1)] = (uint8_t)scale;
-            if (chunk == 0) exps[row] = (uint8_t)exp;
+            scales[row * kFp4Groups + group] = (uint8_t)scale;
+            if (group == 0) exps[row] = (uint8_t)exp;
         }
     } else {
         // vector k of lane l: KV head 2k + l/16, dims 8 (l%16) .. 8 (l%16) + 7

@@ -49,7 +49,8 @@ struct Unit {
     WindowRows win;
 };
 
-template <bool kAppend, bool kWindow>
+// Unit idx of the batch; kPos: query positions per unit
+template <bool kAppend, bool kWindow, int kPos = kUnitPos>
 __device__ __forceinline__ Unit unit_at(const PrefillArgs &a, int idx, int qblocks) {
     Unit t;
     const int per_qb = a.num_seqs * kHkv;
@@ -68,11 +69,11 @@ __device__ __forceinline__ Unit unit_at(const PrefillArgs &a, int idx, int qbloc
         t.error = true;
         return t;
     }
-    if (qb * kUnitPos >= q_len) return t;
+    if (qb * kPos >= q_len) return t;
     t.run = true;
-    t.tok0 = c0 + qb * kUnitPos;
-    t.positions = min(kUnitPos, q_len - qb * kUnitPos);
-    t.pos0 = seq_len - q_len + qb * kUnitPos;
+    t.tok0 = c0 + qb * kPos;
+    t.positions = min(kPos, q_len - qb * kPos);
+    t.pos0 = seq_len - q_len + qb * kPos;
     t.seq_len = seq_len;
     t.kt0 = 0;
     t.ks = 0;
@@ -94,9 +95,9 @@ __device__ __forceinline__ Unit unit_at(const PrefillArgs &a, int idx, int qbloc
 }
 
 // Key tiles of unit idx (the unit_at rule; 0 for a unit without work, which sorts last).
-template <bool kAppend, bool kWindow>
+template <bool kAppend, bool kWindow, int kPos>
 __device__ __forceinline__ int plan_key(const PrefillArgs &a, int idx, int qblocks) {
-    const Unit t = unit_at<kAppend, kWindow>(a, idx, qblocks);
+    const Unit t = unit_at<kAppend, kWindow, kPos>(a, idx, qblocks);
     return t.run ? t.n_kt : 0;
 }
 
@@ -109,7 +110,7 @@ inline int plan_keys(const PrefillArgs &a) { return 2 * a.max_blocks_per_seq + 2
 // first (longest processing time first), written as order[rank] = unit.  Units with equal
 // keys take their ranks in whatever order the atomics resolve; every unit is computed by
 // one CTA on its own, so the outputs do not depend on that order.  nk = key buckets.
-template <bool kAppend, bool kWindow>
+template <bool kAppend, bool kWindow, int kPos = kUnitPos>
 __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const PrefillArgs a, int qblocks, int total,
                                                                        int nk) {
     __shared__ int hist[kPlanMaxKeys];
@@ -118,11 +119,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const Pre
     // The prefill may start its prologue now; it waits for this kernel before it reads the order.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the key of this thread's first unit is needed twice and kept
-    const int key0 = tid < total ? min(plan_key<kAppend, kWindow>(a, tid, qblocks), nk - 1) : 0;
+    const int key0 = tid < total ? min(plan_key<kAppend, kWindow, kPos>(a, tid, qblocks), nk - 1) : 0;
     for (int k = tid; k < nk; k += kPlanThreads) hist[k] = 0;
     __syncthreads();
     for (int idx = tid; idx < total; idx += kPlanThreads)
-        atomicAdd(&hist[idx == tid ? key0 : min(plan_key<kAppend, kWindow>(a, idx, qblocks), nk - 1)], 1);
+        atomicAdd(&hist[idx == tid ? key0 : min(plan_key<kAppend, kWindow, kPos>(a, idx, qblocks), nk - 1)], 1);
     __syncthreads();
     // hist[k] <- first rank of key k = number of units with more key tiles.  Thread t owns
     // the keys hi, hi - 1, ..., hi - per + 1 counted from the top.
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const Pre
     }
     __syncthreads();
     for (int idx = tid; idx < total; idx += kPlanThreads) {
-        const int rank = atomicAdd(&hist[idx == tid ? key0 : min(plan_key<kAppend, kWindow>(a, idx, qblocks), nk - 1)], 1);
+        const int rank = atomicAdd(&hist[idx == tid ? key0 : min(plan_key<kAppend, kWindow, kPos>(a, idx, qblocks), nk - 1)], 1);
         a.order[rank] = idx;
     }
     // Complete only after the kernel before this one on the stream (kv_append lets its
@@ -168,12 +169,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const Pre
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Index of this CTA's r-th unit in the snake order (or -1 past the end); kSplit: the cluster's one.
-template <bool kSplit>
+// Index of this CTA's r-th unit in the snake order (or -1 past the end); kSplit: the cluster's one; kCtas: of
+// so many CTAs that take a unit together.
+template <bool kSplit, int kCtas = 1>
 __device__ __forceinline__ int snake(const PrefillArgs &a, int r, int total) {
     if constexpr (kSplit) return r == 0 ? (int)(blockIdx.x / a.unit_ctas) : -1;
-    const int G = gridDim.x;
-    const int idx = r * G + ((r & 1) ? (G - 1 - (int)blockIdx.x) : (int)blockIdx.x);
+    const int G = gridDim.x / kCtas, cta = (int)blockIdx.x / kCtas;
+    const int idx = r * G + ((r & 1) ? (G - 1 - cta) : cta);
     return idx < total ? idx : -1;
 }
 

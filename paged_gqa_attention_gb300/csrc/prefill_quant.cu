@@ -53,6 +53,7 @@ constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
 static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * 128, "register split");
 constexpr uint32_t kTileBytes = 2 * kHalf;    // a 128 x 128 f16 tile
 constexpr int kStages = 2;                    // f16 tiles of K and of V
+constexpr int kPairPos = 2 * kUnitPos;        // query positions of a pair's unit
 constexpr int kParams = 4;                    // see TileParams
 
 // f16 operands and fp32 accumulation: formats 0 where idesc_bf16 has 1
@@ -64,20 +65,21 @@ constexpr uint32_t kIdescPV = idesc_f16(kRows, kD, true);
 
 // Code tiles on their way in, with their scales: a ring of slots, K and V in turn.  A K tile brings along
 // the V scales of the same rows (in 4 bits their exponents), from which sigma is chosen before the softmax
-// needs it; with two slots those of K are all the first one's.
-template <int kBits>
+// needs it.  A slot of a pair holds the codes of the 64 rows that this CTA converts, and the scales of all.
+template <int kBits, bool kPair>
 struct CodeRing;
-template <>
-struct CodeRing<8> {
-    static constexpr int kSlots = 2, kRow = kD;
-    uint8_t codes[kSlots][kKT * kRow];
+template <bool kPair>
+struct CodeRing<8, kPair> {
+    static constexpr int kSlots = kPair ? 3 : 2, kRow = kD, kRows = kPair ? 64 : kKT;
+    uint8_t codes[kSlots][kRows * kRow];
     float scale[kSlots][kKT];
-    float v_scale[1][kKT];
+    float v_scale[kPair ? kSlots : 1][kKT];   // (with two slots those of K are all the first one's)
+    __device__ __forceinline__ float *v_scales(int st) { return v_scale[kPair ? st : 0]; }
 };
-template <>
-struct CodeRing<4> {
-    static constexpr int kSlots = 3, kRow = kFp4RowCodes;
-    uint8_t codes[kSlots][kKT * kRow];
+template <bool kPair>
+struct CodeRing<4, kPair> {
+    static constexpr int kSlots = kPair ? 6 : 3, kRow = kFp4RowCodes, kRows = kPair ? 64 : kKT;
+    uint8_t codes[kSlots][kRows * kRow];
     uint8_t scale[kSlots][kKT * kFp4Groups];
     uint8_t exp[kSlots][kKT];
     uint8_t v_exp[kSlots][kKT];
@@ -92,17 +94,17 @@ struct TileParams {
     float grow;               // the factor that brings O to units of sigma (1, or sigma has just grown)
 };
 
-template <int kBits>
+template <int kBits, bool kPair>
 struct QuantSmem {
     uint8_t q[2][2][kHalf];          // [tile A|B][dims 0-63 | 64-127]
     uint8_t k[kStages][2][kHalf];
     uint8_t v[kStages][2][kHalf];
     union {
-        CodeRing<kBits> ring;
+        CodeRing<kBits, kPair> ring;
         float ml[2 * kRows][2];      // kSplit, at the end: running maximum and sum of every row
     };
     uint64_t q_full, q_ready, q_empty;
-    uint64_t c_full[CodeRing<kBits>::kSlots], c_empty[CodeRing<kBits>::kSlots];
+    uint64_t c_full[CodeRing<kBits, kPair>::kSlots], c_empty[CodeRing<kBits, kPair>::kSlots];
     uint64_t k_full[kStages], k_empty[kStages];
     uint64_t v_full[kStages], v_empty[kStages];
     uint64_t s_full[2], p_half[2][2], o_done[2];   // per query tile (P in two key halves)
@@ -111,13 +113,16 @@ struct QuantSmem {
     uint32_t tmem_base;
     int abort;
 };
-static_assert(offsetof(QuantSmem<8>, k) == sizeof(QuantSmem<8>::q) &&
-                  sizeof(QuantSmem<8>::q) + sizeof(QuantSmem<8>::k) == 2 * kRows * kD * sizeof(float),
+using SplitSmem = QuantSmem<8, false>;
+static_assert(offsetof(SplitSmem, k) == sizeof(SplitSmem::q) &&
+                  sizeof(SplitSmem::q) + sizeof(SplitSmem::k) == 2 * kRows * kD * sizeof(float),
               "split merge area");
 
-template <int kBits>
-constexpr size_t kSmemBytes = sizeof(QuantSmem<kBits>) + 1024;
-static_assert(kSmemBytes<8> <= 232448 && kSmemBytes<4> <= 232448, "shared memory");
+template <int kBits, bool kPair>
+constexpr size_t kSmemBytes = sizeof(QuantSmem<kBits, kPair>) + 1024;
+static_assert(kSmemBytes<8, false> <= 232448 && kSmemBytes<4, false> <= 232448 && kSmemBytes<8, true> <= 232448 &&
+                  kSmemBytes<4, true> <= 232448,
+              "shared memory");
 
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs)); }
 template <int kRegs>
@@ -141,6 +146,27 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
     return d;
 }
 
+// ---------------------------------------------------------------- a pair of CTAs
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+// Arrive on the barrier at this offset in both CTAs once every tcgen05 operation this thread issued has completed.
+__device__ __forceinline__ void umma_commit_both(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
+// Shared memory of this CTA -> of the peer, completing there.
+__device__ __forceinline__ void copy_to_peer(uint32_t cluster_dst, uint32_t src, uint32_t bytes, uint32_t cluster_bar) {
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(cluster_dst),
+                 "r"(src), "r"(bytes), "r"(cluster_bar)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint4 ld_shared_16(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
@@ -155,9 +181,17 @@ __device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t x, uint32_t
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
-// The work unit dealt as the r-th of this CTA.
-template <bool kPlanned, bool kSplit>
-__device__ __forceinline__ Unit unit_for(const PrefillArgs &a, int idx, int qblocks) {
+// The work unit dealt as the r-th of this CTA.  A pair's unit is 128 positions: one list of keys for both
+// CTAs, the first 64 positions rank 0's, the others (none: computed all the same, and not stored) rank 1's.
+template <bool kPlanned, bool kSplit, bool kPair>
+__device__ __forceinline__ Unit unit_for(const PrefillArgs &a, int idx, int qblocks, int rank) {
+    if constexpr (kPair) {
+        Unit t = unit_at<false, true, kPairPos>(a, kPlanned ? __ldg(a.order + idx) : idx, qblocks);
+        t.tok0 += rank * kUnitPos;
+        t.pos0 += rank * kUnitPos;
+        t.positions = min(kUnitPos, t.positions - rank * kUnitPos);
+        return t;
+    }
     if constexpr (kSplit) {
         // this CTA's run of the unit's key tiles (none: it only takes part in the merge)
         Unit t = unit_at<false, true>(a, idx, qblocks);
@@ -172,15 +206,17 @@ __device__ __forceinline__ Unit unit_for(const PrefillArgs &a, int idx, int qblo
 }
 
 // Fetch rows c0 .. c0 + 127 of the unit's key list (load_list_tile's rule in prefill.cu): codes in
-// boxes of 64 and 16 rows, their scales beside them a run at a time.  Block ids are reported by K.
-template <int kBits>
+// boxes of 64 and 16 rows, their scales beside them a run at a time.  Block ids are reported by K.  A CTA of
+// a pair converts rows first .. first + 63 and fetches the codes of no others.
+template <int kBits, bool kPair>
 __device__ __forceinline__ void load_codes(const PrefillArgs &a, const Unit &t, const int32_t *bt, int c0, bool is_k,
-                                           CodeRing<kBits> &ring, int st, uint32_t bar, const CUtensorMap *map64,
-                                           const CUtensorMap *map16) {
-    constexpr int kRow = CodeRing<kBits>::kRow;
+                                           CodeRing<kBits, kPair> &ring, int st, uint32_t bar, const CUtensorMap *map64,
+                                           const CUtensorMap *map16, int first) {
+    constexpr int kRow = CodeRing<kBits, kPair>::kRow;
     constexpr int kScales = kBits == 8 ? 4 : kFp4Groups + 1;
     const int rows = min(kKT, ((t.win.rows + 15) & ~15) - c0);
-    mbar_arrive_expect_tx(bar, (uint32_t)rows * (kRow + kScales + (is_k ? (kBits == 8 ? 4 : 1) : 0)));
+    const int coded = kPair ? max(0, min(64, rows - first)) : rows;
+    mbar_arrive_expect_tx(bar, (uint32_t)(coded * kRow + rows * (kScales + (is_k ? (kBits == 8 ? 4 : 1) : 0))));
     for (int r = 0; r < rows;) {
         const int p = t.win.position(c0 + r);
         int run = min(rows - r, kBlock - p % kBlock);
@@ -194,7 +230,7 @@ __device__ __forceinline__ void load_codes(const PrefillArgs &a, const Unit &t, 
         const size_t row = ((size_t)blk * kHkv + t.g) * kBlock + off;   // (off and run are multiples of 16)
         if constexpr (kBits == 8) {
             bulk_load(smem_u32(ring.scale[st] + r), static_cast<const float *>(is_k ? a.k_scale : a.v_scale) + row, run * 4, bar);
-            if (is_k) bulk_load(smem_u32(ring.v_scale[0] + r), static_cast<const float *>(a.v_scale) + row, run * 4, bar);
+            if (is_k) bulk_load(smem_u32(ring.v_scales(st) + r), static_cast<const float *>(a.v_scale) + row, run * 4, bar);
         } else {
             bulk_load(smem_u32(ring.scale[st] + r * kFp4Groups),
                       static_cast<const uint8_t *>(is_k ? a.k_scale : a.v_scale) + row * kFp4Groups, run * kFp4Groups, bar);
@@ -202,8 +238,10 @@ __device__ __forceinline__ void load_codes(const PrefillArgs &a, const Unit &t, 
             if (is_k) bulk_load(smem_u32(ring.v_exp[st] + r), a.v_exp + row, run, bar);
         }
         while (run > 0) {
-            const int n = run >= 64 ? 64 : 16;
-            tma_load_4d(smem_u32(ring.codes[st] + r * kRow), run >= 64 ? map64 : map16, bar, 0, t.g, off, blk);
+            const bool big = run >= 64 && (!kPair || (r & 63) == 0);
+            const int n = big ? 64 : 16;
+            if (!kPair || (r & 64) == first)
+                tma_load_4d(smem_u32(ring.codes[st] + (r - first) * kRow), big ? map64 : map16, bar, 0, t.g, off, blk);
             r += n;
             off += n;
             run -= n;
@@ -223,7 +261,8 @@ struct Piece<8> {
     float s;
 
     // lo, hi: addresses of the codes in the ring; row: of the tile
-    __device__ __forceinline__ void read(const CodeRing<8> &ring, int st, uint32_t lo, uint32_t hi, int row, int) {
+    template <bool kPair>
+    __device__ __forceinline__ void read(const CodeRing<8, kPair> &ring, int st, uint32_t lo, uint32_t hi, int row, int) {
         c[0] = ld_shared_16(lo);
         c[1] = ld_shared_16(hi);
         s = ring.scale[st][row];
@@ -250,7 +289,8 @@ struct Piece<4> {
     uint2 c[2];
     uint32_t s[2], exp;
 
-    __device__ __forceinline__ void read(const CodeRing<4> &ring, int st, uint32_t lo, uint32_t hi, int row, int chunk) {
+    template <bool kPair>
+    __device__ __forceinline__ void read(const CodeRing<4, kPair> &ring, int st, uint32_t lo, uint32_t hi, int row, int chunk) {
         c[0] = ld_shared_8(lo);
         c[1] = ld_shared_8(hi);
         const uint8_t *scale = ring.scale[st] + row * kFp4Groups + chunk;
@@ -281,7 +321,7 @@ struct Piece<4> {
 // 4 lane + 3 have.
 constexpr int kNone = -1000;
 __device__ __forceinline__ bool is_dead(const DeadRows &dead, int r) { return (r >= dead.lo && r < dead.hi) || r >= dead.tail; }
-__device__ __forceinline__ int top_exponent(int4 x, bool any_dead, const DeadRows &dead, int lane) {   // 8 bits: floats
+__device__ __forceinline__ int top_of(int4 x, bool any_dead, const DeadRows &dead, int lane) {   // 8 bits: floats
     if (any_dead) {
         if (is_dead(dead, 4 * lane)) x.x = 0;
         if (is_dead(dead, 4 * lane + 1)) x.y = 0;
@@ -289,14 +329,10 @@ __device__ __forceinline__ int top_exponent(int4 x, bool any_dead, const DeadRow
         if (is_dead(dead, 4 * lane + 3)) x.w = 0;
     }
     // as integers positive floats are in order, with infinities and NaN on top
-    int top = __reduce_max_sync(0xffffffffu, max(max(x.x, x.y), max(x.z, x.w)));
-    if (top >= 0x7f800000) {
-        const auto finite = [](int v) { return v < 0x7f800000 ? v : 0; };
-        top = __reduce_max_sync(0xffffffffu, max(max(finite(x.x), finite(x.y)), max(finite(x.z), finite(x.w))));
-    }
-    return top > 0 ? min(max((top >> 23) + 1 - 127, -126), 126) : kNone;
+    const auto finite = [](int v) { return v < 0x7f800000 ? v : 0; };
+    return max(max(finite(x.x), finite(x.y)), max(finite(x.z), finite(x.w)));
 }
-__device__ __forceinline__ int top_exponent(uint32_t x, bool any_dead, const DeadRows &dead, int lane) {   // 4 bits: bytes
+__device__ __forceinline__ int top_of(uint32_t x, bool any_dead, const DeadRows &dead, int lane) {   // 4 bits: bytes
     if (any_dead) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -304,14 +340,18 @@ __device__ __forceinline__ int top_exponent(uint32_t x, bool any_dead, const Dea
     }
     x &= ~__vcmpeq4(x, 0xffffffffu);         // without NaN
     const uint32_t y = __vmaxu4(x, x >> 16);
-    const int top = __reduce_max_sync(0xffffffffu, (int)(max(y & 0xffu, y >> 8 & 0xffu)));
-    return top ? min(max(top - 127, -126), 126) : kNone;
+    return (int)max(y & 0xffu, y >> 8 & 0xffu);
+}
+template <int kBits>
+__device__ __forceinline__ int exponent_of(int top) {   // of the largest of all lanes
+    const int n = kBits == 8 ? (top >> 23) + 1 - 127 : top - 127;
+    return top > 0 ? min(max(n, -126), 126) : kNone;
 }
 
 // 2^n as a float for n in -126 .. 127 (clamped).
 __device__ __forceinline__ float exp2_int(int n) { return __uint_as_float((uint32_t)(min(max(n, -126), 127) + 127) << 23); }
 
-// This warp's share of a code tile into an f16 tile: rounds of 8 rows, `first`, first + 6 and first + 12 of the 16, the
+// This warp's share of rows row0 .. end - 1 of a code tile into an f16 tile: rounds of 8 rows, `first`, first + 6 ..., the
 // next round's read ahead.  Dead rows are zeros: their codes and scales may be anything, and 0 * NaN is not 0.
 // Lanes 8q .. 8q + 3 have row q of the 8, lanes 8q + 4 .. 8q + 7 row q ^ 5, so that with the swizzles below neither
 // a load (whose rows must differ in bit 2) nor a store (in bit 0) meets a bank twice, and no lane has to exchange its
@@ -320,23 +360,24 @@ __device__ __forceinline__ float exp2_int(int n) { return __uint_as_float((uint3
 // unrolled, once for K and once for V, warps waited for instructions more than for anything else (2.3 of 10
 // warp-cycles an instruction).  A round takes a warp some 265 clk on its own: 48 half-rate instructions and their
 // latencies.
-template <int kBits>
-__device__ __forceinline__ void convert_tile(const CodeRing<kBits> &ring, int st, uint32_t dst, float unit, bool any_dead,
-                                             const DeadRows &dead, int first, int lane) {
-    constexpr int kRow = CodeRing<kBits>::kRow, kStep = 8 * kConvertWarps;
+template <int kBits, bool kPair>
+__device__ __forceinline__ void convert_tile(const CodeRing<kBits, kPair> &ring, int st, uint32_t dst, float unit, bool any_dead,
+                                             const DeadRows &dead, int row0, int end, int first, int lane) {
+    constexpr int kRow = CodeRing<kBits, kPair>::kRow, kStep = 8 * kConvertWarps;
     const int c = lane & 3;
-    int row = 8 * first + ((lane >> 3) ^ ((lane & 4) ? 5 : 0));
+    int row = row0 + 8 * first + ((lane >> 3) ^ ((lane & 4) ? 5 : 0));
     // 8 bits: 128-byte rows, 128-byte swizzle (sw128); 4 bits: 64-byte rows, 64-byte swizzle, in which 16-byte
     // piece p of row r is at p ^ (r / 2 % 4).  Either repeats every 8 rows; 64 dims on flip one bit of the address.
-    uint32_t src = smem_u32(ring.codes[st]) + (kBits == 8 ? sw128(row, c)
-                                                          : row * kRow + (((c >> 1) ^ ((row >> 1) & 3)) << 4) + ((c & 1) << 3));
+    const int from = kPair ? row - row0 : row;   // row of the slot
+    uint32_t src = smem_u32(ring.codes[st]) +
+                   (kBits == 8 ? sw128(from, c) : from * kRow + (((c >> 1) ^ ((from >> 1) & 3)) << 4) + ((c & 1) << 3));
     constexpr uint32_t kFlip = kBits == 8 ? 64 : 32;
     uint32_t at = dst + sw128(row, 2 * c);
     Piece<kBits> x;
     x.read(ring, st, src, src ^ kFlip, row, c);
 #pragma unroll 1
     while (true) {
-        const bool more = row + kStep < kKT;
+        const bool more = row + kStep < end;
         Piece<kBits> next = x;
         src += kStep * kRow;
         if (more) next.read(ring, st, src, src ^ kFlip, row + kStep, c);
@@ -372,20 +413,24 @@ __device__ __forceinline__ void convert_q(uint8_t *q, int w, int lane) {
     }
 }
 
-template <int kBits, bool kPlanned, bool kSplit>
+template <int kBits, bool kPlanned, bool kSplit, bool kPair>
 __global__ void __launch_bounds__(kThreads, 1)
 prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
                      const __grid_constant__ CUtensorMap v_map, const __grid_constant__ CUtensorMap k16_map,
                      const __grid_constant__ CUtensorMap v16_map, const PrefillArgs a) {
-    using Smem = QuantSmem<kBits>;
-    constexpr int kRing = CodeRing<kBits>::kSlots;
+    using Smem = QuantSmem<kBits, kPair>;
+    constexpr int kRing = CodeRing<kBits, kPair>::kSlots;
     extern __shared__ uint8_t smem_raw[];
     Smem &sm = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     volatile int *abort_flag = &sm.abort;
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
-    const int qblocks = (a.max_q_len + kUnitPos - 1) / kUnitPos;
+    static_assert(!(kPair && kSplit), "forms");
+    constexpr int kPos = kPair ? kPairPos : kUnitPos;
+    constexpr int kCtas = kPair ? 2 : 1;
+    const int qblocks = (a.max_q_len + kPos - 1) / kPos;
     const int total = a.num_seqs * kHkv * qblocks;
+    const int rank = kPair ? (int)cluster_rank() : 0;
 
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&sm.q_full), 1);
@@ -396,10 +441,10 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             mbar_init(smem_u32(&sm.c_empty[i]), kConvertWarps);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&sm.k_full[i]), kConvertWarps);
-            mbar_init(smem_u32(&sm.k_empty[i]), 1);
-            mbar_init(smem_u32(&sm.v_full[i]), kConvertWarps);
-            mbar_init(smem_u32(&sm.v_empty[i]), 1);
+            mbar_init(smem_u32(&sm.k_full[i]), kPair ? 1 : kConvertWarps);   // pair: its producer, and the peer's copies
+            mbar_init(smem_u32(&sm.k_empty[i]), kCtas);   // both CTAs' products are done with it
+            mbar_init(smem_u32(&sm.v_full[i]), kPair ? 1 : kConvertWarps);
+            mbar_init(smem_u32(&sm.v_empty[i]), kCtas);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&sm.s_full[x]), 1);
@@ -416,7 +461,9 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         tmem_relinquish();
     }
     tc_fence_before();
-    __syncthreads();
+    // (a pair: both CTAs' barriers exist before either reaches for the other's)
+    if constexpr (kPair) cluster_sync_all();
+    else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
     const auto wait_all = [&](uint64_t *bar, uint32_t parity) -> bool {
@@ -438,24 +485,46 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             // the cache and q may be written by the kernel just before this one on the stream
             asm volatile("griddepcontrol.wait;" ::: "memory");
             int units = 0, it = 0;               // units, code tiles (K and V) issued
+            int done = 0;                        // code tiles converted, as far as this warp has looked
             bool ok = true;
+            // Waits for the tiles before `upto`.  A pair's half of one then goes to the peer, from where the other comes.
+            const auto converted = [&](int upto) -> bool {
+                for (; done < upto; ++done) {
+                    if (!wait_all(&sm.c_empty[done % kRing], (done / kRing) & 1)) return false;
+                    if constexpr (kPair) {
+                        const int ks = (done >> 1) % kStages;
+                        const uint32_t half = smem_u32(done & 1 ? sm.v[ks] : sm.k[ks]) + (uint32_t)(64 * rank * 128);
+                        const uint32_t full = smem_u32(done & 1 ? &sm.v_full[ks] : &sm.k_full[ks]);
+                        if (leader) {
+                            const uint32_t dst = peer_addr(half, rank ^ 1), bar = peer_addr(full, rank ^ 1);
+                            copy_to_peer(dst, half, kHalf / 2, bar);
+                            copy_to_peer(dst + kHalf, half + kHalf, kHalf / 2, bar);
+                            mbar_arrive_expect_tx(full, kHalf);
+                        }
+                        __syncwarp();
+                    }
+                }
+                return true;
+            };
             for (int r = 0; ok; ++r) {
-                const int idx = snake<kSplit>(a, r, total);
+                const int idx = snake<kSplit, kCtas>(a, r, total);
                 if (idx < 0) break;
-                const Unit t = unit_for<kPlanned, kSplit>(a, idx, qblocks);
-                if (leader && t.error) record_error(a.err, kErrDevice | kErrQLen);
+                const Unit t = unit_for<kPlanned, kSplit, kPair>(a, idx, qblocks, rank);
+                if (leader && rank == 0 && t.error) record_error(a.err, kErrDevice | kErrQLen);
                 if (!t.run) continue;
                 const int32_t *bt = a.block_table + (size_t)t.s * a.max_blocks_per_seq;
                 for (int i = 0; i < 2 * t.n_kt; ++i, ++it) {
                     const int st = it % kRing;
-                    if (it >= kRing && !(ok = wait_all(&sm.c_empty[st], ((it / kRing) - 1) & 1))) break;
+                    if (it >= kRing && !(ok = converted(it - kRing + 1))) break;
                     const bool is_k = !(i & 1);
                     if (leader)
-                        load_codes<kBits>(a, t, bt, (t.kt0 + (i >> 1)) * kKT, is_k, sm.ring, st, smem_u32(&sm.c_full[st]),
-                                          is_k ? &k_map : &v_map, is_k ? &k16_map : &v16_map);
+                        load_codes<kBits, kPair>(a, t, bt, (t.kt0 + (i >> 1)) * kKT, is_k, sm.ring, st,
+                                                 smem_u32(&sm.c_full[st]), is_k ? &k_map : &v_map,
+                                                 is_k ? &k16_map : &v16_map, 64 * rank);
                     __syncwarp();
                     if (i == 0) {   // Q behind the first K tile, which does not wait for the unit before
-                        if (units >= 1 && !(ok = wait_all(&sm.q_empty, (units - 1) & 1))) {
+                        // (a pair's last tiles first, without which the unit before does not end)
+                        if (units >= 1 && !(ok = (!kPair || converted(it)) && wait_all(&sm.q_empty, (units - 1) & 1))) {
                             ++it;
                             break;
                         }
@@ -472,6 +541,10 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     }
                 }
             }
+            if (kPair && ok) ok = converted(it);
+            // Copies to the peer have landed when the peer's products are done, which the end waits for.  Where something
+            // gave up, those of the last moment are given a hundred times what they take.
+            if (kPair && !ok) __nanosleep(100000);
             // Drain: no TMA copy may still be landing when the CTA exits.  In the normal path every load has
             // been consumed and these waits return at once.
             if (units > 0) mbar_wait(smem_u32(&sm.q_full), (units - 1) & 1);
@@ -480,6 +553,10 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             // ---------------------------------------------------------------- MMA issuer (as in prefill.cu)
             const bool leader = elect_one();
             if constexpr (kPlanned) asm volatile("griddepcontrol.wait;" ::: "memory");
+            const auto commit_tile = [&](uint64_t *bar) {   // a tile of K or V has been read
+                if constexpr (kPair) umma_commit_both(smem_u32(bar));
+                else umma_commit(smem_u32(bar));
+            };
             const uint64_t qd0 = sdesc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
             const uint64_t kd0 = sdesc_sw128(smem_u32(sm.k[0][0]), 16, 1024);
             const uint64_t vd0 = sdesc_sw128(smem_u32(sm.v[0][0]), (uint32_t)kHalf, 1024);
@@ -524,15 +601,15 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     for (int kk = kKT / 32; kk < kKT / 16; ++kk)
                         umma_ts_c<true>(tmem + col_o(x), pa + kk * 8, vb + (uint64_t)(kk * 128), kIdescPV);
                     umma_commit(smem_u32(&sm.o_done[x]));
-                    if (x == 1) umma_commit(smem_u32(&sm.v_empty[vs]));   // B is the V tile's last reader
+                    if (x == 1) commit_tile(&sm.v_empty[vs]);   // B is the V tile's last reader
                 }
                 __syncwarp();
                 return true;
             };
             for (int r = 0; ok; ++r) {
-                const int idx = snake<kSplit>(a, r, total);
+                const int idx = snake<kSplit, kCtas>(a, r, total);
                 if (idx < 0) break;
-                const Unit t = unit_for<kPlanned, kSplit>(a, idx, qblocks);
+                const Unit t = unit_for<kPlanned, kSplit, kPair>(a, idx, qblocks, rank);
                 if (!t.run) continue;
                 if (!(ok = wait_all(&sm.q_ready, units & 1))) break;
                 for (int j = 0; j < t.n_kt; ++j, ++it) {
@@ -543,7 +620,7 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     if (pend_it >= 0 && !(ok = issue_pv(1, pend_it, pend_j))) break;   // O_B, tile j-1
                     issue_s(1, ks);                                        // S_B(j)
                     if (leader) {
-                        umma_commit(smem_u32(&sm.k_empty[ks]));
+                        commit_tile(&sm.k_empty[ks]);
                         if (j == t.n_kt - 1) umma_commit(smem_u32(&sm.q_empty));
                     }
                     __syncwarp();
@@ -570,9 +647,9 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             int units = 0, it = 0;               // units, code tiles (K and V)
             bool ok = true;
             for (int r = 0; ok; ++r) {
-                const int idx = snake<kSplit>(a, r, total);
+                const int idx = snake<kSplit, kCtas>(a, r, total);
                 if (idx < 0) break;
-                const Unit t = unit_for<kPlanned, kSplit>(a, idx, qblocks);
+                const Unit t = unit_for<kPlanned, kSplit, kPair>(a, idx, qblocks, rank);
                 if (!t.run) continue;
                 int sigma = kNone;               // exponent of sigma
                 DeadRows dead(t.win, t.kt0 * kKT);
@@ -586,16 +663,20 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     if (is_k) {
                         dead = DeadRows(t.win, (t.kt0 + (i >> 1)) * kKT);
                         any_dead = dead.any();
-                        int top, v_top;
+                        int top, v_top;              // (read and reduced side by side)
                         if constexpr (kBits == 8) {
-                            top = top_exponent(*reinterpret_cast<const int4 *>(sm.ring.scale[st] + 4 * lane), any_dead, dead, lane);
-                            v_top = top_exponent(*reinterpret_cast<const int4 *>(sm.ring.v_scale[0] + 4 * lane), any_dead, dead,
-                                                 lane);
+                            const int4 s = *reinterpret_cast<const int4 *>(sm.ring.scale[st] + 4 * lane);
+                            const int4 v = *reinterpret_cast<const int4 *>(sm.ring.v_scales(st) + 4 * lane);
+                            top = top_of(s, any_dead, dead, lane);
+                            v_top = top_of(v, any_dead, dead, lane);
                         } else {
-                            top = top_exponent(*reinterpret_cast<const uint32_t *>(sm.ring.exp[st] + 4 * lane), any_dead, dead, lane);
-                            v_top = top_exponent(*reinterpret_cast<const uint32_t *>(sm.ring.v_exp[st] + 4 * lane), any_dead, dead,
-                                                 lane);
+                            const uint32_t s = *reinterpret_cast<const uint32_t *>(sm.ring.exp[st] + 4 * lane);
+                            const uint32_t v = *reinterpret_cast<const uint32_t *>(sm.ring.v_exp[st] + 4 * lane);
+                            top = top_of(s, any_dead, dead, lane);
+                            v_top = top_of(v, any_dead, dead, lane);
                         }
+                        top = exponent_of<kBits>(__reduce_max_sync(0xffffffffu, top));
+                        v_top = exponent_of<kBits>(__reduce_max_sync(0xffffffffu, v_top));
                         if (v_top != kNone && (sigma == kNone || v_top > sigma + kHeadroom)) {
                             if (sigma != kNone) grow = exp2_int(sigma - v_top);
                             sigma = v_top;
@@ -609,14 +690,16 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                         break;
                     if (is_k && w == 0 && lane == 0)
                         sm.params[kt % kParams] = TileParams{exp2_int(unit), exp2_int(sigma == kNone ? 0 : sigma), grow};
-                    // (V starts four warps on, so that over both no warp has more than 6 of the 32 rounds)
-                    convert_tile<kBits>(sm.ring, st, smem_u32(is_k ? sm.k[ks] : sm.v[ks]), exp2_int(-unit), any_dead, dead,
-                                        is_k ? w : w < 2 ? w + 4 : w - 2, lane);
-                    fence_proxy_async_smem();    // generic writes -> visible to the MMA's reads
+                    const uint32_t dst = smem_u32(is_k ? sm.k[ks] : sm.v[ks]);
+                    // (V starts four warps on, so that over both no warp has more rounds than it must)
+                    const int first = is_k ? w : w < 2 ? w + 4 : w - 2;
+                    const int row0 = 64 * rank, end = kPair ? row0 + 64 : kKT;
+                    convert_tile<kBits, kPair>(sm.ring, st, dst, exp2_int(-unit), any_dead, dead, row0, end, first, lane);
+                    fence_proxy_async_smem();    // generic writes -> visible to the MMA's reads, and the copies'
                     __syncwarp();
                     if (lane == 0) {
-                        mbar_arrive(smem_u32(is_k ? &sm.k_full[ks] : &sm.v_full[ks]));
                         mbar_arrive(smem_u32(&sm.c_empty[st]));
+                        if constexpr (!kPair) mbar_arrive(smem_u32(is_k ? &sm.k_full[ks] : &sm.v_full[ks]));
                     }
                     if (i == 0) {                // Q, which has been on its way meanwhile
                         if (!(ok = wait_all(&sm.q_full, units & 1))) { ++it; break; }
@@ -650,15 +733,15 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         [[maybe_unused]] bool fetched = false;
         next.run = false;
         for (int r = 0; ok; ++r) {
-            const int idx = snake<kSplit>(a, r, total);
+            const int idx = snake<kSplit, kCtas>(a, r, total);
             if (idx < 0) break;
             const Unit t = [&]() -> Unit {
                 if constexpr (!kSplit) {
                     const bool have = fetched;
                     fetched = false;
-                    return have ? next : unit_for<kPlanned, kSplit>(a, idx, qblocks);
+                    return have ? next : unit_for<kPlanned, kSplit, kPair>(a, idx, qblocks, rank);
                 } else {
-                    return unit_for<kPlanned, kSplit>(a, idx, qblocks);
+                    return unit_for<kPlanned, kSplit, kPair>(a, idx, qblocks, rank);
                 }
             }();
             if (!t.run) continue;
@@ -776,9 +859,9 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
 
             // ------------------------------------------------------------ epilogue
             if constexpr (!kSplit) {
-                const int idx_next = snake<kSplit>(a, r + 1, total);
+                const int idx_next = snake<kSplit, kCtas>(a, r + 1, total);
                 if (idx_next >= 0) {
-                    next = unit_for<kPlanned, kSplit>(a, idx_next, qblocks);
+                    next = unit_for<kPlanned, kSplit, kPair>(a, idx_next, qblocks, rank);
                     fetched = true;
                 }
             }
@@ -857,6 +940,9 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
 
     // ---------------------------------------------------------------- teardown
     __syncthreads();
+    // (a pair: neither exits while the other may write into its memory or arrive on its barriers; every wait above
+    // is bounded, so both come here)
+    if constexpr (kPair) cluster_sync_all();
     if (warp == kMmaWarp) {
         __syncwarp();
         tc_fence_after();
@@ -864,45 +950,49 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
     }
 }
 
-template <int kBits, bool kPlanned, bool kSplit>
+template <int kBits, bool kPlanned, bool kSplit, bool kPair>
 cudaError_t launch_mode(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
                         const CUtensorMap &v_map, const CUtensorMap &k16_map, const CUtensorMap &v16_map, int num_sms,
                         cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const auto kernel = prefill_quant_kernel<kBits, kPlanned, kSplit>;
+    const auto kernel = prefill_quant_kernel<kBits, kPlanned, kSplit, kPair>;
     static std::atomic<bool> configured[64] = {};
     if (dev < 0 || dev >= 64 || !configured[dev].load()) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<kBits>);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<kBits, kPair>);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(true);
     }
-    const long long qblocks = (a.max_q_len + kUnitPos - 1) / kUnitPos;
+    constexpr int kPos = kPair ? kPairPos : kUnitPos;
+    const long long qblocks = (a.max_q_len + kPos - 1) / kPos;
     const long long units = (long long)a.num_seqs * kHkv * qblocks;
     // Programmatic dependent launch: the producer waits (griddepcontrol.wait) before its first load, so the
     // launch and prologue may overlap the previous kernel on the stream.
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;   // kSplit only
-    attr[1].val.clusterDim.x = kSplit ? (unsigned)a.unit_ctas : 1u;
+    attr[1].id = cudaLaunchAttributeClusterDimension;   // kSplit and kPair only
+    attr[1].val.clusterDim.x = kSplit ? (unsigned)a.unit_ctas : kPair ? 2u : 1u;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = kSplit ? 2 : 1;
+    cfg.numAttrs = 1;
     if constexpr (kPlanned) {
         cfg.gridDim = dim3(1);
         cfg.blockDim = dim3(kPlanThreads);
         cfg.dynamicSmemBytes = 0;
-        e = cudaLaunchKernelEx(&cfg, prefill_plan_kernel<false, true>, a, (int)qblocks, (int)units, plan_keys(a));
+        e = cudaLaunchKernelEx(&cfg, prefill_plan_kernel<false, true, kPos>, a, (int)qblocks, (int)units, plan_keys(a));
         if (e != cudaSuccess) return e;
     }
-    cfg.gridDim = dim3(kSplit ? (unsigned)(units * a.unit_ctas) : (unsigned)std::min<long long>(units, num_sms));
+    cfg.numAttrs = kSplit || kPair ? 2 : 1;
+    cfg.gridDim = dim3(kSplit  ? (unsigned)(units * a.unit_ctas)
+                       : kPair ? 2 * (unsigned)std::min<long long>(units, num_sms / 2)
+                               : (unsigned)std::min<long long>(units, num_sms));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmemBytes<kBits>;
+    cfg.dynamicSmemBytes = kSmemBytes<kBits, kPair>;
     return cudaLaunchKernelEx(&cfg, kernel, q_map, k_map, v_map, k16_map, v16_map, a);
 }
 
@@ -915,11 +1005,11 @@ cudaError_t split_clusters(int (&out)[9]) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    const auto kernel = prefill_quant_kernel<kBits, false, true>;
+    const auto kernel = prefill_quant_kernel<kBits, false, true, false>;
     for (int c = 2; c <= 8; ++c) {
         int n = known[dev][c].load();
         if (n == 0) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<kBits>);
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<kBits, false>);
             if (e != cudaSuccess) return e;
             cudaLaunchAttribute attr[1];
             attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -929,7 +1019,7 @@ cudaError_t split_clusters(int (&out)[9]) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3((unsigned)c);
             cfg.blockDim = dim3(kThreads);
-            cfg.dynamicSmemBytes = kSmemBytes<kBits>;
+            cfg.dynamicSmemBytes = kSmemBytes<kBits, false>;
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
@@ -957,18 +1047,31 @@ cudaError_t launch_bits(PrefillArgs a, long long tiles, const CUtensorMap &q_map
         if (e != cudaSuccess) return e;
         a.unit_ctas = unit_ctas_for(units, tiles, std::min(a.max_q_len, kUnitPos), num_sms, clusters);
     }
+    const auto refused = [](cudaError_t e) {   // a cluster that this device will not run
+        return e == cudaErrorLaunchOutOfResources || e == cudaErrorInvalidClusterSize || e == cudaErrorNotSupported ||
+               e == cudaErrorCooperativeLaunchTooLarge;
+    };
     if (a.unit_ctas > 1) {
         const cudaError_t e =
-            launch_mode<kBits, false, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
-        if (e != cudaErrorLaunchOutOfResources && e != cudaErrorInvalidClusterSize && e != cudaErrorNotSupported &&
-            e != cudaErrorCooperativeLaunchTooLarge)
-            return e;
-        cudaGetLastError();   // the clusters were refused: one CTA a unit instead
+            launch_mode<kBits, false, true, false>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
+        if (!refused(e)) return e;
+        cudaGetLastError();   // one CTA a unit, or a pair, instead
         a.unit_ctas = 1;
     }
-    if (a.order && units > num_sms)   // (units that all start at once need no order)
-        return launch_mode<kBits, true, false>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
-    return launch_mode<kBits, false, false>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
+    // Pairs where a sequence may have more than one CTA's positions
+    if (a.max_q_len > kUnitPos) {
+        const long long pairs = (long long)a.num_seqs * kHkv * ((a.max_q_len + kPairPos - 1) / kPairPos);
+        // (units that all start at once need no order)
+        const cudaError_t e =
+            a.order && pairs > num_sms / 2
+                ? launch_mode<kBits, true, false, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream)
+                : launch_mode<kBits, false, false, true>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
+        if (!refused(e)) return e;
+        cudaGetLastError();
+    }
+    if (a.order && units > num_sms)
+        return launch_mode<kBits, true, false, false>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
+    return launch_mode<kBits, false, false, false>(a, q_map, k_map, v_map, k16_map, v16_map, num_sms, stream);
 }
 
 }  // namespace

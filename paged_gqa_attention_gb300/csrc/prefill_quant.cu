@@ -8,7 +8,7 @@
 // tile comes into being.
 //
 // Codes are not operands: their row scales run along the keys, and a 4-bit row has a scale for every 16
-// dimensions besides.  So the products run in f16, and six warps turn code tiles into f16 tiles in
+// dimensions besides.  So the products run in f16, and converter warps turn code tiles into f16 tiles in
 // shared memory while the tensor cores work on the tiles before:
 //   K' = code * s / 2^E,      E the exponent of the tile's largest scale: a magnitude of at most 448 (2688
 //                             in 4 bits); the scores are multiplied by 2^E together with the softmax scale
@@ -16,17 +16,31 @@
 //                             when a tile's V' could leave f16; O is then rescaled, as it is for the
 //                             running maximum, and the epilogue multiplies by sigma
 // with one rounding to f16 (8 bits: the scale is split into a sum of two f16, so that code * scale is rounded
-// once, to 2^-12 of the value at most half a step; 4 bits: exact).  Values 2^-14 of the largest and less lose bits one by one.
+// once, by 2^-11 of the value at most; 4 bits: exact).  Values 2^-14 of the largest and less lose bits one by one.
 // Q is converted to f16 in place (|q| < 65504, as for the decode over these caches), P is f16.
-// A code tile is converted once per 64 positions: 2 x 16384 values, three instructions a pair, against
-// 4 x 128 x 128 x 256 operations of products; what the conversion costs is shared-memory traffic, 48 KiB
-// an operand tile next to the products' reads.
+//
+// What bounds it is not the products (4 x 128 x 128 x 256 operations a tile, 2048 clk at the tensor cores' rate)
+// but what else a tile asks for: the softmax of 256 rows and the conversion of 2 x 16384 values share the
+// issue slots, and a converter's visit to a tile (waits, scales, fence, arrival) costs as much as its
+// arithmetic.  Hence pairs of CTAs (clusters of two, a sequence's adjacent 64 positions each) walk one list of keys:
+// each converts 64 rows of every tile and copies them to the other's shared memory (bulk copies that
+// complete on the barrier the other's products wait for), so that a row is converted once for 128 positions.
+// Measured, 8192 new tokens after 8192 in 8 bits: 2012 us with the conversion unrolled for K and V apart, 1570
+// in one rolled loop, 1555 with six converters, 1455 in pairs whose converters made the copies (400 clk a
+// visit), 1239 with the copies in the producer, 1224 with the loads of V and the copies in a warp of their own and the
+// tiles' exponents in the producer (1.35 PFLOP/s; 4 chunks of up to 1024 in 4 bits with a window of 2048, which
+// the producer's 2400 clk of issuing loads a tile had held at 132 us: 120).  One CTA alone walking its list, 1555
+// and 129, is left where a sequence has 64 positions at most (there is nobody to share with) and where few
+// units share the GPU, whose keys are split instead.  Products over the pair (tcgen05 with two CTAs' operands) halve
+// the same conversion without copies, but every step then waits for the peer: 1382.
 //
 // CTA = 16 warps, persistent, one per SM:
 //   warps 0-3, 4-7    softmax + epilogue of query tiles A and B (thread = row = TMEM lane)
-//   warps 8-11, 14, 15  converters
-//   warp 12           TMA producer: Q, and the ring of code tiles in the order K(0) V(0) K(1) V(1) ...
+//   warps 8-11, 15    converters; without a pair 14 too
+//   warp 12           TMA producer: Q, and the ring of code tiles in the order K(0) V(0) K(1) V(1) ...; in a pair of
+//                     K alone, and of what the tiles are scaled by
 //   warp 13           TMEM allocator and tcgen05.mma issuer
+//   warp 14           in a pair: V's code tiles, and the copies of converted halves to the peer
 // Every wait is bounded; on expiry the CTA records PA_ERR_TIMEOUT, unwinds, waits (bounded) for its own
 // copies and MMAs, frees tensor memory and exits.
 #include <atomic>
@@ -44,17 +58,21 @@
 namespace pa {
 namespace {
 
-constexpr int kConvertWarps = 6;              // 8-11, 14, 15
+template <bool kPair>
+constexpr int kConvertWarps = kPair ? 5 : 6;  // 8-11, 15 and without a pair 14
 constexpr int kProducerWarp = 12;
 constexpr int kMmaWarp = 13;
+constexpr int kPairWarp = 14;                 // a pair's V loads, and copies to the peer
 constexpr int kThreads = 16 * 32;
-// registers a thread, warpgroup by warpgroup: together the 512 x 128 that the block is launched with
-constexpr int kSoftmaxRegs = 168, kOtherRegs = 88;
+// registers a thread, warpgroup by warpgroup: together the 512 x 128 that the block is launched with (8192 tokens
+// after 8192 with 168 and 88 1300 us, 160 and 96 1224, 152 and 104 1314)
+constexpr int kSoftmaxRegs = 160, kOtherRegs = 96;
 static_assert(2 * kSoftmaxRegs + 2 * kOtherRegs == 4 * 128, "register split");
 constexpr uint32_t kTileBytes = 2 * kHalf;    // a 128 x 128 f16 tile
 constexpr int kStages = 2;                    // f16 tiles of K and of V
 constexpr int kPairPos = 2 * kUnitPos;        // query positions of a pair's unit
-constexpr int kParams = 4;                    // see TileParams
+constexpr int kParams = 8;                    // see TileParams
+constexpr int kReady = 4;                     // see scaled in QuantSmem
 
 // f16 operands and fp32 accumulation: formats 0 where idesc_bf16 has 1
 constexpr uint32_t idesc_f16(int m, int n, bool b_mn_major) {
@@ -85,13 +103,14 @@ struct CodeRing<4, kPair> {
     uint8_t v_exp[kSlots][kKT];
 };
 
-// What the softmax needs of key tile `it`, in entry it % 4.  Entry it is written when K(it) is converted,
-// which needs the slot of K(it - 2), so S_B(it - 2); that was issued after O_B += P_B(it - 3) V, so both
-// query tiles' softmax have read entry it - 3 by then: 4 entries are enough.
+// What key tile `it` is scaled by, in entry it % 8.  An entry is written when the tile's K is in the ring, at the earliest
+// (six slots) when K(it - 3) is converted, which needs the slot of K(it - 5), so S_B(it - 5); that was issued after
+// O_B += P_B(it - 6) V, so both query tiles' softmax have read entry it - 6 by then: 7 entries are enough.
 struct TileParams {
     float k_unit;             // 2^E
     float sigma;
     float grow;               // the factor that brings O to units of sigma (1, or sigma has just grown)
+    int unit, sigma_exp;      // E, and sigma's exponent
 };
 
 template <int kBits, bool kPair>
@@ -107,6 +126,10 @@ struct QuantSmem {
     uint64_t c_full[CodeRing<kBits, kPair>::kSlots], c_empty[CodeRing<kBits, kPair>::kSlots];
     uint64_t k_full[kStages], k_empty[kStages];
     uint64_t v_full[kStages], v_empty[kStages];
+    uint64_t half_done[2][kStages];                // a pair: this CTA's half of K, V is converted
+    // a pair: tile it's entry is written, on it % 4 (that of it + 4 waits, at the earliest, for the conversion of
+    // K(it + 1), so nobody waits for it any more)
+    uint64_t scaled[kReady];
     uint64_t s_full[2], p_half[2][2], o_done[2];   // per query tile (P in two key halves)
     uint64_t mma_idle;
     TileParams params[kParams];
@@ -351,8 +374,42 @@ __device__ __forceinline__ int exponent_of(int top) {   // of the largest of all
 // 2^n as a float for n in -126 .. 127 (clamped).
 __device__ __forceinline__ float exp2_int(int n) { return __uint_as_float((uint32_t)(min(max(n, -126), 127) + 127) << 23); }
 
-// This warp's share of rows row0 .. end - 1 of a code tile into an f16 tile: rounds of 8 rows, `first`, first + 6 ..., the
-// next round's read ahead.  Dead rows are zeros: their codes and scales may be anything, and 0 * NaN is not 0.
+// What the tile whose K is in slot st is scaled by (a warp's work); sigma: its exponent after the tile before, kNone at first.
+template <int kBits, bool kPair>
+__device__ __forceinline__ TileParams scale_tile(CodeRing<kBits, kPair> &ring, int st, const DeadRows &dead, int &sigma, int lane) {
+    // V' stays below 65504: codes reach 448 (2688 with their group's scale), so the tile's largest scale
+    // may be this many powers of two above sigma
+    constexpr int kHeadroom = kBits == 8 ? 7 : 4;
+    const bool any_dead = dead.any();
+    int top, v_top;                              // (read and reduced side by side)
+    if constexpr (kBits == 8) {
+        const int4 s = *reinterpret_cast<const int4 *>(ring.scale[st] + 4 * lane);
+        const int4 v = *reinterpret_cast<const int4 *>(ring.v_scales(st) + 4 * lane);
+        top = top_of(s, any_dead, dead, lane);
+        v_top = top_of(v, any_dead, dead, lane);
+    } else {
+        const uint32_t s = *reinterpret_cast<const uint32_t *>(ring.exp[st] + 4 * lane);
+        const uint32_t v = *reinterpret_cast<const uint32_t *>(ring.v_exp[st] + 4 * lane);
+        top = top_of(s, any_dead, dead, lane);
+        v_top = top_of(v, any_dead, dead, lane);
+    }
+    top = exponent_of<kBits>(__reduce_max_sync(0xffffffffu, top));
+    v_top = exponent_of<kBits>(__reduce_max_sync(0xffffffffu, v_top));
+    TileParams p;
+    p.grow = 1.f;
+    if (v_top != kNone && (sigma == kNone || v_top > sigma + kHeadroom)) {
+        if (sigma != kNone) p.grow = exp2_int(sigma - v_top);
+        sigma = v_top;
+    }
+    p.unit = top == kNone ? 0 : top;
+    p.sigma_exp = sigma == kNone ? 0 : sigma;
+    p.k_unit = exp2_int(p.unit);
+    p.sigma = exp2_int(p.sigma_exp);
+    return p;
+}
+
+// This warp's share of rows row0 .. end - 1 of a code tile into an f16 tile: rounds of 8 rows, `first` and every 6th (a
+// pair: 5th) from there on, the next round's read ahead.  Dead rows are zeros: their codes and scales may be anything, and 0 * NaN is not 0.
 // Lanes 8q .. 8q + 3 have row q of the 8, lanes 8q + 4 .. 8q + 7 row q ^ 5, so that with the swizzles below neither
 // a load (whose rows must differ in bit 2) nor a store (in bit 0) meets a bank twice, and no lane has to exchange its
 // pieces first.
@@ -363,7 +420,7 @@ __device__ __forceinline__ float exp2_int(int n) { return __uint_as_float((uint3
 template <int kBits, bool kPair>
 __device__ __forceinline__ void convert_tile(const CodeRing<kBits, kPair> &ring, int st, uint32_t dst, float unit, bool any_dead,
                                              const DeadRows &dead, int row0, int end, int first, int lane) {
-    constexpr int kRow = CodeRing<kBits, kPair>::kRow, kStep = 8 * kConvertWarps;
+    constexpr int kRow = CodeRing<kBits, kPair>::kRow, kStep = 8 * kConvertWarps<kPair>;
     const int c = lane & 3;
     int row = row0 + 8 * first + ((lane >> 3) ^ ((lane & 4) ? 5 : 0));
     // 8 bits: 128-byte rows, 128-byte swizzle (sw128); 4 bits: 64-byte rows, 64-byte swizzle, in which 16-byte
@@ -400,10 +457,11 @@ __device__ __forceinline__ void convert_tile(const CodeRing<kBits, kPair> &ring,
 }
 
 // Q in place, bf16 -> f16: this warp's share.
+template <int kWarps>
 __device__ __forceinline__ void convert_q(uint8_t *q, int w, int lane) {
     uint4 *p = reinterpret_cast<uint4 *>(q) + lane;
 #pragma unroll 2
-    for (int i = w; i < 4 * kHalf / 16 / 32; i += kConvertWarps) {
+    for (int i = w; i < 4 * kHalf / 16 / 32; i += kWarps) {
         uint4 x = p[i * 32];
         x.x = bf16x2_to_f16x2(x.x);
         x.y = bf16x2_to_f16x2(x.y);
@@ -428,23 +486,26 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
     static_assert(!(kPair && kSplit), "forms");
     constexpr int kPos = kPair ? kPairPos : kUnitPos;
     constexpr int kCtas = kPair ? 2 : 1;
+    constexpr int kConv = kConvertWarps<kPair>;
     const int qblocks = (a.max_q_len + kPos - 1) / kPos;
     const int total = a.num_seqs * kHkv * qblocks;
     const int rank = kPair ? (int)cluster_rank() : 0;
 
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(&sm.q_full), 1);
-        mbar_init(smem_u32(&sm.q_ready), kConvertWarps);
+        mbar_init(smem_u32(&sm.q_ready), kConv);
         mbar_init(smem_u32(&sm.q_empty), 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(smem_u32(&sm.c_full[i]), 1);
-            mbar_init(smem_u32(&sm.c_empty[i]), kConvertWarps);
+            mbar_init(smem_u32(&sm.c_empty[i]), kConv);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(smem_u32(&sm.k_full[i]), kPair ? 1 : kConvertWarps);   // pair: its producer, and the peer's copies
+            mbar_init(smem_u32(&sm.k_full[i]), kPair ? 1 : kConv);   // pair: its pair warp, and the peer's copies
             mbar_init(smem_u32(&sm.k_empty[i]), kCtas);   // both CTAs' products are done with it
-            mbar_init(smem_u32(&sm.v_full[i]), kPair ? 1 : kConvertWarps);
+            mbar_init(smem_u32(&sm.v_full[i]), kPair ? 1 : kConv);
             mbar_init(smem_u32(&sm.v_empty[i]), kCtas);
+            mbar_init(smem_u32(&sm.half_done[0][i]), kConv);
+            mbar_init(smem_u32(&sm.half_done[1][i]), kConv);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(smem_u32(&sm.s_full[x]), 1);
@@ -452,6 +513,7 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             mbar_init(smem_u32(&sm.p_half[x][1]), 4);
             mbar_init(smem_u32(&sm.o_done[x]), 1);
         }
+        for (int i = 0; i < kReady; ++i) mbar_init(smem_u32(&sm.scaled[i]), 1);
         mbar_init(smem_u32(&sm.mma_idle), 1);
         sm.abort = 0;
         fence_barrier_init();
@@ -485,27 +547,7 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
             // the cache and q may be written by the kernel just before this one on the stream
             asm volatile("griddepcontrol.wait;" ::: "memory");
             int units = 0, it = 0;               // units, code tiles (K and V) issued
-            int done = 0;                        // code tiles converted, as far as this warp has looked
             bool ok = true;
-            // Waits for the tiles before `upto`.  A pair's half of one then goes to the peer, from where the other comes.
-            const auto converted = [&](int upto) -> bool {
-                for (; done < upto; ++done) {
-                    if (!wait_all(&sm.c_empty[done % kRing], (done / kRing) & 1)) return false;
-                    if constexpr (kPair) {
-                        const int ks = (done >> 1) % kStages;
-                        const uint32_t half = smem_u32(done & 1 ? sm.v[ks] : sm.k[ks]) + (uint32_t)(64 * rank * 128);
-                        const uint32_t full = smem_u32(done & 1 ? &sm.v_full[ks] : &sm.k_full[ks]);
-                        if (leader) {
-                            const uint32_t dst = peer_addr(half, rank ^ 1), bar = peer_addr(full, rank ^ 1);
-                            copy_to_peer(dst, half, kHalf / 2, bar);
-                            copy_to_peer(dst + kHalf, half + kHalf, kHalf / 2, bar);
-                            mbar_arrive_expect_tx(full, kHalf);
-                        }
-                        __syncwarp();
-                    }
-                }
-                return true;
-            };
             for (int r = 0; ok; ++r) {
                 const int idx = snake<kSplit, kCtas>(a, r, total);
                 if (idx < 0) break;
@@ -513,42 +555,112 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 if (leader && rank == 0 && t.error) record_error(a.err, kErrDevice | kErrQLen);
                 if (!t.run) continue;
                 const int32_t *bt = a.block_table + (size_t)t.s * a.max_blocks_per_seq;
-                for (int i = 0; i < 2 * t.n_kt; ++i, ++it) {
+                // Q behind the first K tile, which does not wait for the unit before
+                const auto load_q = [&]() -> bool {
+                    if (units >= 1 && !wait_all(&sm.q_empty, (units - 1) & 1)) return false;
+                    if (leader) {
+                        const uint32_t qbar = smem_u32(&sm.q_full);
+                        mbar_arrive_expect_tx(qbar, 2 * kTileBytes);
+                        for (int x = 0; x < 2; ++x) {
+                            tma_load_3d(smem_u32(sm.q[x][0]), &q_map, qbar, 0, t.g * kGroup, t.tok0 + x * kTilePos);
+                            tma_load_3d(smem_u32(sm.q[x][1]), &q_map, qbar, 64, t.g * kGroup, t.tok0 + x * kTilePos);
+                        }
+                    }
+                    __syncwarp();
+                    ++units;
+                    return true;
+                };
+                // code tile i of the unit, `it` of the CTA
+                const auto load_tile = [&](int i) -> bool {
                     const int st = it % kRing;
-                    if (it >= kRing && !(ok = converted(it - kRing + 1))) break;
+                    if (it >= kRing && !wait_all(&sm.c_empty[st], ((it / kRing) - 1) & 1)) return false;
                     const bool is_k = !(i & 1);
                     if (leader)
                         load_codes<kBits, kPair>(a, t, bt, (t.kt0 + (i >> 1)) * kKT, is_k, sm.ring, st,
                                                  smem_u32(&sm.c_full[st]), is_k ? &k_map : &v_map,
                                                  is_k ? &k16_map : &v16_map, 64 * rank);
                     __syncwarp();
-                    if (i == 0) {   // Q behind the first K tile, which does not wait for the unit before
-                        // (a pair's last tiles first, without which the unit before does not end)
-                        if (units >= 1 && !(ok = (!kPair || converted(it)) && wait_all(&sm.q_empty, (units - 1) & 1))) {
-                            ++it;
-                            break;
-                        }
+                    return true;
+                };
+                if constexpr (kPair) {
+                    // K alone, and what its tiles are scaled by: the tile's entry, before the next one's load
+                    int sigma = kNone;
+                    if (!(ok = load_tile(0))) break;
+                    for (int j = 0; j < t.n_kt; ++j) {
+                        const int kt = it >> 1, st = it % kRing;
+                        if (!(ok = wait_all(&sm.c_full[st], (it / kRing) & 1))) { it += 2; break; }
+                        const TileParams p = scale_tile(sm.ring, st, DeadRows(t.win, j * kKT), sigma, lane);
                         if (leader) {
-                            const uint32_t qbar = smem_u32(&sm.q_full);
-                            mbar_arrive_expect_tx(qbar, 2 * kTileBytes);
-                            for (int x = 0; x < 2; ++x) {
-                                tma_load_3d(smem_u32(sm.q[x][0]), &q_map, qbar, 0, t.g * kGroup, t.tok0 + x * kTilePos);
-                                tma_load_3d(smem_u32(sm.q[x][1]), &q_map, qbar, 64, t.g * kGroup, t.tok0 + x * kTilePos);
-                            }
+                            sm.params[kt % kParams] = p;
+                            mbar_arrive(smem_u32(&sm.scaled[kt % kReady]));
                         }
                         __syncwarp();
-                        ++units;
+                        it += 2;
+                        if (j == 0 && !(ok = load_q())) break;
+                        if (j + 1 < t.n_kt && !(ok = load_tile(2 * (j + 1)))) break;
+                    }
+                } else {
+                    for (int i = 0; i < 2 * t.n_kt; ++i) {
+                        if (!(ok = load_tile(i))) break;
+                        ++it;
+                        if (i == 0 && !(ok = load_q())) break;
                     }
                 }
             }
-            if (kPair && ok) ok = converted(it);
-            // Copies to the peer have landed when the peer's products are done, which the end waits for.  Where something
-            // gave up, those of the last moment are given a hundred times what they take.
-            if (kPair && !ok) __nanosleep(100000);
             // Drain: no TMA copy may still be landing when the CTA exits.  In the normal path every load has
             // been consumed and these waits return at once.
             if (units > 0) mbar_wait(smem_u32(&sm.q_full), (units - 1) & 1);
-            for (int i = max(0, it - kRing); i < it; ++i) mbar_wait(smem_u32(&sm.c_full[i % kRing]), (i / kRing) & 1);
+            for (int i = max(0, it - kRing); i < it; ++i)
+                if (!kPair || !(i & 1)) mbar_wait(smem_u32(&sm.c_full[i % kRing]), (i / kRing) & 1);
+        } else if (kPair && warp == kPairWarp) {
+            // ---------------------------------------------------------------- V loads, and a pair's exchange
+            const bool leader = elect_one();
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            int kt = 0;                          // key tiles
+            bool ok = true;
+            // This CTA's half of key tile k to the peer, from where the other comes
+            const auto send = [&](int k) -> bool {
+                const int ks = k % kStages;
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    if (!wait_all(&sm.half_done[v][ks], (k / kStages) & 1)) return false;
+                    if (leader) {
+                        const uint32_t half = smem_u32(v ? sm.v[ks] : sm.k[ks]) + (uint32_t)(64 * rank * 128);
+                        const uint32_t full = smem_u32(v ? &sm.v_full[ks] : &sm.k_full[ks]);
+                        const uint32_t dst = peer_addr(half, rank ^ 1), bar = peer_addr(full, rank ^ 1);
+                        copy_to_peer(dst, half, kHalf / 2, bar);
+                        copy_to_peer(dst + kHalf, half + kHalf, kHalf / 2, bar);
+                        mbar_arrive_expect_tx(full, kHalf);
+                    }
+                    __syncwarp();
+                }
+                return true;
+            };
+            for (int r = 0; ok; ++r) {
+                const int idx = snake<kSplit, kCtas>(a, r, total);
+                if (idx < 0) break;
+                const Unit t = unit_for<kPlanned, kSplit, kPair>(a, idx, qblocks, rank);
+                if (!t.run) continue;
+                const int32_t *bt = a.block_table + (size_t)t.s * a.max_blocks_per_seq;
+                for (int j = 0; j < t.n_kt; ++j, ++kt) {
+                    const int it = 2 * kt + 1, st = it % kRing;
+                    if (it >= kRing && !(ok = wait_all(&sm.c_empty[st], ((it / kRing) - 1) & 1))) break;
+                    if (leader)
+                        load_codes<kBits, kPair>(a, t, bt, j * kKT, false, sm.ring, st, smem_u32(&sm.c_full[st]), &v_map,
+                                                 &v16_map, 64 * rank);
+                    __syncwarp();
+                    if (kt > 0 && !(ok = send(kt - 1))) {
+                        ++kt;
+                        break;
+                    }
+                }
+            }
+            if (ok && kt > 0) ok = send(kt - 1);
+            // Copies to the peer have landed when the peer's products are done, which the end waits for.  Where something
+            // gave up, those of the last moment are given a hundred times what they take.
+            if (!ok) __nanosleep(100000);
+            for (int i = max(0, 2 * kt - kRing); i < 2 * kt; ++i)
+                if (i & 1) mbar_wait(smem_u32(&sm.c_full[i % kRing]), (i / kRing) & 1);
         } else if (warp == kMmaWarp) {
             // ---------------------------------------------------------------- MMA issuer (as in prefill.cu)
             const bool leader = elect_one();
@@ -640,10 +752,7 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
         } else {
             // ---------------------------------------------------------------- converters
             if constexpr (kPlanned) asm volatile("griddepcontrol.wait;" ::: "memory");
-            const int w = warp < kProducerWarp ? warp - kSoftmaxWarps : warp - kSoftmaxWarps - 2;
-            // V' stays below 65504: codes reach 448 (2688 with their group's scale), so the tile's largest scale
-            // may be this many powers of two above sigma
-            constexpr int kHeadroom = kBits == 8 ? 7 : 4;
+            const int w = warp < kProducerWarp ? warp - kSoftmaxWarps : warp - (16 - kConv);
             int units = 0, it = 0;               // units, code tiles (K and V)
             bool ok = true;
             for (int r = 0; ok; ++r) {
@@ -654,56 +763,40 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 int sigma = kNone;               // exponent of sigma
                 DeadRows dead(t.win, t.kt0 * kKT);
                 bool any_dead = false;
+                TileParams par = {};
                 for (int i = 0; i < 2 * t.n_kt; ++i, ++it) {     // K(0), V(0), K(1), ...
                     const bool is_k = !(i & 1);
                     const int st = it % kRing, kt = it >> 1, ks = kt % kStages;
                     if (!(ok = wait_all(&sm.c_full[st], (it / kRing) & 1))) break;
-                    int unit;                    // exponent of what the tile is divided by
-                    float grow = 1.f;
                     if (is_k) {
                         dead = DeadRows(t.win, (t.kt0 + (i >> 1)) * kKT);
                         any_dead = dead.any();
-                        int top, v_top;              // (read and reduced side by side)
-                        if constexpr (kBits == 8) {
-                            const int4 s = *reinterpret_cast<const int4 *>(sm.ring.scale[st] + 4 * lane);
-                            const int4 v = *reinterpret_cast<const int4 *>(sm.ring.v_scales(st) + 4 * lane);
-                            top = top_of(s, any_dead, dead, lane);
-                            v_top = top_of(v, any_dead, dead, lane);
+                        if constexpr (kPair) {
+                            if (!(ok = wait_all(&sm.scaled[kt % kReady], (kt / kReady) & 1))) break;
+                            par = sm.params[kt % kParams];
                         } else {
-                            const uint32_t s = *reinterpret_cast<const uint32_t *>(sm.ring.exp[st] + 4 * lane);
-                            const uint32_t v = *reinterpret_cast<const uint32_t *>(sm.ring.v_exp[st] + 4 * lane);
-                            top = top_of(s, any_dead, dead, lane);
-                            v_top = top_of(v, any_dead, dead, lane);
+                            par = scale_tile(sm.ring, st, dead, sigma, lane);
                         }
-                        top = exponent_of<kBits>(__reduce_max_sync(0xffffffffu, top));
-                        v_top = exponent_of<kBits>(__reduce_max_sync(0xffffffffu, v_top));
-                        if (v_top != kNone && (sigma == kNone || v_top > sigma + kHeadroom)) {
-                            if (sigma != kNone) grow = exp2_int(sigma - v_top);
-                            sigma = v_top;
-                        }
-                        unit = top == kNone ? 0 : top;
-                    } else {
-                        unit = sigma == kNone ? 0 : sigma;
                     }
+                    const int unit = is_k ? par.unit : par.sigma_exp;   // exponent of what the tile is divided by
                     if (kt >= kStages &&
                         !(ok = wait_all(is_k ? &sm.k_empty[ks] : &sm.v_empty[ks], ((kt / kStages) - 1) & 1)))
                         break;
-                    if (is_k && w == 0 && lane == 0)
-                        sm.params[kt % kParams] = TileParams{exp2_int(unit), exp2_int(sigma == kNone ? 0 : sigma), grow};
+                    if (!kPair && is_k && w == 0 && lane == 0) sm.params[kt % kParams] = par;
                     const uint32_t dst = smem_u32(is_k ? sm.k[ks] : sm.v[ks]);
-                    // (V starts four warps on, so that over both no warp has more rounds than it must)
-                    const int first = is_k ? w : w < 2 ? w + 4 : w - 2;
+                    // (V starts two warps on, so that over both the rounds are nearly even)
+                    const int first = is_k ? w : w < 2 ? w + kConv - 2 : w - 2;
                     const int row0 = 64 * rank, end = kPair ? row0 + 64 : kKT;
                     convert_tile<kBits, kPair>(sm.ring, st, dst, exp2_int(-unit), any_dead, dead, row0, end, first, lane);
                     fence_proxy_async_smem();    // generic writes -> visible to the MMA's reads, and the copies'
                     __syncwarp();
                     if (lane == 0) {
                         mbar_arrive(smem_u32(&sm.c_empty[st]));
-                        if constexpr (!kPair) mbar_arrive(smem_u32(is_k ? &sm.k_full[ks] : &sm.v_full[ks]));
+                        mbar_arrive(smem_u32(kPair ? &sm.half_done[!is_k][ks] : is_k ? &sm.k_full[ks] : &sm.v_full[ks]));
                     }
                     if (i == 0) {                // Q, which has been on its way meanwhile
                         if (!(ok = wait_all(&sm.q_full, units & 1))) { ++it; break; }
-                        convert_q(sm.q[0][0], w, lane);
+                        convert_q<kConv>(sm.q[0][0], w, lane);
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(smem_u32(&sm.q_ready));

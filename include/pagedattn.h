@@ -358,8 +358,10 @@ pa_status paged_attn_decode_window_fp8(pa_shape shape, void *out, float *lse, co
  * a window as long as the context (INT32_MAX will do) and no sinks is plain causal attention.  Arguments,
  * workspace, rules and errors as for paged_attn_prefill_window (out 32-byte aligned), k_codes .. v_scale as for
  * paged_attn_decode_fp8, |q| < 65504.  Products run in f16: a value of the cache enters as the f16 nearest to code *
- * scale, relative to a power of two taken from the scales that the same 64 tokens' keys have; rows whose scale
- * is 2^-14 of the largest of them or less lose bits one by one.
+ * scale divided by a power of two, for K one at or above the largest scale among 128 keys that are worked on
+ * together, for V the largest among the keys so far, and quotients under 2^-14 lose bits one by one.  A work unit is 64
+ * consecutive new tokens of a sequence, 128 where max_q_len is above 64: a NaN or infinity in a V row that some
+ * of a unit's tokens see and others do not may reach the outputs of all of them.
  */
 pa_status paged_attn_prefill_fp8(pa_shape shape, void *out, float *lse, const void *q,
                                  const void *k_codes, const void *v_codes, const float *k_scale,
@@ -408,8 +410,8 @@ pa_status paged_rope_append_fp4(pa_shape shape, float rope_theta, const int32_t 
 /*
  * paged_attn_decode_fp4, paged_attn_prefill_fp4: paged_attn_decode_window and paged_attn_prefill_window over the
  * 4-bit cache (an INT32_MAX window: all of the context).  Arguments, workspace, rules and errors as for those;
- * |q| < 65504; split_tokens is a multiple of 256.  In the prefill V rows whose exponent is 14 or more
- * below the largest of the same 64 tokens' keys lose bits one by one.
+ * |q| < 65504; split_tokens is a multiple of 256.  The prefill's values and units are those of
+ * paged_attn_prefill_fp8, with 2^(e - 127) for the scale.
  */
 pa_status paged_attn_decode_fp4(pa_shape shape, void *out, float *lse, const void *q,
                                 const void *k_codes, const void *v_codes, const void *k_scale,

@@ -439,7 +439,7 @@ pa_status paged_attn_prefill_fp4(pa_shape shape, void *out, float *lse, const vo
  *   cu_rows int32 [num_seqs + 1], first int32 [num_seqs]; total_rows >= cu_rows[num_seqs]: rows behind the
  *   last sequence are left as they are.  Table entries of blocks without such a row are not used.
  *   A row whose block id is outside the pool, whose position is outside the table or whose cu_rows are inconsistent
- *   comes back as NaN and records PA_ERR_DEVICE.  Outputs must not overlap the cache.
+ *   comes back as NaN and records PA_ERR_DEVICE.  Outputs are 32-byte aligned and must not overlap the cache.
  */
 pa_status paged_kv_read_fp8(pa_shape shape, void *k_out, void *v_out, const void *k_codes,
                             const void *v_codes, const float *k_scale, const float *v_scale,

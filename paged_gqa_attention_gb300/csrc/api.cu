@@ -738,7 +738,7 @@ static pa_status kv_read_impl(int bits, pa_shape shape, void *k_out, void *v_out
     if (total_rows == 0) return PA_OK;
     if (!k_out || !v_out || !k_codes || !v_codes || !low.ok(bits) || !block_table || !cu_rows || !first)
         return PA_ERR_INVALID_ARG;
-    if (!aligned16(k_out) || !aligned16(v_out) || !aligned16(k_codes) || !aligned16(v_codes) ||
+    if (!aligned32(k_out) || !aligned32(v_out) || !aligned16(k_codes) || !aligned16(v_codes) ||
         !aligned4(block_table) || !aligned4(cu_rows) || !aligned4(first))
         return PA_ERR_INVALID_ARG;
     ReadArgs a = {};

@@ -8,9 +8,10 @@
 //
 // The pass reads 132 or 73 bytes a row and writes 256: it is bound by HBM.  A warp takes 4 consecutive
 // rows of K or of V; a lane 16 codes (16 or 8 bytes) at a time, whose 32 bytes of output make the warp's
-// stores whole lines, and every load of the 4 rows goes out before the first is used.  The CTA's
-// 8 warps take 16 rows of K and of V, so that the scales, which lie 256 slots a head, come in
-// whole sectors.
+// stores whole lines, and every load of the 4 rows goes out before the first is used.  The scales of the
+// 4 x 8 (row, head) pairs come a pair a lane and are handed round (a load for every 16 codes kept the load
+// queues full).  The CTA's 8 warps take 16 rows of K and of V, so that the scales, which lie 256 slots a
+// head, come in whole sectors.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -57,6 +58,7 @@ __device__ __forceinline__ long long place_of(const ReadArgs &a, int t, bool rep
 template <int kBits>
 __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const ReadArgs a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ float group_scale[kBits == 4 ? kWarps : 1][32][kFp4Groups];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const bool is_v = warp & 1;
     const long long t0 = (long long)blockIdx.x * kRowsPerCta + (warp >> 1) * kRowsPerWarp;
@@ -77,27 +79,46 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const ReadArgs a) 
     const void *scales = is_v ? a.v_scale : a.k_scale;
     const uint8_t *exps = is_v ? a.v_exp : a.k_exp;
     uint4 c[kRowsPerWarp][2];
-    float s[kRowsPerWarp][2];
 #pragma unroll
     for (int r = 0; r < kRowsPerWarp; ++r) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             c[r][u] = make_uint4(0u, 0u, 0u, 0u);
-            s[r][u] = __int_as_float(0x7fc00000);
             if (place[r] < 0) continue;
-            const int chunk = u * 32 + lane, head = chunk >> 3;
-            const size_t row = ((size_t)(place[r] / kBlock) * kHkv + head) * kBlock + (size_t)(place[r] % kBlock);
+            const int chunk = u * 32 + lane;
             if constexpr (kBits == 8) {
                 c[r][u] = *(reinterpret_cast<const uint4 *>(codes + place[r] * (kHkv * kD)) + chunk);
-                s[r][u] = static_cast<const float *>(scales)[row];
             } else {
                 const uint2 w = *(reinterpret_cast<const uint2 *>(codes + place[r] * (kHkv * kFp4RowCodes)) + chunk);
                 c[r][u].x = w.x;
                 c[r][u].y = w.y;
-                s[r][u] = __uint_as_float(static_cast<const uint8_t *>(scales)[row * kFp4Groups + (chunk & 7)] |
-                                          (uint32_t)exps[row] << 8);
             }
         }
+    }
+    // what scales KV head l % 8 of row l / 8, in lane l: one load (4 bits: two) for the warp's 32
+    const long long at = __shfl_sync(0xffffffffu, mine, lane >> 3);
+    const size_t row = at < 0 ? 0 : ((size_t)(at / kBlock) * kHkv + (lane & 7)) * kBlock + (size_t)(at % kBlock);
+    float head_scale = __int_as_float(0x7fc00000);   // (of a row that is nowhere)
+    if constexpr (kBits == 8) {
+        if (at >= 0) head_scale = static_cast<const float *>(scales)[row];
+    } else {
+        uint2 w = make_uint2(0u, 0u);
+        if (at >= 0) {
+            w = static_cast<const uint2 *>(scales)[row];
+            head_scale = fp4_unit(exps[row]);
+        }
+        uint32_t h[4];
+        e4m3x4_to_f16x2x2(w.x, h[0], h[1]);
+        e4m3x4_to_f16x2x2(w.y, h[2], h[3]);
+        float4 f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 lo = __half22float2(*reinterpret_cast<const __half2 *>(&h[2 * i]));
+            const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&h[2 * i + 1]));
+            f[i] = make_float4(lo.x * head_scale, lo.y * head_scale, hi.x * head_scale, hi.y * head_scale);
+            *reinterpret_cast<float4 *>(&group_scale[warp][lane][4 * i]) = f[i];
+        }
+        __syncwarp();
     }
     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(is_v ? a.v_out : a.k_out);
 #pragma unroll
@@ -106,12 +127,14 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const ReadArgs a) 
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             uint32_t h[8];   // f16 pairs of the codes
-            float scale = s[r][u];
+            const int from = r * kHkv + u * 4 + (lane >> 3);   // the lane of this chunk's row and head
+            float scale;
             if constexpr (kBits == 8) {
                 e4m3x4_to_f16x2x2(c[r][u].x, h[0], h[1]);
                 e4m3x4_to_f16x2x2(c[r][u].y, h[2], h[3]);
                 e4m3x4_to_f16x2x2(c[r][u].z, h[4], h[5]);
                 e4m3x4_to_f16x2x2(c[r][u].w, h[6], h[7]);
+                scale = __shfl_sync(0xffffffffu, head_scale, from);
             } else {
                 uint32_t lo[4], hi[4];
                 e2m1x8_to_f16x2x4(c[r][u].x, lo);
@@ -121,8 +144,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const ReadArgs a) 
                     h[e] = lo[e];
                     h[4 + e] = hi[e];
                 }
-                const uint32_t w = __float_as_uint(scale);
-                if (place[r] >= 0) scale = e4m3_value(w & 0xffu) * fp4_unit(w >> 8);
+                scale = group_scale[warp][from][lane & 7];
             }
             uint32_t w[8];
 #pragma unroll
@@ -130,9 +152,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv_read_kernel(const ReadArgs a) 
                 const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[e]));
                 w[e] = pack_bf16x2(f.x * scale, f.y * scale);
             }
-            uint4 *d = reinterpret_cast<uint4 *>(out + (t0 + r) * (kHkv * kD) + (u * 32 + lane) * 16);
-            d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            st_global_32b(out + (t0 + r) * (kHkv * kD) + (u * 32 + lane) * 16, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
         }
     }
 }

@@ -72,7 +72,8 @@ def test_read_refuses(lib, bits):
     a, fn = read_args(p, bits), lib.paged_kv_read_fp8 if bits == 8 else lib.paged_kv_read_fp4
     wide = ("k_out", "v_out", "kp", "vp", "ks", "vs", "ws") + (("ke", "ve") if bits == 4 else ())
     for bad in (nothing_and_misaligned(p, wide, ("bt", "cu", "first"))
-                + [dict(seqs=-1), dict(rows=-1), dict(seqs=0), dict(w=0), dict(nb=0), dict(w=1 << 23), dict(ws_bytes=255)]):
+                + [dict(seqs=-1), dict(rows=-1), dict(seqs=0), dict(w=0), dict(nb=0), dict(w=1 << 23), dict(ws_bytes=255),
+                   dict(k_out=p(20, 16)), dict(v_out=p(20, 16))]):
         assert call(fn, a, bad) == 1, bad
     for shape in OTHER_SHAPES:
         assert call(fn, a, dict(shape=shape)) == 2

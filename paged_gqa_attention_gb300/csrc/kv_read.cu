@@ -12,6 +12,8 @@
 // 4 x 8 (row, head) pairs come a pair a lane and are handed round (a load for every 16 codes kept the load
 // queues full).  The CTA's 8 warps take 16 rows of K and of V, so that the scales, which lie 256 slots a
 // head, come in whole sectors.
+// Measured: 94311 tokens from 8 bits 86.8 us (585 MB: 6.75 TB/s, the copy rate), 25078 from 4 bits 20.3 us
+// (6.5 TB/s); with a scale load for every 16 codes 100 and 30.9, with 16-byte stores 93 and 29.
 #include <cuda_fp16.h>
 
 #include "common.cuh"

@@ -681,7 +681,7 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 const uint32_t sd = tmem + col_s(x);
                 if (leader) {
                     umma_ss_c<false>(sd, qa, kb, kIdescQK);
-    #pragma unroll
+#pragma unroll
                     for (int kk = 1; kk < kD / 16; ++kk) {
                         const uint64_t off = (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);
                         umma_ss_c<true>(sd, qa + off, kb + off, kIdescQK);
@@ -699,7 +699,7 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                 tc_fence_after();
                 if (leader) {
                     umma_ts(tmem + col_o(x), pa, vb, kIdescPV, pj > 0 ? 1u : 0u);
-    #pragma unroll
+#pragma unroll
                     for (int kk = 1; kk < kKT / 32; ++kk)
                         umma_ts_c<true>(tmem + col_o(x), pa + kk * 8, vb + (uint64_t)(kk * 128), kIdescPV);
                 }
@@ -709,7 +709,7 @@ prefill_quant_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_con
                     tc_fence_after();
                 }
                 if (leader) {
-    #pragma unroll
+#pragma unroll
                     for (int kk = kKT / 32; kk < kKT / 16; ++kk)
                         umma_ts_c<true>(tmem + col_o(x), pa + kk * 8, vb + (uint64_t)(kk * 128), kIdescPV);
                     umma_commit(smem_u32(&sm.o_done[x]));

@@ -43,7 +43,7 @@
  *
  * Streams.  `stream` is a cudaStream_t (NULL = the legacy default stream).  Calls
  * are asynchronous and stream-ordered; PA_OK means "validated and launched".  The
- * decode, prefill, projection, rotated-append and read-back kernels are launched as programmatic dependents
+ * decode, prefill, projection, rotated-append, 4-bit append and read-back kernels are launched as programmatic dependents
  * of the kernel before them on the stream: they may start before it has finished, and wait for
  * it before touching q, x, k_new, v_new, positions, gains, the pools, out, k_out, v_out or lse.  block_table,
  * seq_lens, cu_q_lens, cu_rows and first may be read earlier, so a kernel that writes them immediately before a

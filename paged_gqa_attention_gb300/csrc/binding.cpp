@@ -14,6 +14,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -114,7 +115,7 @@ const int32_t *ints(const at::Tensor *t) { return static_cast<const int32_t *>(t
 // `out` as given (None: a new tensor of that shape); false when it is not a plain one of it.
 bool output(PyObject *o, at::IntArrayRef shape, int dev, at::Tensor *out) {
     if (o == Py_None) {
-        *out = at::empty(shape, at::TensorOptions().dtype(at::kBFloat16).device(at::kCUDA, dev));
+        *out = at::Tensor(at::detail::empty_cuda(shape, at::kBFloat16, c10::Device(c10::kCUDA, (c10::DeviceIndex)dev), std::nullopt));
         return true;
     }
     const at::Tensor *t = tensor(o);

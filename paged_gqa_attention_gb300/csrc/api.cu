@@ -804,8 +804,8 @@ pa_status paged_rope_append_fp8(pa_shape shape, float rope_theta, const int32_t 
                                 size_t workspace_bytes, void *stream) {
     return rope_append_impl(shape, rope_theta, positions, axes, pair_axis, q_norm_weight, k_norm_weight, norm_eps,
                             q_out, q, q_stride, k_new, k_stride, v_new, v_stride, 8, k_codes, v_codes,
-                            LowBit{k_scale, v_scale, nullptr, nullptr}, block_table, max_blocks_per_seq, num_blocks, cu_q_lens, seq_lens, num_seqs,
-                            total_tokens, workspace, workspace_bytes, stream);
+                            LowBit{k_scale, v_scale, nullptr, nullptr}, block_table, max_blocks_per_seq, num_blocks,
+                            cu_q_lens, seq_lens, num_seqs, total_tokens, workspace, workspace_bytes, stream);
 }
 
 pa_status paged_rope_append_fp4(pa_shape shape, float rope_theta, const int32_t *positions, int32_t axes,

@@ -115,7 +115,9 @@ const int32_t *ints(const at::Tensor *t) { return static_cast<const int32_t *>(t
 // `out` as given (None: a new tensor of that shape); false when it is not a plain one of it.
 bool output(PyObject *o, at::IntArrayRef shape, int dev, at::Tensor *out) {
     if (o == Py_None) {
-        *out = at::Tensor(at::detail::empty_cuda(shape, at::kBFloat16, c10::Device(c10::kCUDA, (c10::DeviceIndex)dev), std::nullopt));
+        // (what at::empty comes to here, without the dispatcher: 0.5 us less)
+        const c10::Device on(c10::kCUDA, (c10::DeviceIndex)dev);
+        *out = at::Tensor(at::detail::empty_cuda(shape, at::kBFloat16, on, std::nullopt));
         return true;
     }
     const at::Tensor *t = tensor(o);

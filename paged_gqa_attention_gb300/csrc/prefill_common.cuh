@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) prefill_plan_kernel(const Pre
     }
     __syncthreads();
     for (int idx = tid; idx < total; idx += kPlanThreads) {
-        const int rank = atomicAdd(&hist[idx == tid ? key0 : min(plan_key<kAppend, kWindow, kPos>(a, idx, qblocks), nk - 1)], 1);
+        const int key = idx == tid ? key0 : min(plan_key<kAppend, kWindow, kPos>(a, idx, qblocks), nk - 1);
+        const int rank = atomicAdd(&hist[key], 1);
         a.order[rank] = idx;
     }
     // Complete only after the kernel before this one on the stream (kv_append lets its

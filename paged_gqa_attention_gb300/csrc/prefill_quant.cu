@@ -178,15 +178,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 
 // Arrive on the barrier at this offset in both CTAs once every tcgen05 operation this thread issued has completed.
 __device__ __forceinline__ void umma_commit_both(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-                 "h"((uint16_t)3)
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 ::"r"(bar), "h"((uint16_t)3)
                  : "memory");
 }
 
 // Shared memory of this CTA -> of the peer, completing there.
 __device__ __forceinline__ void copy_to_peer(uint32_t cluster_dst, uint32_t src, uint32_t bytes, uint32_t cluster_bar) {
-    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(cluster_dst),
-                 "r"(src), "r"(bytes), "r"(cluster_bar)
+    asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(cluster_dst), "r"(src), "r"(bytes), "r"(cluster_bar)
                  : "memory");
 }
 
@@ -252,7 +252,8 @@ __device__ __forceinline__ void load_codes(const PrefillArgs &a, const Unit &t, 
         int off = p % kBlock;
         const size_t row = ((size_t)blk * kHkv + t.g) * kBlock + off;   // (off and run are multiples of 16)
         if constexpr (kBits == 8) {
-            bulk_load(smem_u32(ring.scale[st] + r), static_cast<const float *>(is_k ? a.k_scale : a.v_scale) + row, run * 4, bar);
+            const void *scale = is_k ? a.k_scale : a.v_scale;
+            bulk_load(smem_u32(ring.scale[st] + r), static_cast<const float *>(scale) + row, run * 4, bar);
             if (is_k) bulk_load(smem_u32(ring.v_scales(st) + r), static_cast<const float *>(a.v_scale) + row, run * 4, bar);
         } else {
             bulk_load(smem_u32(ring.scale[st] + r * kFp4Groups),
@@ -376,7 +377,8 @@ __device__ __forceinline__ float exp2_int(int n) { return __uint_as_float((uint3
 
 // What the tile whose K is in slot st is scaled by (a warp's work); sigma: its exponent after the tile before, kNone at first.
 template <int kBits, bool kPair>
-__device__ __forceinline__ TileParams scale_tile(CodeRing<kBits, kPair> &ring, int st, const DeadRows &dead, int &sigma, int lane) {
+__device__ __forceinline__ TileParams scale_tile(CodeRing<kBits, kPair> &ring, int st, const DeadRows &dead, int &sigma,
+                                                 int lane) {
     // V' stays below 65504: codes reach 448 (2688 with their group's scale), so the tile's largest scale
     // may be this many powers of two above sigma
     constexpr int kHeadroom = kBits == 8 ? 7 : 4;
@@ -409,7 +411,8 @@ __device__ __forceinline__ TileParams scale_tile(CodeRing<kBits, kPair> &ring, i
 }
 
 // This warp's share of rows row0 .. end - 1 of a code tile into an f16 tile: rounds of 8 rows, `first` and every 6th (a
-// pair: 5th) from there on, the next round's read ahead.  Dead rows are zeros: their codes and scales may be anything, and 0 * NaN is not 0.
+// pair: 5th) from there on, the next round's read ahead.  Dead rows are zeros: their codes and scales may be anything,
+// and 0 * NaN is not 0.
 // Lanes 8q .. 8q + 3 have row q of the 8, lanes 8q + 4 .. 8q + 7 row q ^ 5, so that with the swizzles below neither
 // a load (whose rows must differ in bit 2) nor a store (in bit 0) meets a bank twice, and no lane has to exchange its
 // pieces first.
@@ -418,8 +421,8 @@ __device__ __forceinline__ TileParams scale_tile(CodeRing<kBits, kPair> &ring, i
 // warp-cycles an instruction).  A round takes a warp some 265 clk on its own: 48 half-rate instructions and their
 // latencies.
 template <int kBits, bool kPair>
-__device__ __forceinline__ void convert_tile(const CodeRing<kBits, kPair> &ring, int st, uint32_t dst, float unit, bool any_dead,
-                                             const DeadRows &dead, int row0, int end, int first, int lane) {
+__device__ __forceinline__ void convert_tile(const CodeRing<kBits, kPair> &ring, int st, uint32_t dst, float unit,
+                                             bool any_dead, const DeadRows &dead, int row0, int end, int first, int lane) {
     constexpr int kRow = CodeRing<kBits, kPair>::kRow, kStep = 8 * kConvertWarps<kPair>;
     const int c = lane & 3;
     int row = row0 + 8 * first + ((lane >> 3) ^ ((lane & 4) ? 5 : 0));

@@ -198,7 +198,16 @@ constexpr SplitCost kSplitCost = {0.42, 1.0, 0.0049, 1.4, 1.9, 0.07, 1.5, 5};   
 constexpr SplitCost kSplitCostFp4 = {1.1, 1.57, 0.005, 2.3, 1.8, 0.22, 1.7, 2};        // 256 tokens in 4 bits
 constexpr SplitCost kSplitCostFp8 = {0.78, 1.8, 0.0053, 1.7, 2.3, 0.15, 1.5, 1};       // 128 tokens in 8 bits
 
-int auto_window_split(int batch, long long tiles, int num_sms, const SplitCost &c) {
+// Whether `pairs` (sequence, KV head) pairs in `splits` merge as clusters: up to 8 splits, and with `room` known only
+// clusters that are all there at once, an SM for each CTA where there are SMs enough.  The GPU packs the others two CTAs
+// an SM while SMs are idle: in 4 bits, 2 sequences and 20000 tokens in 8 25.6 us as clusters, 17.5 through the
+// workspace, 6 and 1500 in 6 12.5 and 9.2; but 5 and 6000 in 6, two CTAs an SM in any case, 13.4 and 14.9.
+bool merges_as_cluster(long long pairs, long long splits, int num_sms, const ClusterRoom *room) {
+    if (splits < 2 || splits > 8) return false;
+    return !room || pairs <= (pairs * splits <= num_sms ? room->lone : room->fit)[splits];
+}
+
+int auto_window_split(int batch, long long tiles, int num_sms, const SplitCost &c, const ClusterRoom *room = nullptr) {
     const long long pairs = (long long)batch * kHkv, places = 2LL * num_sms;
     const double stream = c.stream_us * (double)pairs * (double)tiles;
     const bool waves = pairs > places;
@@ -219,8 +228,8 @@ int auto_window_split(int batch, long long tiles, int num_sms, const SplitCost &
         } else {
             us = walk > stream ? walk + 0.25 * stream : stream + 0.25 * walk;
         }
-        if (splits > 1)
-            us += !waves && splits <= 8 ? c.cluster_us : c.merge_us + c.merge_each_us * (double)splits;
+        const bool cluster = !waves && merges_as_cluster(pairs, splits, num_sms, room);
+        if (splits > 1) us += cluster ? c.cluster_us : c.merge_us + c.merge_each_us * (double)splits;
         if (n == 1 || us < best_us) {
             best = per;
             best_us = us;
@@ -958,8 +967,10 @@ pa_status paged_attn_decode_fp4(pa_shape shape, void *out, float *lse, const voi
     if (sms <= 0) return PA_ERR_CUDA;
     if (!get_encoder()) return PA_ERR_CUDA;
     const long long tiles = window_tiles_bound(window, sinks, max_blocks_per_seq, kDecodeFp4TileTokens);
+    ClusterRoom room;
+    if (decode_fp4_clusters(room) != cudaSuccess) return PA_ERR_CUDA;
     const long long per_split = split_tokens ? split_tokens / kDecodeFp4TileTokens
-                                             : auto_window_split(batch, tiles, sms, kSplitCostFp4);
+                                             : auto_window_split(batch, tiles, sms, kSplitCostFp4, &room);
     const long long nsplit = (tiles + per_split - 1) / per_split;
     if (nsplit > 65535) return PA_ERR_INVALID_ARG;
     const size_t entries = (size_t)batch * kHkv * (size_t)nsplit;
@@ -992,7 +1003,7 @@ pa_status paged_attn_decode_fp4(pa_shape shape, void *out, float *lse, const voi
     a.err = reinterpret_cast<uint32_t *>(ws);
     a.window = window;
     a.sinks = sinks;
-    a.cluster_merge = nsplit > 1 && nsplit <= 8 && (long long)batch * kHkv * nsplit <= 2LL * sms ? 1 : 0;
+    a.cluster_merge = merges_as_cluster((long long)batch * kHkv, nsplit, sms, &room) ? 1 : 0;
     return launch_decode_fp4(a, k_map, v_map, k16_map, v16_map, static_cast<cudaStream_t>(stream)) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;

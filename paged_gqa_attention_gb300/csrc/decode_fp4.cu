@@ -588,7 +588,47 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
     if (a.lse && (c & 31) == 0) a.lse[(size_t)b * kHq + qh] = (GM + __log2f(GL)) * kLn2;
 }
 
+// As much shared memory as lets one CTA alone onto an SM
+constexpr size_t kLoneBytes = 131072;
+static_assert(kLoneBytes >= kSmemBytes && 2 * (kLoneBytes + 1024) > 233472, "one CTA per SM");
+
 }  // namespace
+
+cudaError_t decode_fp4_clusters(ClusterRoom &room) {
+    static std::atomic<int> known[64][2][9];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    for (int c = 2; c <= 8; ++c) {
+        for (int two = 0; two < 2; ++two) {
+            int &out = two ? room.fit[c] : room.lone[c];
+            out = known[dev][two][c].load();
+            if (out != 0) continue;
+            e = cudaFuncSetAttribute(decode_fp4_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLoneBytes);
+            if (e != cudaSuccess) return e;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1;
+            attr[0].val.clusterDim.y = (unsigned)c;
+            attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(1, (unsigned)c);
+            cfg.blockDim = dim3(kThreads);
+            cfg.dynamicSmemBytes = two ? kSmemBytes : kLoneBytes;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, decode_fp4_kernel<true>, &cfg) != cudaSuccess) {
+                cudaGetLastError();   // none this time; asked again next time
+                continue;
+            }
+            out = n > 0 ? n : -1;
+            known[dev][two][c].store(out);
+        }
+    }
+    return cudaSuccess;
+}
 
 cudaError_t launch_decode_fp4(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                               const CUtensorMap &k16_map, const CUtensorMap &v16_map, cudaStream_t stream) {
@@ -598,10 +638,11 @@ cudaError_t launch_decode_fp4(const DecodeArgs &a, const CUtensorMap &k_map, con
     if (e != cudaSuccess) return e;
     static std::atomic<bool> configured[64] = {};
     if (dev < 0 || dev >= 64 || !configured[dev].load()) {
-        for (const auto kernel : {decode_fp4_kernel<false>, decode_fp4_kernel<true>}) {
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-            if (e != cudaSuccess) return e;
-        }
+        e = cudaFuncSetAttribute(decode_fp4_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+        if (e != cudaSuccess) return e;
+        // (as decode_fp4_clusters sets it)
+        e = cudaFuncSetAttribute(decode_fp4_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLoneBytes);
+        if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(true);
     }
     cudaLaunchConfig_t cfg = {};

@@ -279,6 +279,12 @@ cudaError_t launch_wait_selftest(uint32_t *err, uint64_t limit_ns, cudaStream_t 
 void *static_scratch_address(cudaError_t *status);
 
 // Decode over the 4-bit cache, window (or all of the context) and sinks as above.
+// How many clusters of c CTAs, c = 2 .. 8, fit on the current device at once: with an SM for each CTA, and with two CTAs
+// an SM (looked up once per device; a lookup that failed leaves 0 and is made again next time).
+struct ClusterRoom {
+    int lone[9] = {}, fit[9] = {};
+};
+cudaError_t decode_fp4_clusters(ClusterRoom &room);
 cudaError_t launch_decode_fp4(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                               const CUtensorMap &k16_map, const CUtensorMap &v16_map, cudaStream_t stream);
 

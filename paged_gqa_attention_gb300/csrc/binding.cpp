@@ -320,7 +320,7 @@ PyObject *decode_fp4(PyObject *, PyObject *const *o, Py_ssize_t n) {
 PyObject *prefill_low(PyObject *, PyObject *const *o, Py_ssize_t n) {
     if (n != 17) Py_RETURN_NONE;
     return guarded([&]() -> PyObject * {
-        const int bits = o[5] == Py_None ? 8 : 4;
+        const int bits = o[5] == Py_None && o[6] == Py_None ? 8 : 4;
         Attention a;
         int32_t max_q_len, window, sinks;
         double scale;
@@ -374,7 +374,7 @@ PyObject *append_fp4(PyObject *, PyObject *const *o, Py_ssize_t n) {
 PyObject *kv_read(PyObject *, PyObject *const *o, Py_ssize_t n) {
     if (n != 13) Py_RETURN_NONE;
     return guarded([&]() -> PyObject * {
-        const int bits = o[4] == Py_None ? 8 : 4;
+        const int bits = o[4] == Py_None && o[5] == Py_None ? 8 : 4;
         Cache cache;
         int32_t rows;
         if (!cache.take(o, bits) || !as_int32(o[9], &rows) || rows < 0) Py_RETURN_NONE;

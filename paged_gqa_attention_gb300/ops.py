@@ -1030,7 +1030,7 @@ def paged_kv_read_fp8(k_codes, v_codes, k_scale, v_scale, block_table, cu_rows, 
 def paged_kv_read_fp4(k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, block_table, cu_rows, first, total_rows: int,
                       workspace, *, k_out=None, v_out=None, stream=None):
     """paged_kv_read_fp8 of the 4-bit cache."""
-    if stream is None:
+    if stream is None and k_exp is not None:      # (the binding tells an 8-bit cache by that)
         got = (_binding or _usual()).kv_read(k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, block_table, cu_rows, first,
                                              total_rows, workspace, k_out, v_out)
         if got is not None:
@@ -1110,7 +1110,7 @@ def paged_attn_prefill_fp4(q, k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, 
                            max_q_len: int, workspace, *, window: int = FULL_WINDOW, sinks: int = 0,
                            scale: float = DEFAULT_SCALE, out=None, lse=None, stream=None) -> torch.Tensor:
     """paged_attn_prefill_fp8 over the 4-bit cache."""
-    if stream is None:
+    if stream is None and k_exp is not None:      # (the binding tells an 8-bit cache by that)
         got = (_binding or _usual()).prefill_low(q, k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, block_table, cu_q_lens,
                                                  seq_lens, max_q_len, workspace, window, sinks, scale, out, lse)
         if got is not None:

@@ -131,7 +131,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         tmp = BINDING_PATH + f".tmp{os.getpid()}"
         torch_lib = os.path.join(os.path.dirname(torch.__file__), "lib")
         _run([gxx, "-shared", "-o", tmp, bound.result(), "-L", os.path.dirname(LIB_PATH),
-              "-l:" + os.path.basename(LIB_PATH), "-L", torch_lib, "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+              "-l:" + os.path.basename(LIB_PATH), "-L", torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
               "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + torch_lib], "linking _binding.so")
         if _recorded_abi() not in (None, binding_abi()):
             os.remove(BINDING_ABI_PATH)      # (it names the old one)

@@ -14,7 +14,6 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
-#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -115,9 +114,8 @@ const int32_t *ints(const at::Tensor *t) { return static_cast<const int32_t *>(t
 // `out` as given (None: a new tensor of that shape); false when it is not a plain one of it.
 bool output(PyObject *o, at::IntArrayRef shape, int dev, at::Tensor *out) {
     if (o == Py_None) {
-        // (what at::empty comes to here, without the dispatcher: 0.5 us less)
-        const c10::Device on(c10::kCUDA, (c10::DeviceIndex)dev);
-        *out = at::Tensor(at::detail::empty_cuda(shape, at::kBFloat16, on, std::nullopt));
+        // (through the dispatcher: deterministic fills of new memory and dispatch modes are the caller's to have)
+        *out = at::empty(shape, at::TensorOptions().dtype(at::kBFloat16).device(at::kCUDA, dev));
         return true;
     }
     const at::Tensor *t = tensor(o);

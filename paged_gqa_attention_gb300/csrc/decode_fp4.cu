@@ -24,11 +24,11 @@
 //     the odd ones.  No operand is permuted and no column idle; the accumulator of piece c holds dims
 //     32c + 4r (rows r < 8), 32c + 4(r - 8) + 2, and one more in columns 4..7;
 //   * the row's power of two enters S in fp32, and for V through P: each warp accumulates
-//     P * 2^(e - sigma) in f16, sigma the largest exponent it has seen, and rescales its accumulator
-//     when sigma grows, as the online softmax does for its maximum.  A lane looks a token up and hands on
-//     what the others need of it;
+//     P * 2^(e - sigma) in f16, sigma the largest exponent it has seen (of rows that are not zero), and rescales its
+//     accumulator when sigma grows, as the online softmax does for its maximum.  A lane looks a token up and hands
+//     on what the others need of it;
 //   * tokens that are not attended to get scale 0 in V (every code is finite) and score -infinity.
-// Measured: 64 sequences of 8192 to 16384 tokens 189 us (933 MB: 4.9 TB/s; with a multiply and a permute for
+// Measured: 64 sequences of 8192 to 16384 tokens 191 us (933 MB: 4.9 TB/s; with a multiply and a permute for
 // every pair 274), 64 of 16384 227 us (5.3 TB/s), 32 of 128 to 4096 28.6, one of 9001 10.0, one tile 5.0.
 #include <cuda_fp16.h>
 
@@ -311,7 +311,7 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
             const uint32_t seen = __ballot_sync(0xffffffffu, ok);
             const float kf = fp4_unit(sm.exps[st][0][w * kWarpTokens + lane]) * a.scale_log2;
             const uint32_t ev = sm.exps[st][1][w * kWarpTokens + lane];
-            const int ve = !ok || ev == 0 ? kNoSigma : (int)ev - 127;   // 128: NaN
+            int ve = !ok || ev == 0 ? kNoSigma : (int)ev - 127;   // 128: NaN
 
             // S^T[2 x 16 tokens x 8 columns] = K . Q^T, 64 dims per ldmatrix
             float x[2][4];
@@ -382,6 +382,12 @@ decode_fp4_kernel(const __grid_constant__ CUtensorMap k_map, const __grid_consta
                 m1 = mn1;
                 l0 *= alpha0;
                 l1 *= alpha1;
+                // a zero row (every scale 0) has the exponent 2^0, far above rows of ordinary size: it sets no unit
+                // (and needs none; rows at or below sigma do not matter)
+                if (ve > sigma && ve < 128) {
+                    const uint2 y = *reinterpret_cast<const uint2 *>(vsc + lane * kFp4Groups);
+                    if ((y.x | y.y) == 0u) ve = kNoSigma;
+                }
                 const int top = __reduce_max_sync(0xffffffffu, ve < 128 ? ve : kNoSigma);
                 const float grow = top > sigma ? pow2_or_0(sigma - top) : 1.f;
                 sigma = max(sigma, top);

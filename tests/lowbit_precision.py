@@ -55,10 +55,11 @@ class Rows(LowCache):
         """(out, lse, tolerance of out, tolerance of lse) in 64 bits.
 
         out = sum w v / sum w.  What the kernels round, u = 2^-11 being half a step of f16:
-          weights     to f16 for the products only: u of sum p |v|.  Those below 2^-14 (of weights whose largest is at least 1)
-                      by 2^-25 each: n 2^-25 of the largest |v| seen, over n keys.  In the decode a weight carries its V row's
-                      power of two over the largest of the rows seen: 2^-25 of 2688 2^e, where the largest row quantised
-                      is above 1344 (1 - 1/16) 2^e: 2.2 times as much;
+          weights     to f16 for the products only: u of sum p |v|.  Those below 2^-14 (the largest is 1 at least, so p is no
+                      larger than the weight) by 2^-25, and by no more than themselves: min(2^-25, p) |v| each.  In the decode
+                      a weight carries its V row's power of two over the largest of the rows seen: 2^-25 of 2688 2^e, where
+                      the largest row quantised is above 1344 (1 - 1/16) 2^e: 2^-25 of 2.2 times the largest |v|, and
+                      p |v| at most;
           scores      fp32 sums of 128 products, 2^-24 or (truncated) 2^-23 of sum |q k| scale for each: 2^-16 a, a the
                       largest such sum of the keys seen; the exponential, its argument and the softmax scale add less than
                       2^-16 (1 + a).  A score that is off by ds moves p by as much, relatively, in numerator and
@@ -87,7 +88,12 @@ class Rows(LowCache):
             out, abs_v = torch.einsum("htn,nhd->thd", w, v), torch.einsum("htn,nhd->thd", w, v.abs())
             a = torch.einsum("thd,nhd->htn", q.abs(), k.abs()) * SCALE
             a = torch.where(seen, a, 0.0).amax(-1).T                                       # [t, h]
-            v_max = torch.where(seen[..., None], v.abs().amax(-1), 0.0).amax(1)            # [t, h]
+            size = v.abs().amax(-1).T[:, None]                                             # [h, 1, n]
+            if prefill:
+                lost = torch.minimum(w, torch.tensor(2.0 ** -25, dtype=w.dtype)) * size
+            else:
+                lost = torch.minimum(w * size, 2.2 * 2.0 ** -25 * torch.where(seen, size, 0.0).amax(-1, keepdim=True))
+            lost = torch.where(seen, lost, 0.0).sum(-1).T                                  # [t, h]
             ds = 2.0 ** -16 * 2 * (1 + a)
             v_unit = torch.zeros(m, 32, dtype=torch.float64)
             if prefill:
@@ -101,7 +107,7 @@ class Rows(LowCache):
                 ds = ds + (u * a if self.bits == 8 else 0) + part * k_unit * q.abs().sum(-1) * SCALE
             ds = ds[..., None]
             tol = u * abs_v * (2 if prefill and self.bits == 8 else 1) * 1.01 + ds * (1 + 2 * ds) * (abs_v + out.abs())
-            tol = tol + (n * 2.0 ** -25 * v_max * (1 if prefill else 2.2) + part * v_unit)[..., None] + n * 2.0 ** -23 * abs_v
+            tol = tol + (lost + part * v_unit)[..., None] + n * 2.0 ** -23 * abs_v
             outs.append(out)
             lses.append(lse.T)
             tols.append(tol * (1 + 2.0 ** -8) + 2.0 ** -8 * out.abs())

@@ -24,7 +24,7 @@
 //     token quantises the token's K and V rows of its KV head (kv_append_fp8's rule),
 //     writes codes and scales to the cache and patches them into the landed stage;
 //   * the V scale enters through P: each warp keeps a running reference sigma (the
-//     largest V scale it has seen), accumulates P * (s_v / sigma) in f16 and rescales
+//     largest V scale it has seen on a row that is not zero), accumulates P * (s_v / sigma) in f16 and rescales
 //     its accumulator when sigma grows, as the online softmax does for its maximum; the
 //     warp merge multiplies by sigma back.
 // The sliding-window form (kWindow) walks the list of stages that hold a visible token, as in
@@ -392,8 +392,8 @@ __device__ __forceinline__ void decode_fp8_body(const CUtensorMap &k_map, const 
 
             // V scales of this warp's tokens (0 past the context end: scale slots there
             // may hold anything) and their maximum
-            const float sv_lo = v_lo_ok ? vsc[gq] : 0.f;
-            const float sv_hi = v_hi_ok ? vsc[gq + 8] : 0.f;
+            float sv_lo = v_lo_ok ? vsc[gq] : 0.f;
+            float sv_hi = v_hi_ok ? vsc[gq + 8] : 0.f;
             // the accumulator's reference V scale grows with the largest scale seen; its
             // reciprocal is recomputed only then (an approximate reciprocal: the factor it
             // introduces is undone exactly by the same values in grow and the final sigma)
@@ -402,6 +402,24 @@ __device__ __forceinline__ void decode_fp8_body(const CUtensorMap &k_map, const 
             // (one vote finds the stages that raise it; only they reduce over the warp)
             float grow = 1.f;
             if (__any_sync(0xffffffffu, fmaxf(fmaxf(sv_lo, sv_hi), 0x1p-100f) > sigma)) {
+                // A zero row has the scale 1, far above that of rows of ordinary size: it sets no reference (and needs
+                // none).  The four lanes of a token look at 32 of its codes each.
+                if (__any_sync(0xffffffffu, sv_lo == 1.f || sv_hi == 1.f)) {
+                    const uint8_t *codes = sm.codes[st][1];
+                    uint32_t any[2] = {0u, 0u};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const uint4 y = *reinterpret_cast<const uint4 *>(codes + sw128(w * 16 + 8 * h + gq, 2 * tq + c));
+                            any[h] |= y.x | y.y | y.z | y.w;
+                        }
+                        any[h] |= __shfl_xor_sync(0xffffffffu, any[h], 1);
+                        any[h] |= __shfl_xor_sync(0xffffffffu, any[h], 2);
+                    }
+                    if (sv_lo == 1.f && (any[0] & 0x7f7f7f7fu) == 0u) sv_lo = 0.f;
+                    if (sv_hi == 1.f && (any[1] & 0x7f7f7f7fu) == 0u) sv_hi = 0.f;
+                }
                 float svm = fmaxf(sv_lo, sv_hi);
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) svm = fmaxf(svm, __shfl_xor_sync(0xffffffffu, svm, o));

@@ -15,12 +15,13 @@ def _lib():
     lib_ready()
 
 
+@pytest.mark.parametrize("bits", [8, 4])
 @pytest.mark.parametrize("power", [0, -10])
 @pytest.mark.parametrize("split", [False, True])
-def test_decode_zero_rows_set_no_unit(power, split):
-    """A zero V row has the exponent 2^0, far above that of rows of ordinary size: they must keep their weights' bits.
-    Every head pair has one head that looks at a single key and one that looks at many."""
-    c = Rows([1500, 700, 33] if split else [700] * 40, [1] * (3 if split else 40), FULL, 0, 61)
+def test_decode_zero_rows_set_no_unit(bits, power, split):
+    """A zero V row has the scale 1 (the exponent 2^0 in 4 bits), far above that of rows of ordinary size: they must keep
+    their weights' bits.  Every head pair has one head that looks at a single key and one that looks at many."""
+    c = Rows([1500, 700, 33] if split else [700] * 40, [1] * (3 if split else 40), FULL, 0, 61, bits)
     c.v_host *= 2.0 ** power
     c.v_host[:, 3::17] *= 0
     c.v_host[:, 100:140] *= 0                    # a whole warp's share
@@ -29,8 +30,9 @@ def test_decode_zero_rows_set_no_unit(power, split):
     c.compare(False, f"2^{power}")
 
 
-def test_decode_of_zero_rows_alone():
-    c = Rows([600, 40], [1, 1], FULL, 0, 63)
+@pytest.mark.parametrize("bits", [8, 4])
+def test_decode_of_zero_rows_alone(bits):
+    c = Rows([600, 40], [1, 1], FULL, 0, 63, bits)
     c.v_host *= 0
     c.upload()
     c.qd = c.q.cuda()

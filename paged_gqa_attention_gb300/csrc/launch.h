@@ -86,7 +86,7 @@ struct DecodeArgs {
     float *part_ml;        // [batch * 8 * nsplit][4][2]
     uint32_t *err;
     // Sliding window (window > 0): a sequence of n tokens attends to its first `sinks` and its
-    // last `window` ones.  Splits then cut the list of 64-token tiles (128 in the 8-bit cache)
+    // last `window` ones.  Splits then cut the list of 64-token tiles (128 in the 8-bit cache, 256 in the 4-bit one)
     // that hold a visible token, split_tokens / tile of them a CTA.
     int32_t window;
     int32_t sinks;
@@ -260,13 +260,13 @@ cudaError_t launch_prefill_window(PrefillArgs a, long long tiles, const CUtensor
                                   const CUtensorMap &v_map, const CUtensorMap &k16_map, const CUtensorMap &v16_map,
                                   int num_sms, cudaStream_t stream);
 
-// The prefill with the append of the new tokens fused in (a.k_new set): kn_map / vn_map are
-// 3-D maps (dim, head, token) over k_new / v_new with box {64, 1, 128}.
 // The same over the 8-bit cache, or the 4-bit one when a.k_exp is set: maps over the code pools.
 cudaError_t launch_prefill_quant(PrefillArgs a, long long tiles, const CUtensorMap &q_map, const CUtensorMap &k_map,
                                  const CUtensorMap &v_map, const CUtensorMap &k16_map, const CUtensorMap &v16_map,
                                  int num_sms, cudaStream_t stream);
 
+// The prefill with the append of the new tokens fused in (a.k_new set): kn_map / vn_map are
+// 3-D maps (dim, head, token) over k_new / v_new with box {64, 1, 128}.
 cudaError_t launch_prefill_append(const PrefillArgs &a, const CUtensorMap &q_map, const CUtensorMap &k_map,
                                   const CUtensorMap &v_map, const CUtensorMap &kn_map, const CUtensorMap &vn_map,
                                   int num_sms, cudaStream_t stream);
@@ -278,13 +278,13 @@ cudaError_t launch_wait_selftest(uint32_t *err, uint64_t limit_ns, cudaStream_t 
 // failure.
 void *static_scratch_address(cudaError_t *status);
 
-// Decode over the 4-bit cache, window (or all of the context) and sinks as above.
 // How many clusters of c CTAs, c = 2 .. 8, fit on the current device at once: with an SM for each CTA, and with two CTAs
 // an SM (looked up once per device; a lookup that failed leaves 0 and is made again next time).
 struct ClusterRoom {
     int lone[9] = {}, fit[9] = {};
 };
 cudaError_t decode_fp4_clusters(ClusterRoom &room);
+// Decode over the 4-bit cache (a.k_exp and its scales set), window (or all of the context) and sinks as above.
 cudaError_t launch_decode_fp4(const DecodeArgs &a, const CUtensorMap &k_map, const CUtensorMap &v_map,
                               const CUtensorMap &k16_map, const CUtensorMap &v16_map, cudaStream_t stream);
 

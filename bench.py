@@ -55,9 +55,9 @@ TRAFFIC = {
                "sources": ("decode.cu", "cluster.cuh", "common.cuh", "window.cuh"),
                "sha": "4ca59ac25fa8f5db", "workload": "batched_decode"},
     # one ncu capture of the fused 8-bit decode step (batch 32, 126 MB of 8-bit K/V)
-    "decode_fp8": {"bytes_per_launch": 131144960 + 3577600,
+    "decode_fp8": {"bytes_per_launch": 131113216 + 3390208,
                    "sources": ("decode_fp8.cu", "cluster.cuh", "common.cuh", "window.cuh"),
-                   "sha": "790e2d839b28aa14", "workload": "batched_decode_fp8"},
+                   "sha": "d2586ce29df09f3f", "workload": "batched_decode_fp8"},
     # one ncu capture of the causal prefill of 4096 tokens with the prompt's append fused in
     "prefill": {"bytes_per_launch": 50456064 + 13347584,
                 "sources": ("prefill.cu", "prefill_common.cuh", "cluster.cuh", "common.cuh", "window.cuh"),

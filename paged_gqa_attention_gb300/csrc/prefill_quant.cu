@@ -16,7 +16,7 @@
 //                             when a tile's V' could leave f16; O is then rescaled, as it is for the
 //                             running maximum, and the epilogue multiplies by sigma
 // with one rounding to f16 (8 bits: the scale is split into a sum of two f16, so that code * scale is rounded
-// once, by 2^-11 of the value at most; 4 bits: exact).  Values 2^-14 of the largest and less lose bits one by one.
+// once, by 2^-11 of the value at most; 4 bits: exact).  Quotients under 2^-14 lose bits one by one.
 // Q is converted to f16 in place (|q| < 65504, as for the decode over these caches), P is f16.
 //
 // What bounds it is not the products (4 x 128 x 128 x 256 operations a tile, 2048 clk at the tensor cores' rate)
@@ -28,8 +28,9 @@
 // Measured, 8192 new tokens after 8192 in 8 bits: 2012 us with the conversion unrolled for K and V apart, 1570
 // in one rolled loop, 1555 with six converters, 1455 in pairs whose converters made the copies (400 clk a
 // visit), 1239 with the copies in the producer, 1224 with the loads of V and the copies in a warp of their own and the
-// tiles' exponents in the producer (1.35 PFLOP/s; 4 chunks of up to 1024 in 4 bits with a window of 2048, which
-// the producer's 2400 clk of issuing loads a tile had held at 132 us: 120).  One CTA alone walking its list, 1555
+// tiles' exponents in the producer (1.35 PFLOP/s; the vote on small scales has since added 1 %; 4 chunks of up to 1024
+// in 4 bits with a window of 2048, which the producer's 2400 clk of issuing loads a tile had held at 132 us: 120).  One
+// CTA alone walking its list, 1555
 // and 129, is left where a sequence has 64 positions at most (there is nobody to share with) and where few
 // units share the GPU, whose keys are split instead.  Products over the pair (tcgen05 with two CTAs' operands) halve
 // the same conversion without copies, but every step then waits for the peer: 1382.

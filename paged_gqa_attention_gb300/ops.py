@@ -1047,7 +1047,8 @@ def paged_attn_decode_fp4(q, k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, b
                           split_tokens: int = 0, stream=None) -> torch.Tensor:
     """One query token per sequence over the 4-bit cache: the whole context, or its first `sinks` and last
     `window` tokens; q [B, 32, 128] -> out [B, 32, 128] (bf16).  A row with seq_lens 0 gives zeros.
-    split_tokens: visible tokens per CTA (a multiple of 256), 0 = the library's choice."""
+    split_tokens: visible tokens per CTA (a multiple of 256), 0 = the library's choice (by the table's width
+    and the window, not by seq_lens: behind a table much wider than the contexts, give one)."""
     if stream is None:
         got = (_binding or _usual()).decode_fp4(q, k_codes, v_codes, k_scale, v_scale, k_exp, v_exp, block_table, seq_lens,
                                                 workspace, window, sinks, scale, split_tokens, out, lse)
